@@ -22,12 +22,16 @@ OPERANDS_BF16 = 1
 FLAG_TEST_STALL = 0x1
 FLAG_TEST_STALL_MMA = 0x4
 FLAG_E2M1_V = 0x2
+BF16 = 0
+FP16 = 1
+FP32 = 2
 PATH_SPECIALISED = 0
 PATH_GENERAL = 1
 
 # Every symbol include/kvq.h declares.
 EXPORTS = ("kvq_status_string", "kvq_version", "kvq_cache_bytes", "kvq_pack", "kvq_append", "kvq_dequant",
-           "kvq_decode_workspace_size", "kvq_decode_path", "kvq_decode_attn", "kvq_decode_attn_static", "kvq_merge")
+           "kvq_decode_workspace_size", "kvq_decode_path", "kvq_decode_attn", "kvq_decode_attn_static", "kvq_merge",
+           "kvq_prompt_attn", "kvq_append_chunk", "kvq_chunk_workspace_size", "kvq_chunk_attn")
 
 
 class CacheDesc(ctypes.Structure):
@@ -40,6 +44,22 @@ class AttnDesc(ctypes.Structure):
     _fields_ = [("cache", CacheDesc), ("batch", ctypes.c_int32), ("num_q_heads", ctypes.c_int32),
                 ("max_blocks", ctypes.c_int32), ("operand_mode", ctypes.c_int32), ("sm_scale", ctypes.c_float),
                 ("num_ctas", ctypes.c_int32), ("flags", ctypes.c_uint32)]
+
+
+class Rows(ctypes.Structure):
+    _fields_ = [("data", ctypes.c_void_p), ("stride_token", ctypes.c_int64), ("stride_head", ctypes.c_int64)]
+
+
+class PromptDesc(ctypes.Structure):
+    _fields_ = [("dtype", ctypes.c_int32), ("head_dim", ctypes.c_int32), ("num_q_heads", ctypes.c_int32),
+                ("num_kv_heads", ctypes.c_int32), ("batch", ctypes.c_int32), ("total_tokens", ctypes.c_int32),
+                ("causal", ctypes.c_int32), ("sm_scale", ctypes.c_float), ("flags", ctypes.c_uint32)]
+
+
+class ChunkDesc(ctypes.Structure):
+    _fields_ = [("cache", CacheDesc), ("dtype", ctypes.c_int32), ("batch", ctypes.c_int32),
+                ("total_tokens", ctypes.c_int32), ("num_q_heads", ctypes.c_int32), ("max_blocks", ctypes.c_int32),
+                ("causal", ctypes.c_int32), ("sm_scale", ctypes.c_float), ("flags", ctypes.c_uint32)]
 
 
 class KvqError(RuntimeError):
@@ -88,6 +108,15 @@ def load(path: str | None = None) -> ctypes.CDLL:
     lib.kvq_decode_attn_static.argtypes = [ctypes.POINTER(AttnDesc), P, P, P, P, P, P, P, P, P, P, P, P, P]
     lib.kvq_merge.restype = I32
     lib.kvq_merge.argtypes = [P, P, I32, I32, I32, P, P, P]
+    R = ctypes.POINTER(Rows)
+    lib.kvq_prompt_attn.restype = I32
+    lib.kvq_prompt_attn.argtypes = [ctypes.POINTER(PromptDesc), R, R, R, P, P, P, P, P]
+    lib.kvq_append_chunk.restype = I32
+    lib.kvq_append_chunk.argtypes = [ctypes.POINTER(CacheDesc), I32, R, R, I32, I32, P, P, P, I32] + [P] * 12
+    lib.kvq_chunk_workspace_size.restype = I32
+    lib.kvq_chunk_workspace_size.argtypes = [ctypes.POINTER(ChunkDesc), ctypes.POINTER(SZ)]
+    lib.kvq_chunk_attn.restype = I32
+    lib.kvq_chunk_attn.argtypes = [ctypes.POINTER(ChunkDesc), R] + [P] * 12 + [SZ, P, P]
     _ = U32
     if path is None:
         _LIB = lib

@@ -16,11 +16,10 @@ namespace {
 
 constexpr int kMaxBatchDecode = 1024;
 
-bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
-
-int group_of(const kvq_cache_desc* c) { return c->group_size == 0 ? 128 : c->group_size; }
 int block_bytes(const kvq_cache_desc* c) { return kBlockTokens * c->head_dim * c->bits / 8; }
 int sz_per_block(const kvq_cache_desc* c) { return kBlockTokens * c->head_dim / group_of(c); }
+
+}  // namespace
 
 kvq_status check_cache(const kvq_cache_desc* c) {
   if (c == nullptr) return KVQ_ERR_INVALID_ARG;
@@ -34,6 +33,8 @@ kvq_status check_cache(const kvq_cache_desc* c) {
   if (c->num_kv_heads < 1 || c->num_pages < 1) return KVQ_ERR_INVALID_ARG;
   return KVQ_OK;
 }
+
+namespace {
 
 // The specialised decode kernel's geometry; others take the general kernel.
 bool default_geometry(const kvq_cache_desc* c) { return c->head_dim == kHeadDim && group_of(c) == 128; }

@@ -82,6 +82,12 @@ struct DecodeParams {
   unsigned long long* prof;  // cycle counters [grid][32] in profiling builds, else null
 };
 
+inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+inline int group_of(const kvq_cache_desc* c) { return c->group_size == 0 ? 128 : c->group_size; }
+
+// KVQ_OK when the cache descriptor is well-formed and built (host only).
+kvq_status check_cache(const kvq_cache_desc* c);
+
 // KVQ_OK when the current device is an sm_103 GPU (and its SM count in
 // *sm_count when non-null), else KVQ_ERR_DEVICE; launches nothing.
 kvq_status check_device(int* sm_count);

@@ -133,6 +133,45 @@ typedef struct kvq_attn_desc {
  * KVQ_ERR_UNSUPPORTED. */
 #define KVQ_FLAG_E2M1_V 0x2u
 
+/* Element types of the 16-bit (and fp32) row tensors below. */
+typedef enum kvq_dtype { KVQ_BF16 = 0, KVQ_FP16 = 1, KVQ_FP32 = 2 } kvq_dtype;
+
+/* A tensor of rows [tokens][heads][head_dim] with head_dim contiguous: element
+ * (t, h, c) at data[t * stride_token + h * stride_head + c].  data is 16-byte
+ * aligned and the strides are positive multiples of 16 bytes, so that slices
+ * of a fused projection and transposed layouts are read where they lie. */
+typedef struct kvq_rows {
+  const void* data;
+  int64_t stride_token; /* elements */
+  int64_t stride_head;  /* elements */
+} kvq_rows;
+
+/* Attention over whole prompts (kvq_prompt_attn). */
+typedef struct kvq_prompt_desc {
+  int32_t dtype;        /* KVQ_BF16 or KVQ_FP16: q, k, v and out */
+  int32_t head_dim;     /* 64, 128 or 256 */
+  int32_t num_q_heads;  /* 1 to 16 times num_kv_heads */
+  int32_t num_kv_heads;
+  int32_t batch;        /* sequences, 1 to 65535 */
+  int32_t total_tokens; /* rows of q, k and v */
+  int32_t causal;       /* 1: token i sees tokens 0 .. i of its sequence; 0: all of them */
+  float sm_scale;       /* <= 0 selects 1/sqrt(head_dim) */
+  uint32_t flags;       /* 0 or KVQ_FLAG_TEST_STALL */
+} kvq_prompt_desc;
+
+/* Attention of a chunk of new tokens over the cache (kvq_chunk_attn). */
+typedef struct kvq_chunk_desc {
+  kvq_cache_desc cache;
+  int32_t dtype;        /* KVQ_BF16 or KVQ_FP16: q and out */
+  int32_t batch;        /* sequences, 1 to 65535 */
+  int32_t total_tokens; /* rows of q */
+  int32_t num_q_heads;  /* 1 to 16 times num_kv_heads */
+  int32_t max_blocks;   /* page_table row length; contiguous: blocks per sequence */
+  int32_t causal;       /* 1: a new token sees the cache up to itself; 0: the whole sequence */
+  float sm_scale;       /* <= 0 selects 1/sqrt(head_dim) */
+  uint32_t flags;       /* 0 or KVQ_FLAG_TEST_STALL */
+} kvq_chunk_desc;
+
 /* Human-readable name of a status code (static storage). */
 KVQ_API const char* kvq_status_string(kvq_status status);
 
@@ -300,6 +339,99 @@ KVQ_API kvq_status kvq_decode_attn_static(const kvq_attn_desc* desc, const uint1
  */
 KVQ_API kvq_status kvq_merge(const float* o_parts, const float* lse_parts, int32_t rows, int32_t splits,
                              int32_t head_dim, float* out, float* lse, void* stream);
+
+/*
+ * Attention over whole prompts: packed sequences of different lengths, grouped
+ * query heads, 16-bit q, k and v that are not (yet) in a cache.  Sequence b is
+ * rows [cu_seqlens[b], cu_seqlens[b + 1]) of q, k and v; within it
+ *   out[i, h] = sum_t softmax_t(S[i, t]) v[t, h / G_q],
+ *   S[i, t] = sm_scale * q[i, h] . k[t, h / G_q],  t <= i when causal,
+ * lse[i, h] = ln sum_t exp(S[i, t]).  Scores, softmax statistics and output
+ * sums are fp32; the probabilities are rounded to the 16-bit type for the
+ * second product (their sum is not), the output once at the end.
+ *   cu_seqlens int32 [batch + 1], cu_seqlens[0] >= 0, not decreasing, at most
+ *              total_tokens; sequences may be empty
+ *   out        16-bit [total_tokens][num_q_heads][head_dim], contiguous; rows
+ *              outside every sequence are left as they were
+ *   lse        fp32 [total_tokens][num_q_heads], or NULL
+ * Device errors: KVQ_DEV_BAD_SEQ_LEN (a decreasing or out-of-range
+ * cu_seqlens entry: that sequence is skipped), KVQ_DEV_TIMEOUT.
+ */
+KVQ_API kvq_status kvq_prompt_attn(const kvq_prompt_desc* desc, const kvq_rows* q, const kvq_rows* k,
+                                   const kvq_rows* v, const int32_t* cu_seqlens, void* out, float* lse,
+                                   uint32_t* dev_status, void* stream);
+
+/*
+ * Append a chunk of new tokens of every sequence to a packed K and V cache:
+ * rows [cu_seqlens[b], cu_seqlens[b + 1]) of k and v go to positions
+ * seq_lens[b], seq_lens[b] + 1, ... of sequence b.  The cache then equals what
+ * kvq_pack makes of the whole sequence (the group rule given there), and the
+ * caller advances seq_lens[b] by the chunk's length.
+ *
+ * A group of a channel-wise cache runs along the block's tokens, so a block
+ * that was begun earlier is quantized again from its raw rows, which the
+ * windows hold as for kvq_append: rows [0, seq_lens[b] % 128) of sequence b's
+ * window are the raw rows of its partial last block.  On return window_out
+ * holds those of the new partial last block (nothing is written to it when the
+ * last block is full).  window_out may be the window itself; with another
+ * buffer the call can be repeated or undone, as drafted tokens that are
+ * rejected need it.  A token-wise cache may do without (both NULL): its
+ * earlier codes are kept as they are.
+ *   dtype      KVQ_BF16, KVQ_FP16 or KVQ_FP32: k and v
+ *   k, v       rows [total_tokens][num_kv_heads][head_dim]
+ *   cu_seqlens int32 [batch + 1] as for kvq_prompt_attn
+ *   seq_lens   int32 [batch], tokens already cached; seq_lens[b] plus the
+ *              chunk's length at most max_blocks * 128
+ *   windows    fp32 [batch][num_kv_heads][128][head_dim], 16-byte aligned;
+ *              window and window_out of a channel-wise scheme must be given
+ * Device errors as kvq_append; a sequence with a bad length or a bad page is
+ * skipped (that block of it).  Values that are not finite, or whose group
+ * overflows fp16, leave their group zero and set KVQ_DEV_NONFINITE.
+ */
+KVQ_API kvq_status kvq_append_chunk(const kvq_cache_desc* cache, int32_t dtype, const kvq_rows* k, const kvq_rows* v,
+                                    int32_t batch, int32_t total_tokens, const int32_t* cu_seqlens,
+                                    const int32_t* seq_lens, const int32_t* page_table, int32_t max_blocks,
+                                    const float* k_window, const float* v_window, float* k_window_out,
+                                    float* v_window_out, uint8_t* k_codes, uint16_t* k_scale, uint16_t* k_zero,
+                                    uint8_t* v_codes, uint16_t* v_scale, uint16_t* v_zero, uint32_t* dev_status,
+                                    void* stream);
+
+/* Workspace bytes kvq_chunk_attn needs for `desc` (host only, no device needed). */
+KVQ_API kvq_status kvq_chunk_workspace_size(const kvq_chunk_desc* desc, size_t* bytes);
+
+/*
+ * Attention of a chunk of new tokens over the packed cache: a step of a
+ * chunked prompt, or the check of drafted tokens.  The new tokens are already
+ * in the cache (kvq_append_chunk): with n = cu_seqlens[b + 1] - cu_seqlens[b]
+ * and len = seq_lens[b] tokens in all, row cu_seqlens[b] + i of q is the token
+ * at position len - n + i and attends, when causal, to positions 0 to its own
+ * (a row at a negative position attends to nothing: out = 0, lse = -inf), else
+ * to all len of them.  n = 1 everywhere is a decode step; kvq_decode_attn
+ * is the faster call for that alone.
+ *
+ * The values x_hat = s * code + z are rounded once, to fp16, and both products
+ * run on fp16 operands with fp32 sums: q is scaled per row by a power of two
+ * (undone in the score), the probabilities likewise.  Where |s * code + z| of
+ * a group exceeds the fp16 range (65504) its scale is lowered to fit and
+ * KVQ_DEV_NONFINITE is set.
+ *   q          rows [total_tokens][num_q_heads][head_dim]
+ *   cu_seqlens int32 [batch + 1] as for kvq_prompt_attn
+ *   seq_lens   int32 [batch], each in [0, max_blocks * 128]
+ *   page_table int32 [batch][max_blocks] or NULL (contiguous)
+ *   out        16-bit [total_tokens][num_q_heads][head_dim], contiguous; rows
+ *              outside every sequence are left as they were
+ *   lse        fp32 [total_tokens][num_q_heads], or NULL
+ *   workspace  >= kvq_chunk_workspace_size bytes, 256-byte aligned; needs no
+ *              initialisation; concurrent calls need separate workspaces
+ * Device errors: KVQ_DEV_BAD_SEQ_LEN (rows of that sequence: out = 0,
+ * lse = -inf), KVQ_DEV_BAD_PAGE (that block's values are taken as zeros),
+ * KVQ_DEV_NONFINITE, KVQ_DEV_TIMEOUT.
+ */
+KVQ_API kvq_status kvq_chunk_attn(const kvq_chunk_desc* desc, const kvq_rows* q, const uint8_t* k_codes,
+                                  const uint16_t* k_scale, const uint16_t* k_zero, const uint8_t* v_codes,
+                                  const uint16_t* v_scale, const uint16_t* v_zero, const int32_t* cu_seqlens,
+                                  const int32_t* seq_lens, const int32_t* page_table, void* out, float* lse,
+                                  void* workspace, size_t workspace_bytes, uint32_t* dev_status, void* stream);
 
 #ifdef __cplusplus
 }
