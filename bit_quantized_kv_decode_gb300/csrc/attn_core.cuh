@@ -1,0 +1,171 @@
+// What the attention kernels over rows of new tokens share: which rows a CTA
+// has, one softmax step of a 128 x 128 score tile in tensor memory, and the
+// epilogue.
+//
+// Rows of a tile are (token, query head of one KV group) pairs, token-major:
+// all heads of the group ride in one tile, so K and V are read once for them
+// and a chunk of a few tokens still fills rows.  Row r of a tile is tensor-
+// memory lane r; one thread owns it, so the softmax needs no exchange between
+// threads and any group size works (the last 128 mod G_q rows stay unused).
+#pragma once
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include "attn_rows.h"
+#include "kvq_ptx.cuh"
+
+namespace kvq {
+namespace rows {
+
+constexpr int kTile = 128;          // rows of a tile, and keys of a tile
+constexpr float kRescaleLog2 = 8.f;  // a row's reference maximum moves when its scores exceed it by this (log2 units)
+
+// fp32 pairs in one register pair: the FMA pipe takes both at once.
+__device__ __forceinline__ uint64_t pair(float a, float b) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ void unpair(uint64_t v, float& a, float& b) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v));
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ float ex2(float x) {
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+// Two values rounded to 16 bits, lo in the low half.
+template <bool FP16>
+__device__ __forceinline__ uint32_t round2(float lo, float hi) {
+  uint32_t r;
+  if (FP16) asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  else asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+
+// A row's softmax state: the reference maximum m (in score units), the sum l
+// of exp2(c (s - m) + kShift) so far.
+struct RowState {
+  float m = -INFINITY, l = 0.f;
+};
+
+// 16-bit floating point with 5 exponent bits (fp16) loses probabilities below
+// 2^-24; raised by 2^7 they keep their bits down to 2^-31, and with the 2^8
+// that the reference maximum may lag they stay below 2^15.
+template <bool FP16>
+__host__ __device__ constexpr float shift_log2() { return FP16 ? 7.f : 0.f; }
+
+// Multiplies this warp's lanes of the D accumulator columns at t_o by alpha.
+template <int D>
+__device__ __forceinline__ void scale_rows(uint32_t t_o, float alpha) {
+  const uint64_t a2 = pair(alpha, alpha);
+#pragma unroll
+  for (int c = 0; c < D / 32; ++c) {
+    uint32_t o[32];
+    tmem_ld_32x32b_x32(t_o + 32 * c, o);
+    tc_wait_ld();
+#pragma unroll
+    for (int i = 0; i < 32; i += 2) {
+      float x, y;
+      unpair(mul2(pair(__uint_as_float(o[i]), __uint_as_float(o[i + 1])), a2), x, y);
+      o[i] = __float_as_uint(x);
+      o[i + 1] = __float_as_uint(y);
+    }
+    tmem_st_32x32b_x32p(t_o + 32 * c, o);
+  }
+}
+
+// One softmax step of this warp's 32 rows: scores in columns t_s, columns at
+// or past `seen` hidden (seen >= 128: none), probabilities written over the
+// scores as 16-bit pairs.  PERM(i) gives the score column of operand position
+// i (a permutation within the tile).  c: scale times log2(e).
+//
+// The output sums are rescaled only when a row's maximum has grown by more
+// than 2^8 since its reference was taken: until then exp2 stays below 2^8 and
+// nothing is lost in fp32, and nearly every tile is spared the pass over D
+// accumulator columns.  Each row decides for itself, so that a row's result
+// does not depend on its neighbours.
+// sums_ready() returns when the output sums hold every earlier tile.
+template <int D, bool FP16, class Perm, class Ready>
+__device__ __forceinline__ void softmax_tile(uint32_t t_s, uint32_t t_o, float c, int seen, bool first, RowState& st,
+                                             Perm perm, Ready sums_ready) {
+  uint32_t s[kTile];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) tmem_ld_32x32b_x32(t_s + 32 * i, s + 32 * i);
+  tc_wait_ld();
+  if (__any_sync(0xffffffffu, seen < kTile)) {
+#pragma unroll
+    for (int i = 0; i < kTile; ++i) s[i] = i < seen ? s[i] : 0xff800000u;
+  }
+  float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+  for (int i = 0; i < kTile; i += 8) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      mx[j] = fmaxf(fmaxf(mx[j], __uint_as_float(s[i + 2 * j])), __uint_as_float(s[i + 2 * j + 1]));
+  }
+  const float mt = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+  const bool grow = (mt - st.m) * c > kRescaleLog2;  // also the row's first finite score (m = -inf)
+  float alpha = 1.f;
+  if (grow) {
+    alpha = ex2((st.m - mt) * c);
+    st.m = mt;
+    st.l *= alpha;
+  }
+  if (!first && __any_sync(0xffffffffu, grow)) {
+    sums_ready();
+    scale_rows<D>(t_o, alpha);
+  }
+  const float off = (st.m == -INFINITY ? 0.f : -st.m * c) + shift_log2<FP16>();
+  const uint64_t c2 = pair(c, c), off2 = pair(off, off);
+  uint64_t sum0 = pair(0.f, 0.f), sum1 = sum0;
+#pragma unroll
+  for (int q = 0; q < 2; ++q) {
+    uint32_t p[32];
+#pragma unroll
+    for (int i = 0; i < 32; ++i) {
+      const int a = perm(64 * q + 2 * i), b = perm(64 * q + 2 * i + 1);
+      float x, y;
+      unpair(fma2(pair(__uint_as_float(s[a]), __uint_as_float(s[b])), c2, off2), x, y);
+      x = ex2(x);
+      y = ex2(y);
+      if (i & 1) sum1 = add2(sum1, pair(x, y));
+      else sum0 = add2(sum0, pair(x, y));
+      p[i] = round2<FP16>(x, y);
+    }
+    tmem_st_32x32b_x32p(t_s + 32 * q, p);
+  }
+  float x, y;
+  unpair(add2(sum0, sum1), x, y);
+  st.l += x + y;
+  tc_wait_st();
+}
+
+// lse in natural units.
+template <bool FP16>
+__device__ __forceinline__ float row_lse(const RowState& st, float c) {
+  return st.l > 0.f || isnan(st.l) ? (st.m * c + log2f(st.l) - shift_log2<FP16>()) * 0.6931471805599453f : -INFINITY;
+}
+
+// 3-D tensor map of a row tensor (channels, heads, tokens), 128-byte swizzle,
+// boxes of 64 channels x `heads` x `tokens`.  Defined in prompt_attn.cu.
+cudaError_t encode_rows_map(void* map, const Rows& r, int head_dim, int heads, int total, int box_heads, int box_tokens,
+                            bool fp16);
+
+}  // namespace rows
+}  // namespace kvq

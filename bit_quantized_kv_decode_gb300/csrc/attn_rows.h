@@ -43,6 +43,8 @@ __device__ __forceinline__ SeqRows seq_rows(const int32_t* cu, int b, int total)
 
 cudaError_t launch_row_attn_simple(const RowAttnParams& p, bool cached, cudaStream_t stream);
 
+cudaError_t launch_prompt_attn(const RowAttnParams& p, cudaStream_t stream);
+
 struct AppendParams {
   Rows x[2];  // K, V rows
   int dtype;

@@ -1,0 +1,532 @@
+// Attention over whole prompts on tcgen05: out = softmax(scale Q K^T) V per
+// packed sequence, K and V 16-bit rows read where they lie.
+//
+// A CTA has NT tiles of 128 rows of one sequence and KV head (kvq rows: tokens
+// x the heads of the group) and walks the key tiles of 128 tokens from its
+// last visible one down, so that the tiles that need masks come first.
+// Warps 0-3 (and 4-7) own one tile each: a thread per row takes the row's 128
+// scores from tensor memory, keeps the running maximum and sum, and puts the
+// probabilities back as the A operand of the second product.  Warp 8 copies Q,
+// K and V by TMA into a ring of slots; warp 9 issues the MMAs:
+//   S_i = Q_i K^T (both from shared memory), O_i += P_i V (P from tensor memory).
+// With two tiles (head dims 64 and 128) the tensor cores work on one tile's
+// products while the other's softmax runs; with one (head dim 256: two
+// accumulators would not fit tensor memory) the scores are double-buffered
+// along the keys instead and S of tile j + 2 follows PV of tile j.
+//
+// Tensor memory (512 columns): S_0, S_1 (128 each; P_i over S_i), O_0, O_1.
+#include <cuda.h>
+#include <cudaTypedefs.h>
+
+#include "attn_core.cuh"
+
+namespace kvq {
+namespace rows {
+
+cudaError_t encode_rows_map(void* map, const Rows& r, int head_dim, int heads, int total, int box_heads, int box_tokens,
+                            bool fp16) {
+  static const PFN_cuTensorMapEncodeTiled_v12000 encode = [] {
+    void* f = nullptr;
+    cudaDriverEntryPointQueryResult found;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &found) != cudaSuccess ||
+        found != cudaDriverEntryPointSuccess)
+      f = nullptr;
+    return reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(f);
+  }();
+  if (encode == nullptr) return cudaErrorNotSupported;
+  const cuuint64_t dims[3] = {(cuuint64_t)head_dim, (cuuint64_t)heads, (cuuint64_t)total};
+  const cuuint64_t strides[2] = {(cuuint64_t)r.sh * 2, (cuuint64_t)r.st * 2};
+  const cuuint32_t box[3] = {64, (cuuint32_t)box_heads, (cuuint32_t)box_tokens};
+  const cuuint32_t step[3] = {1, 1, 1};
+  const CUresult e = encode(static_cast<CUtensorMap*>(map),
+                            fp16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3,
+                            const_cast<void*>(r.data), dims, strides, box, step, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                            CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return e == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
+}
+
+namespace {
+
+template <int D>
+struct Shape {
+  static constexpr int kNT = D > 128 ? 1 : 2;      // row tiles
+  static constexpr int kAhead = D > 128 ? 2 : 1;   // score tiles issued ahead of their PV, per row tile
+  static constexpr int kChunks = D / 64;           // 64-channel chunks of a row (16 KB per 128 rows)
+  static constexpr int kSlotCh = D > 128 ? 2 : kChunks;  // chunks of a ring slot
+  static constexpr int kParts = kChunks / kSlotCh;       // slots of a K or V tile
+  static constexpr int kSlotBytes = kSlotCh * 16384;
+  static constexpr int kQBytes = kNT * kChunks * 16384;
+  static constexpr int kSlots = D == 64 ? 8 : 5;
+  static constexpr int kThreads = 384;  // three warpgroups: softmax, softmax, copies and products
+  static constexpr int kSmem = kQBytes + kSlots * kSlotBytes + 512 + 4 * D;
+  static_assert(kSmem <= 227 * 1024, "shared memory");
+};
+
+struct Aux {  // after the ring
+  uint64_t full[8], empty[8], q, fixed[2], s[2], p[2], sums, done;
+  uint32_t tmem;
+  int fail, any_bad;
+  int seq_first, seq_n, tile;  // this CTA's sequence (rows [first, first + n)) and tile; tile < 0: none
+};
+static_assert(sizeof(Aux) <= 512, "Aux");
+
+// The first tokens, counted from the first key tile that is not seen whole
+// (two such tiles at most), at which a channel of V holds a NaN, +inf, -inf:
+// ten bits each, kNone where there is none.
+constexpr uint32_t kNone = 0x3ff;
+constexpr uint32_t kNoneAll = kNone | kNone << 10 | kNone << 20;
+
+// Which sequence and tile the rank-th CTA of a KV head has.  Run by one warp.
+// Causal tiles cost in proportion to their place in the sequence, so they are
+// handed out by falling place over all sequences at once: the rank's place t
+// is found by bisection on cum(t) = sum_b max(0, tiles_b - t), the number of
+// tiles at places >= t.  (Up to 256 sequences, eight to a lane; beyond that,
+// and without a causal mask, in order of the sequences.)
+__device__ void find_tile(const RowAttnParams& p, int rank, int per_tile, bool lead, Aux* aux) {
+  const int lane = threadIdx.x & 31;
+  int seq = -1, tile = -1;
+  if (p.causal && p.batch <= 256) {
+    int nt[8], most = 0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const int b = lane + 32 * i;
+      nt[i] = 0;
+      if (b < p.batch) {
+        const SeqRows s = seq_rows(p.cu, b, p.total);
+        if (s.bad && lead) report(p.dev_status, KVQ_DEV_BAD_SEQ_LEN);
+        nt[i] = (s.n + per_tile - 1) / per_tile;
+      }
+      most = max(most, nt[i]);
+    }
+    most = __reduce_max_sync(0xffffffffu, most);
+    auto cum = [&](int t) {
+      int n = 0;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) n += max(0, nt[i] - t);
+      return __reduce_add_sync(0xffffffffu, n);
+    };
+    if (rank < cum(0)) {
+      int lo = 0, hi = most;  // cum(lo) > rank >= cum(hi)
+      while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (cum(mid) > rank) lo = mid;
+        else hi = mid;
+      }
+      tile = lo;
+      int k = rank - cum(lo + 1);  // the k-th sequence with more than `tile` tiles
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const uint32_t has = __ballot_sync(0xffffffffu, nt[i] > tile);
+        if (seq < 0) {
+          if (k < __popc(has)) seq = 32 * i + __fns(has, 0, k + 1);
+          else k -= __popc(has);
+        }
+      }
+    }
+  } else {
+    for (int b0 = 0; b0 < p.batch && seq < 0; b0 += 32) {
+      const int b = b0 + lane;
+      SeqRows s{0, 0, false};
+      if (b < p.batch) s = seq_rows(p.cu, b, p.total);
+      if (s.bad && lead) report(p.dev_status, KVQ_DEV_BAD_SEQ_LEN);
+      const int n = (s.n + per_tile - 1) / per_tile;
+      int incl = n;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int v = __shfl_up_sync(0xffffffffu, incl, o);
+        if (lane >= o) incl += v;
+      }
+      const uint32_t past = __ballot_sync(0xffffffffu, incl > rank);
+      if (past != 0) {
+        const int l = __ffs(past) - 1;
+        seq = b0 + l;
+        tile = rank - (__shfl_sync(0xffffffffu, incl, l) - __shfl_sync(0xffffffffu, n, l));
+        break;
+      }
+      rank -= __shfl_sync(0xffffffffu, incl, 31);
+    }
+  }
+  if (lane == 0) {
+    aux->tile = tile;
+    if (tile >= 0) {
+      const SeqRows s = seq_rows(p.cu, seq, p.total);
+      aux->seq_first = s.first;
+      aux->seq_n = s.n;
+    }
+  }
+}
+
+// A V tile that some rows see only in part: tokens from `valid` on (another
+// sequence's rows, or none) become zeros, and values that are not finite are
+// zeroed and noted in `bad`, so that a zero probability keeps them out of the
+// rows before them; the epilogue adds them to the rows from there on.  token0:
+// the tile's first token as `bad` counts them.  One warp.
+template <bool FP16>
+__device__ void mend_values(unsigned char* slot, int chunks, int channel0, int token0, int valid, uint32_t* bad,
+                            int* any_bad) {
+  const int lane = threadIdx.x & 31;
+  const uint32_t inf = FP16 ? 0x7c00u : 0x7f80u;
+  uint32_t acc = 0;
+  const int n = chunks * kTile * 8;
+#pragma unroll 4
+  for (int i = lane; i < n; i += 32) {  // 16 bytes each; rows of 8
+    const int t = (i >> 3) & (kTile - 1);
+    uint4* at = reinterpret_cast<uint4*>(slot) + i;
+    if (t >= valid) {
+      *at = make_uint4(0u, 0u, 0u, 0u);
+    } else {
+      const uint4 v = *at;
+      const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {  // an all-ones exponent in either half carries into its sign bit
+        const uint32_t e = (w[j] & (inf * 0x10001u)) + (FP16 ? 0x04000400u : 0x00800080u);
+        acc |= e & 0x80008000u;
+      }
+    }
+  }
+  if (!__any_sync(0xffffffffu, acc != 0)) return;
+  if (lane == 0) *any_bad = 1;
+#pragma unroll 1
+  for (int i = lane; i < n; i += 32) {
+    const int t = (i >> 3) & (kTile - 1), chunk = (i >> 3) / kTile, c16 = (i & 7) ^ (t & 7);
+    if (t >= valid) continue;
+    uint16_t* at = reinterpret_cast<uint16_t*>(slot) + i * 8;
+#pragma unroll 1
+    for (int j = 0; j < 8; ++j) {
+      const uint32_t w = at[j];
+      if ((w & inf) != inf) continue;
+      const int shift = (w & 0x7fffu) != inf ? 0 : (w >> 15) ? 20 : 10;
+      uint32_t* word = &bad[channel0 + chunk * 64 + c16 * 8 + j];
+      uint32_t was = *word;
+      while (((was >> shift) & kNone) > (uint32_t)(token0 + t)) {
+        const uint32_t got = atomicCAS(word, was, (was & ~(kNone << shift)) | (uint32_t)(token0 + t) << shift);
+        if (got == was) break;
+        was = got;
+      }
+      at[j] = 0;
+    }
+  }
+}
+
+template <int D, bool FP16>
+__global__ void __launch_bounds__(Shape<D>::kThreads, 1)
+prompt_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CUtensorMap map_k,
+              const __grid_constant__ CUtensorMap map_v, const RowAttnParams p) {
+  using Sh = Shape<D>;
+  constexpr int NT = Sh::kNT;
+  extern __shared__ __align__(1024) unsigned char smem[];
+  unsigned char* q_s = smem;
+  unsigned char* ring = smem + Sh::kQBytes;
+  Aux* aux = reinterpret_cast<Aux*>(ring + Sh::kSlots * Sh::kSlotBytes);
+  uint32_t* bad = reinterpret_cast<uint32_t*>(reinterpret_cast<unsigned char*>(aux) + 512);  // [D]
+  volatile int* fail = &aux->fail;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int kvh = blockIdx.x % p.num_kv_heads, rank = blockIdx.x / p.num_kv_heads;
+  const int tok_tile = kTile / p.gq;          // tokens of a row tile
+  const int tok_cta = tok_tile * NT;
+
+  if (warp == 0) find_tile(p, rank, tok_cta, blockIdx.x == 0, aux);
+  if (warp == 8) {
+    if (lane == 0) {
+      tma_prefetch_map(&map_q);
+      tma_prefetch_map(&map_k);
+      tma_prefetch_map(&map_v);
+      for (int i = 0; i < Sh::kSlots; ++i) {
+        mbar_init(&aux->full[i], 1);
+        mbar_init(&aux->empty[i], 1);
+      }
+      mbar_init(&aux->q, 1);
+      mbar_init(&aux->sums, 1);
+      mbar_init(&aux->done, 1);
+      for (int i = 0; i < 2; ++i) {
+        mbar_init(&aux->fixed[i], 1);
+        mbar_init(&aux->s[i], 1);
+        mbar_init(&aux->p[i], 4);
+      }
+      aux->fail = 0;
+      aux->any_bad = 0;
+      fence_barrier_init();
+    }
+    __syncwarp();
+  }
+  if (warp == 9) {
+    tmem_alloc(&aux->tmem, 512);
+    tmem_relinquish();
+  }
+  for (int i = tid; i < D; i += Sh::kThreads) bad[i] = kNoneAll;
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = aux->tmem;
+  const int tile = aux->tile;
+  if (tile >= 0) {
+    const int first = aux->seq_first, n = aux->seq_n;
+    const int tok0 = tile * tok_cta;                        // first token of the CTA, in its sequence
+    const int ntok = min(tok_cta, n - tok0);
+    const int act = NT == 2 && ntok > tok_tile ? 2 : 1;     // row tiles in use
+    const int last = p.causal ? (tok0 + ntok - 1) / kTile : (n - 1) / kTile;  // last visible key tile
+    const int tiles = last + 1;
+    // the first `mend` tiles of the walk hold tokens that some row must not see
+    const int clean = p.causal ? (tok0 + 1) / kTile : n / kTile;  // key tiles below this are seen whole by every row
+    const int mend = tiles - min(clean, tiles);
+    const uint64_t limit = (p.flags & KVQ_FLAG_TEST_STALL) ? 50ull * 1000 * 1000 : 2ull * 1000 * 1000 * 1000;
+    auto wait = [&](uint64_t* bar, uint32_t parity) -> bool {
+      if (mbar_wait_bounded<true>(bar, parity, fail, limit)) return true;
+      *fail = 1;
+      return false;
+    };
+
+    // Registers: 384 threads x 168 at launch; the softmax warpgroups take 208
+    // each (a row's 128 scores stay in registers), the third keeps 88.
+    if (warp >= (NT == 2 ? 8 : 4)) {
+      setmaxnreg_dec<88>();
+    if (warp == 8) {
+      // ------------------------------------------------------------ copies
+      int slot = 0, round = 0, issued = 0;
+      bool ok = true;
+      auto load = [&](const CUtensorMap& map, int j, int part) {  // one slot of key tile j
+        if (!ok) return;
+        if (round > 0) ok = wait(&aux->empty[slot], (round - 1) & 1);
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) return;
+        if (lane == 0) {
+          mbar_arrive_expect_tx(&aux->full[slot], Sh::kSlotBytes);
+#pragma unroll
+          for (int c = 0; c < Sh::kSlotCh; ++c)
+            tma_load_3d(ring + slot * Sh::kSlotBytes + c * 16384, &map, (part * Sh::kSlotCh + c) * 64, kvh,
+                        first + j * kTile, &aux->full[slot]);
+        }
+        ++issued;
+        if (++slot == Sh::kSlots) { slot = 0; ++round; }
+      };
+      if (lane == 0) {
+        const int box = tok_tile * p.gq * 128;
+        mbar_arrive_expect_tx(&aux->q, act * Sh::kChunks * box);
+        for (int i = 0; i < act; ++i)
+          for (int c = 0; c < Sh::kChunks; ++c)
+            tma_load_3d(q_s + (i * Sh::kChunks + c) * 16384, &map_q, c * 64, kvh * p.gq, first + tok0 + i * tok_tile,
+                        &aux->q);
+      }
+      const bool stall = (p.flags & KVQ_FLAG_TEST_STALL) && blockIdx.x == 0;
+      for (int i = 0; i < Sh::kAhead && i < tiles; ++i)
+        for (int part = 0; part < Sh::kParts; ++part) load(map_k, last - i, part);
+      for (int i = 0; i < tiles && ok; ++i) {
+        if (stall) break;  // test hook: the V tiles of the first CTA are withheld
+        const int vslot = slot, vround = round;
+        for (int part = 0; part < Sh::kParts; ++part) load(map_v, last - i, part);
+        if (i + Sh::kAhead < tiles)
+          for (int part = 0; part < Sh::kParts; ++part) load(map_k, last - i - Sh::kAhead, part);
+        if (i < mend && ok) {
+          int s = vslot, r = vround;
+          for (int part = 0; part < Sh::kParts && ok; ++part) {
+            ok = __all_sync(0xffffffffu, wait(&aux->full[s], r & 1));
+            if (ok)
+              mend_values<FP16>(ring + s * Sh::kSlotBytes, Sh::kSlotCh, part * Sh::kSlotCh * 64,
+                                (last - i - clean) * kTile, min(kTile, n - (last - i) * kTile), bad, &aux->any_bad);
+            if (++s == Sh::kSlots) { s = 0; ++r; }
+          }
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&aux->fixed[i]);
+        }
+      }
+      // copies in flight land before this CTA's shared memory is given up
+      const int from = issued > Sh::kSlots ? issued - Sh::kSlots : 0;
+      for (int k = from; k < issued; ++k)
+        mbar_wait_bounded<true>(&aux->full[k % Sh::kSlots], (k / Sh::kSlots) & 1, nullptr, limit);
+      mbar_wait_bounded<true>(&aux->q, 0, nullptr, limit);
+    } else if (warp == 9) {
+      // ------------------------------------------------------------ products
+      if (lane == 0) {
+        constexpr uint32_t fmt = FP16 ? 0u : 1u;
+        constexpr uint32_t idesc_s = make_idesc(fmt, fmt, 0, 0, 128, 128);
+        constexpr int kN = D < 128 ? D : 128;
+        constexpr uint32_t idesc_o = make_idesc(fmt, fmt, 0, 1, 128, kN);
+        const uint32_t q_a = smem_u32(q_s), ring_a = smem_u32(ring);
+        int slot = 0, round = 0;  // next slot to consume
+        bool ok = wait(&aux->q, 0);
+        // S of row tile i <- Q_i K^T with K in the slots from `sl`
+        auto scores = [&](int i, int buf, int sl) {
+          const uint32_t d = tmem + 128 * buf;
+#pragma unroll
+          for (int k = 0; k < D / 16; ++k) {
+            const int c = k / 4, part = c / Sh::kSlotCh;
+            int s = sl + part;
+            if (s >= Sh::kSlots) s -= Sh::kSlots;
+            mma_f16_ss(d, make_smem_desc_sw128(q_a + (i * Sh::kChunks + c) * 16384 + (k % 4) * 32, 0),
+                       make_smem_desc_sw128(ring_a + s * Sh::kSlotBytes + (c % Sh::kSlotCh) * 16384 + (k % 4) * 32, 0),
+                       idesc_s, k > 0);
+          }
+        };
+        auto values = [&](int i, int buf, int sl, bool add) {
+#pragma unroll
+          for (int part = 0; part < Sh::kParts; ++part) {
+            int s = sl + part;
+            if (s >= Sh::kSlots) s -= Sh::kSlots;
+#pragma unroll
+            for (int k = 0; k < kTile / 16; ++k)
+              mma_f16_ts(tmem + 256 + i * D + part * 128, tmem + 128 * buf + 8 * k,
+                         make_smem_desc_sw128(ring_a + s * Sh::kSlotBytes + k * 2048, 16384), idesc_o, add || k > 0);
+          }
+        };
+        auto take = [&](int& sl) {  // the next tile's slots, loaded
+          sl = slot;
+          for (int part = 0; part < Sh::kParts && ok; ++part) {
+            ok = wait(&aux->full[slot], round & 1);
+            if (++slot == Sh::kSlots) { slot = 0; ++round; }
+          }
+        };
+        auto release = [&](int sl) {
+          for (int part = 0; part < Sh::kParts; ++part) {
+            tc_commit(&aux->empty[sl]);
+            if (++sl == Sh::kSlots) sl = 0;
+          }
+        };
+        int ks;
+#pragma unroll 1
+        for (int j = 0; j < Sh::kAhead && j < tiles && ok; ++j) {
+          take(ks);
+          if (!ok) break;
+#pragma unroll 1
+          for (int i = 0; i < act; ++i) {
+            scores(i, NT == 2 ? i : j, ks);
+            tc_commit(&aux->s[NT == 2 ? i : j]);
+          }
+          release(ks);
+        }
+#pragma unroll 1
+        for (int j = 0; j < tiles && ok; ++j) {
+          int vs;
+          take(vs);
+          if (ok && j < mend) ok = wait(&aux->fixed[j], 0);
+          const bool more = j + Sh::kAhead < tiles;
+          if (ok && more) take(ks);
+#pragma unroll 1
+          for (int i = 0; i < act && ok; ++i) {
+            const int buf = NT == 2 ? i : j & 1;
+            ok = wait(&aux->p[buf], (NT == 2 ? j : j >> 1) & 1);
+            if (!ok) break;
+            tc_fence_after();
+            values(i, buf, vs, j > 0);
+            if (NT == 1) tc_commit(&aux->sums);
+            if (i == act - 1) release(vs);
+            if (more) {
+              scores(i, buf, ks);
+              tc_commit(&aux->s[buf]);
+            }
+          }
+          if (ok && more) release(ks);
+        }
+        tc_commit(&aux->done);
+        mbar_wait_bounded<true>(&aux->done, 0, nullptr, limit);  // nothing in flight when tensor memory is freed
+      }
+      __syncwarp();
+    }
+    } else {
+      // ------------------------------------------------------------ softmax
+      setmaxnreg_inc<208>();
+      const int i = NT == 2 ? warp >> 2 : 0;
+      const int r = tid & 127;  // row of the tile = lane of tensor memory
+      const uint32_t lanes = (uint32_t)(warp & 3) << 21;
+      const int rows = min(tok_tile, ntok - i * tok_tile) * p.gq;
+      if (i < act) {
+        const bool mine = r < rows, any = (warp & 3) * 32 < rows;
+        const int tok = tok0 + i * tok_tile + r / p.gq;
+        const uint32_t t_o = tmem + lanes + 256 + i * D;
+        RowState st;
+        bool ok = true;
+        for (int j = 0; j < tiles && ok; ++j) {
+          const int buf = NT == 2 ? i : j & 1;
+          ok = __all_sync(0xffffffffu, wait(&aux->s[buf], (NT == 2 ? j : j >> 1) & 1));
+          if (!ok) break;
+          tc_fence_after();
+          if (any) {
+            const int k0 = (last - j) * kTile;
+            const int seen = !mine ? kTile : (p.causal ? min(n, tok + 1) : n) - k0;
+            softmax_tile<D, FP16>(tmem + lanes + 128 * buf, t_o, p.scale_log2, seen, j == 0, st,
+                                  [](int x) { return x; },
+                                  // two tiles: S of tile j was issued after PV of tile j - 1, and so is done after it
+                                  [&] {
+                                    if (NT == 1) {
+                                      wait(&aux->sums, (j - 1) & 1);
+                                      __syncwarp();
+                                      tc_fence_after();
+                                    }
+                                  });
+          }
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&aux->p[buf]);
+        }
+        ok = ok && __all_sync(0xffffffffu, wait(&aux->done, 0));
+        if (ok && any) {
+          tc_fence_after();
+          const long long row = (long long)(first + tok) * p.num_q_heads + kvh * p.gq + r % p.gq;
+          const float inv = st.l > 0.f || isnan(st.l) ? 1.f / st.l : 0.f;
+          uint4* dst = reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.out) + row * D);
+          const bool spoiled = aux->any_bad != 0;
+#pragma unroll
+          for (int c = 0; c < D / 32; ++c) {
+            uint32_t o[32];
+            tmem_ld_32x32b_x32(t_o + 32 * c, o);
+            tc_wait_ld();
+            if (mine) {
+              float x[32];
+#pragma unroll
+              for (int k = 0; k < 32; ++k) x[k] = __uint_as_float(o[k]) * inv;
+              if (spoiled) {
+#pragma unroll
+                for (int k = 0; k < 32; ++k) {
+                  const uint32_t w = bad[32 * c + k], at = (uint32_t)(tok - clean * kTile);
+                  if ((w & kNone) != kNone && at >= (w & kNone)) x[k] = NAN;
+                  if ((w >> 10 & kNone) != kNone && at >= (w >> 10 & kNone)) x[k] += INFINITY;
+                  if ((w >> 20) != kNone && at >= (w >> 20)) x[k] -= INFINITY;
+                }
+              }
+#pragma unroll
+              for (int k = 0; k < 4; ++k)
+                dst[4 * c + k] = make_uint4(round2<FP16>(x[8 * k], x[8 * k + 1]), round2<FP16>(x[8 * k + 2], x[8 * k + 3]),
+                                            round2<FP16>(x[8 * k + 4], x[8 * k + 5]),
+                                            round2<FP16>(x[8 * k + 6], x[8 * k + 7]));
+            }
+          }
+          if (mine && p.lse != nullptr) p.lse[row] = row_lse<FP16>(st, p.scale_log2);
+        }
+      }
+    }
+  }
+  __syncwarp();
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 9) tmem_dealloc(tmem, 512);
+  if (tid == 0 && aux->fail) report(p.dev_status, KVQ_DEV_TIMEOUT);
+}
+
+template <int D, bool FP16>
+cudaError_t launch(const RowAttnParams& p, cudaStream_t stream) {
+  using Sh = Shape<D>;
+  CUtensorMap maps[3];
+  cudaError_t e = encode_rows_map(&maps[0], p.q, D, p.num_q_heads, p.total, p.gq, kTile / p.gq, FP16);
+  if (e == cudaSuccess) e = encode_rows_map(&maps[1], p.k, D, p.num_kv_heads, p.total, 1, kTile, FP16);
+  if (e == cudaSuccess) e = encode_rows_map(&maps[2], p.v, D, p.num_kv_heads, p.total, 1, kTile, FP16);
+  if (e != cudaSuccess) return e;
+  e = cudaFuncSetAttribute(prompt_kernel<D, FP16>, cudaFuncAttributeMaxDynamicSharedMemorySize, Sh::kSmem);
+  if (e != cudaSuccess) return e;
+  const long long tiles = p.total / (kTile / p.gq * Sh::kNT) + (p.batch < p.total ? p.batch : p.total);
+  if (tiles * p.num_kv_heads > 0x7fffffffLL) return cudaErrorInvalidValue;
+  prompt_kernel<D, FP16><<<(unsigned)(tiles * p.num_kv_heads), Sh::kThreads, Sh::kSmem, stream>>>(maps[0], maps[1],
+                                                                                                 maps[2], p);
+  return cudaGetLastError();
+}
+
+}  // namespace
+}  // namespace rows
+
+cudaError_t launch_prompt_attn(const RowAttnParams& p, cudaStream_t stream) {
+  if (p.head_dim == 64) return p.fp16 ? rows::launch<64, true>(p, stream) : rows::launch<64, false>(p, stream);
+  if (p.head_dim == 128) return p.fp16 ? rows::launch<128, true>(p, stream) : rows::launch<128, false>(p, stream);
+  return p.fp16 ? rows::launch<256, true>(p, stream) : rows::launch<256, false>(p, stream);
+}
+
+}  // namespace kvq

@@ -78,7 +78,7 @@ KVQ_API kvq_status kvq_prompt_attn(const kvq_prompt_desc* d, const kvq_rows* q, 
   p.gq = d->num_q_heads / d->num_kv_heads;
   p.head_dim = d->head_dim; p.causal = d->causal; p.fp16 = d->dtype == KVQ_FP16;
   p.scale_log2 = scale_log2(d->sm_scale, d->head_dim); p.flags = d->flags;
-  return launch_row_attn_simple(p, false, static_cast<cudaStream_t>(stream)) == cudaSuccess ? KVQ_OK : KVQ_ERR_CUDA;
+  return launch_prompt_attn(p, static_cast<cudaStream_t>(stream)) == cudaSuccess ? KVQ_OK : KVQ_ERR_CUDA;
 }
 
 KVQ_API kvq_status kvq_append_chunk(const kvq_cache_desc* cache, int32_t dtype, const kvq_rows* k, const kvq_rows* v,

@@ -223,3 +223,16 @@ def test_many_sequences():
         rows = slice(cu[b], cu[b + 1])
         ref, _, tol, _ = attend64(q[rows], k[rows], v[rows], 0, True, 1 / 8, HALF_STEP[q.dtype])
         assert_rows_close(out[rows], ref, tol, q.dtype, f"sequence {b}")
+
+
+@pytest.mark.parametrize("dim", [64, 128, 256])
+def test_withheld_copies_time_out(dim):
+    """A copy that never arrives ends in a status, not in a hang; the next call
+    is right again."""
+    import bit_quantized_kv_decode_gb300 as kvq
+    q, k, v = make(700, 4, 2, dim, torch.bfloat16, seed=14)
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    kvq.prompt_attn(q, k, v, starts([700]).cuda(), dev_status=status, flags=kvq.FLAG_TEST_STALL)
+    torch.cuda.synchronize()
+    assert int(status.item()) == kvq.DEV_TIMEOUT
+    check(q, k, v, [700])
