@@ -1,0 +1,118 @@
+// Chunk attention: launch shape, workspace and the merge of cut tiles.
+#include "chunk_attn.cuh"
+
+namespace kvq {
+namespace chunk {
+namespace {
+
+constexpr int kGrid = 152;  // one CTA per SM; they do not wait on one another, so fewer SMs only take longer
+constexpr int kSmem = 227 * 1024;
+constexpr int kMergeThreads = 256, kMergeRows = 32;
+
+// Joins the parts of the tile that the border between CTAs blockIdx.x and
+// blockIdx.x + 1 is the first to cut, rows blockIdx.y * 32 on:
+// lse = log2 sum 2^lse_i, out = sum 2^(lse_i - lse) o_i.  A warp per row.
+template <int D>
+__global__ void __launch_bounds__(kMergeThreads) merge_kernel(const Params P, int nt, int grid) {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  __shared__ long long scan[kMergeThreads / 32], range[3];
+  __shared__ Place at;
+  const RowAttnParams& p = P.r;
+  const int cta = blockIdx.x + 1, tid = threadIdx.x, lane = tid & 31;
+  const int tok_tile = kTile / p.gq, tok_cta = tok_tile * nt;
+  find_place<kMergeThreads>(p, tok_cta, cta, grid, scan, &at, range, false);
+  const long long total = range[2];
+  if (range[0] >= total || at.x == 0) return;  // past the last step (`at` is unset), or between two tiles
+  const long long tile0 = at.tile0, before = total * (cta - 1) / grid;
+  if (before > tile0) return;  // an earlier border cut this tile
+  uint32_t bad = 0;
+  const Seq s = load_seq(p, at.b, &bad);
+  const long long end = tile0 + tile_steps(s, at.t, tok_cta, p.causal);
+  const int slot0 = 2 * (cta - 1) + (before == tile0 ? 0 : 1);
+  for (int i = tid >> 5; i < kMergeRows; i += kMergeThreads / 32) {
+    const int prow = blockIdx.y * kMergeRows + i, r = prow & (kTile - 1);
+    const int tile_tok = at.t * tok_cta + (prow / kTile) * tok_tile, tok = tile_tok + r / p.gq;
+    if (r >= tok_tile * p.gq || tok >= s.n) continue;
+    const size_t pitch = (size_t)nt * kTile;
+    auto part = [&](int c) { return (size_t)(c < cta ? slot0 : 2 * c) * pitch + prow; };
+    float m = -INFINITY;
+    for (int c = cta - 1 + lane; c < grid && total * c / grid < end; c += 32)
+      if (c < cta || total * (c + 1) / grid > total * c / grid) m = fmaxf(m, P.part_lse[part(c)]);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+    float acc[D / 32], sum = 0.f;
+#pragma unroll
+    for (int c = 0; c < D / 32; ++c) acc[c] = 0.f;
+    for (int c = cta - 1; c < grid && total * c / grid < end; ++c) {
+      if (c >= cta && total * (c + 1) / grid <= total * c / grid) continue;
+      const size_t at_part = part(c);
+      const float l = P.part_lse[at_part];
+      if (l == -INFINITY) continue;  // nothing seen in this part
+      const float w = exp2f(l - m);
+      sum += w;
+      const float* o = P.part_o + at_part * D + lane * (D / 32);
+#pragma unroll
+      for (int e = 0; e < D / 32; ++e) acc[e] = fmaf(w, o[e], acc[e]);
+    }
+    const float inv = sum > 0.f || isnan(sum) ? 1.f / sum : 0.f;
+    const long long row = (long long)(s.first + tok) * p.num_q_heads + at.h * p.gq + r % p.gq;
+    uint32_t* dst = reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(p.out) + row * D + lane * (D / 32));
+#pragma unroll
+    for (int e = 0; e < D / 64; ++e)
+      dst[e] = p.fp16 ? rows::round2<true>(acc[2 * e] * inv, acc[2 * e + 1] * inv)
+                      : rows::round2<false>(acc[2 * e] * inv, acc[2 * e + 1] * inv);
+    if (lane == 0 && p.lse != nullptr)
+      p.lse[row] = sum > 0.f || isnan(sum) ? (m + log2f(sum)) * 0.6931471805599453f : -INFINITY;
+  }
+}
+
+}  // namespace
+}  // namespace chunk
+
+ChunkPlan chunk_plan(int head_dim, int batch, int total, int num_q_heads, int num_kv_heads) {
+  ChunkPlan c;
+  // two row tiles where the sequences have more rows than one on average
+  // (head dim 256: one, its accumulators fill tensor memory)
+  const long long rows = (long long)total * (num_q_heads / num_kv_heads);
+  c.nt = head_dim <= 128 && rows > (long long)batch * chunk::kTile ? 2 : 1;
+  c.grid = chunk::kGrid;
+  const size_t slots = (size_t)2 * c.grid * c.nt * chunk::kTile;
+  c.part_lse = slots * head_dim * sizeof(float);
+  c.total = c.part_lse + slots * sizeof(float);
+  return c;
+}
+
+cudaError_t launch_chunk_attn(const RowAttnParams& p, const ChunkPlan& plan, void* workspace, cudaStream_t stream) {
+  using namespace chunk;
+  Params P{};
+  P.r = p;
+  P.part_o = static_cast<float*>(workspace);
+  P.part_lse = reinterpret_cast<float*>(static_cast<unsigned char*>(workspace) + plan.part_lse);
+  const int nsz = kBlockTokens * p.head_dim / p.group;
+  P.gshift = p.group == 32 ? 5 : p.group == 64 ? 6 : 7;
+  P.table_bytes = 4 * nsz;
+  P.unit_bytes = kBlockTokens * p.head_dim * p.bits / 8 + 4 * nsz;
+  const int fixed = fixed_bytes(p.head_dim, plan.nt) + dequant_groups(plan.nt) * 2 * P.table_bytes;
+  P.units = (kSmem - fixed) / P.unit_bytes;
+  if (P.units > kMaxUnits) P.units = kMaxUnits;
+  P.units &= ~1;  // a unit's place in the ring belongs to one dequantising warpgroup
+  if (P.units < 2) return cudaErrorInvalidValue;
+  const size_t smem = (size_t)fixed + (size_t)P.units * P.unit_bytes;
+  cudaError_t e = p.bits == 2 ? launch_i2(p.head_dim, plan.nt, P, plan.grid, smem, stream)
+                              : launch_i4(p.head_dim, plan.nt, P, plan.grid, smem, stream);
+  if (e != cudaSuccess) return e;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(plan.grid - 1), (unsigned)(plan.nt * kTile / kMergeRows));
+  cfg.blockDim = dim3(kMergeThreads);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  if (p.head_dim == 64) return cudaLaunchKernelEx(&cfg, merge_kernel<64>, P, plan.nt, plan.grid);
+  if (p.head_dim == 128) return cudaLaunchKernelEx(&cfg, merge_kernel<128>, P, plan.nt, plan.grid);
+  return cudaLaunchKernelEx(&cfg, merge_kernel<256>, P, plan.nt, plan.grid);
+}
+
+}  // namespace kvq

@@ -1,0 +1,758 @@
+// Attention of chunks of new tokens over the packed cache, on tcgen05.
+//
+// Work: a row tile is up to NT x 128 (token, head) rows of one sequence and KV
+// head, and costs one step per key tile of 128 tokens (a cache block).  All
+// steps of all tiles, in a fixed order, are cut into as many equal ranges as
+// there are CTAs; a CTA walks its range tile by tile (a segment each).  A tile
+// that a range border cuts leaves partial results (normalised outputs and
+// their log-sum-exp) that merge_kernel joins; at most two segments of a CTA are
+// partial.  So ragged batches, one long sequence and many short ones balance
+// alike, without a host round trip: every CTA works the cut out by itself from
+// cu_seqlens and seq_lens.
+//
+// A step: the block's packed codes, scales and offsets come in by bulk copies
+// (warp `copy`); a dequantising warpgroup turns them into fp16 operands in
+// shared memory (x_hat = s code + z, one rounding); S = Q K^T and O += P V run
+// on the tensor cores with fp32 accumulators in tensor memory; a thread per
+// row does the softmax in between (attn_core.cuh).  K and V operands are both
+// K-major: K rows are tokens, V rows are channels, as the cache packs them, and
+// neighbouring codes are split off two at a time (the halves of a 32-bit word),
+// which leaves the contraction index in a permuted order within 8 (4-bit) or
+// 16 (2-bit) elements; Q's channels and P's tokens are put in the same order.
+#pragma once
+#include "attn_core.cuh"
+#include "chunk_attn.h"
+
+namespace kvq {
+namespace chunk {
+
+using rows::kTile;
+using rows::RowState;
+
+// ---------------------------------------------------------------- the plan
+
+// Tokens of sequence b's chunk and of its cache; a bad entry empties it.
+struct Seq {
+  int first, n, len;
+};
+__device__ __forceinline__ Seq load_seq(const RowAttnParams& p, int b, uint32_t* bad) {
+  const SeqRows s = seq_rows(p.cu, b, p.total);
+  int len = p.seq_lens[b];
+  if (s.bad) *bad |= KVQ_DEV_BAD_SEQ_LEN;
+  if (len < 0 || len > p.max_blocks * kBlockTokens) {
+    *bad |= KVQ_DEV_BAD_SEQ_LEN;
+    len = 0;
+  }
+  return {s.first, s.n, len};
+}
+// Key tiles that tile t (tok tokens) of the sequence sees.
+__device__ __forceinline__ int key_tiles(const Seq& s, int t, int tok, int causal) {
+  const int end = min((t + 1) * tok, s.n);
+  const int top = causal ? s.len - s.n + end : s.len;
+  return top > 0 ? (top + kTile - 1) / kTile : 0;
+}
+// Steps of tile t: a tile that sees nothing still has its rows written.
+__device__ __forceinline__ int tile_steps(const Seq& s, int t, int tok, int causal) {
+  return max(1, key_tiles(s, t, tok, causal));
+}
+__device__ __forceinline__ long long seq_steps(const Seq& s, int tok, int causal) {
+  const int nt = (s.n + tok - 1) / tok;
+  if (nt == 0) return 0;
+  if (!causal) return (long long)nt * tile_steps(s, 0, tok, 0);
+  long long n = 0;
+  for (int t = 0; t < nt; ++t) n += tile_steps(s, t, tok, 1);
+  return n;
+}
+
+// A place in the order of all steps: head, sequence, tile, step of the tile.
+struct Place {
+  int h, b, t, x;
+  int pad;
+  long long per_head, tile0;  // steps of one head; index of the tile's first step
+};
+
+// The place of step `at` (of all per_head * heads), found by the whole block;
+// scan: block-wide scratch of blockDim.x / 32 long longs; range: the CTA's
+// steps [range[0], range[1]) and range[2] of them in all.
+template <int NT>
+__device__ __forceinline__ void find_place(const RowAttnParams& p, int tok, int cta, int grid, long long* scan,
+                                           Place* out, long long* range, bool report_bad) {
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int per = (p.batch + NT - 1) / NT, b0 = min(p.batch, tid * per), b1 = min(p.batch, b0 + per);
+  uint32_t bad = 0;
+  long long mine = 0;
+  for (int b = b0; b < b1; ++b) mine += seq_steps(load_seq(p, b, &bad), tok, p.causal);
+  if (report_bad && bad) report(p.dev_status, bad);
+  long long incl = mine;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const long long v = __shfl_up_sync(0xffffffffu, incl, o);
+    if (lane >= o) incl += v;
+  }
+  if (lane == 31) scan[warp] = incl;
+  __syncthreads();
+  long long base = 0, all = 0;
+  for (int w = 0; w < NT / 32; ++w) {
+    if (w < warp) base += scan[w];
+    all += scan[w];
+  }
+  const long long lo = base + incl - mine;  // this thread's sequences: steps [lo, lo + mine) of a head
+  const long long total = all * p.num_kv_heads;
+  const long long s0 = total * cta / grid, s1 = total * (cta + 1) / grid;
+  if (tid == 0) {
+    range[0] = s0;
+    range[1] = s1;
+    range[2] = total;
+  }
+  if (all > 0 && s0 < total) {
+    const int h = (int)(s0 / all);
+    long long at = s0 - h * all - lo;
+    if (at >= 0 && at < mine) {
+      for (int b = b0; b < b1; ++b) {
+        const Seq s = load_seq(p, b, &bad);
+        const long long n = seq_steps(s, tok, p.causal);
+        if (at >= n) {
+          at -= n;
+          continue;
+        }
+        int t = 0;
+        for (;; ++t) {
+          const int w = tile_steps(s, t, tok, p.causal);
+          if (at < w) break;
+          at -= w;
+        }
+        *out = Place{h, b, t, (int)at, 0, all, s0 - at};
+        break;
+      }
+    }
+  }
+  __syncthreads();
+}
+
+// ------------------------------------------------------------- segments
+
+struct Segment {
+  int kvh, first, n, len, tile, b;
+  int top, tiles;  // key tiles top, top - 1, ..., top - tiles + 1; tiles < 0: no more segments
+  int slot;        // partial results' slot, or -1: the tile is whole
+};
+
+struct Aux {
+  uint64_t raw_full[kMaxUnits], raw_empty[kMaxUnits];
+  uint64_t full[4], empty[4];
+  uint64_t seg_full[4], seg_empty[4];
+  uint64_t prep[2];
+  uint64_t s[2], p[2], q, sums, done;
+  uint32_t tmem;
+  int fail;
+  int raw_bad[kMaxUnits];
+  Segment seg[4];
+  Place start;
+  long long range[3];
+};
+static_assert(sizeof(Aux) <= kAuxBytes, "Aux");
+
+// ------------------------------------------------------ dequantisation
+
+__device__ __forceinline__ uint32_t and_or(uint32_t a, uint32_t m, uint32_t o) { return (a & m) | o; }
+__device__ __forceinline__ __half2 as_h2(uint32_t v) { return *reinterpret_cast<__half2*>(&v); }
+__device__ __forceinline__ uint32_t as_u32(__half2 v) { return *reinterpret_cast<uint32_t*>(&v); }
+
+// A word of codes as fp16 integers, two per register: word halves give codes
+// (i, i + 4) of 8 four-bit or (i, i + 8) of 16 two-bit codes.  0x6400 | m is
+// the fp16 number 1024 + m, so a code in place at bit 2^k is (h - 1024) 2^-k,
+// exactly.
+template <int BITS>
+__device__ __forceinline__ void unpack_word(uint32_t w, __half2* c) {
+  const uint32_t w8 = w >> 8;
+  if (BITS == 4) {
+    const __half2 one = as_h2(0xe400e400u);                                     // -1024
+    const __half2 r16 = as_h2(0x2c002c00u), o16 = as_h2(0xd400d400u);           // 1/16, -64
+    c[0] = __hadd2(as_h2(and_or(w, 0x000f000fu, 0x64006400u)), one);
+    c[1] = __hfma2(as_h2(and_or(w, 0x00f000f0u, 0x64006400u)), r16, o16);
+    c[2] = __hadd2(as_h2(and_or(w8, 0x000f000fu, 0x64006400u)), one);
+    c[3] = __hfma2(as_h2(and_or(w8, 0x00f000f0u, 0x64006400u)), r16, o16);
+  } else {
+#pragma unroll
+    for (int hi = 0; hi < 2; ++hi) {
+      const uint32_t v = hi ? w8 : w;
+      c[4 * hi] = __hadd2(as_h2(and_or(v, 0x00030003u, 0x64006400u)), as_h2(0xe400e400u));
+      c[4 * hi + 1] = __hfma2(as_h2(and_or(v, 0x000c000cu, 0x64006400u)), as_h2(0x34003400u), as_h2(0xdc00dc00u));
+      c[4 * hi + 2] = __hfma2(as_h2(and_or(v, 0x00300030u, 0x64006400u)), as_h2(0x2c002c00u), as_h2(0xd400d400u));
+      c[4 * hi + 3] = __hfma2(as_h2(and_or(v, 0x00c000c0u, 0x64006400u)), as_h2(0x24002400u), as_h2(0xcc00cc00u));
+    }
+  }
+}
+// Operand position of element e within a word's block of codes, and back.
+template <int BITS>
+__host__ __device__ constexpr int position_of(int e) {
+  return BITS == 4 ? (e & ~7) + ((e & 3) << 1) + ((e >> 2) & 1) : (e & ~15) + ((e & 7) << 1) + ((e >> 3) & 1);
+}
+template <int BITS>
+__host__ __device__ constexpr int element_at(int i) {
+  return BITS == 4 ? (i & ~7) + ((i & 7) >> 1) + ((i & 1) << 2) : (i & ~15) + ((i & 15) >> 1) + ((i & 1) << 3);
+}
+
+// The block's scales and offsets into the table that the dequantising threads
+// read: checked (a group whose values would not fit fp16 has its scale
+// lowered to fit, one that is not finite is zeroed) and, where they belong to
+// columns, in operand order: col_major: [group][column] u16 scales, then
+// offsets; else [entry] (scale | offset << 16).
+template <int BITS>
+__device__ __forceinline__ void prepare_table(const uint16_t* s, const uint16_t* z, int nsz, bool by_column, bool value,
+                                              int D, int gshift, bool bad, unsigned char* table, uint32_t* dev_status) {
+  const int t = threadIdx.x & 127;
+  const float most = (float)((1 << BITS) - 1);
+  uint16_t* ts = reinterpret_cast<uint16_t*>(table);
+  uint16_t* tz = ts + nsz;
+  for (int e = t; e < nsz; e += 128) {
+    __half sh = __ushort_as_half(s[e]), zh = __ushort_as_half(z[e]);
+    const float sf = __half2float(sh), zf = __half2float(zh);
+    if (bad) {
+      sh = zh = __ushort_as_half(0);
+    } else if (!(fmaf(sf, most, zf) <= 65504.f) || !(zf >= -65504.f)) {
+      report(dev_status, KVQ_DEV_NONFINITE);
+      if (!isfinite(sf) || !isfinite(zf)) sh = zh = __ushort_as_half(0);
+      else sh = __float2half_rd((65504.f - zf) / most);
+    }
+    if (!by_column) {
+      reinterpret_cast<uint32_t*>(table)[e] = __half_as_ushort(sh) | (uint32_t)__half_as_ushort(zh) << 16;
+    } else {
+      int at;
+      if (!value) {  // K, channel-wise: entry group * D + channel
+        at = (e & ~15) + position_of<BITS>(e & 15);
+      } else {       // V, token-wise: entry token * (D / G) + group
+        const int gpt = D >> gshift, tok = e / gpt, g = e - tok * gpt;
+        at = g * kTile + position_of<BITS>(tok);
+      }
+      ts[at] = __half_as_ushort(sh);
+      tz[at] = __half_as_ushort(zh);
+    }
+  }
+}
+
+// One slot (part) of a K or V block: codes -> fp16 operand tile of NROWS rows
+// x kCols columns, 128-byte swizzled, 64 columns to a chunk.  128 threads.
+template <int BITS, int D, bool VALUE, bool BYCOL>
+__device__ __forceinline__ void dequant_part(const unsigned char* codes, const unsigned char* table, int nsz, int part,
+                                             int gshift, unsigned char* slot) {
+  constexpr int kRowsAll = VALUE ? D : kTile;            // rows of the packed block
+  constexpr int kNR = VALUE ? (D < 128 ? D : 128) : kTile;  // rows of the part
+  constexpr int kCols = VALUE ? kTile : (D < 128 ? D : 128);  // columns of the part
+  constexpr int kPer = 128 / BITS;                       // codes of a 16-byte piece
+  constexpr int kChunks = kCols / kPer;
+  constexpr int kWord = 32 / BITS;                       // codes of a word
+  const int t = threadIdx.x & 127;
+#pragma unroll
+  for (int i = 0; i < kNR * kChunks / 128; ++i) {
+    const int piece = t + 128 * i, row = piece % kNR, chunk = piece / kNR;
+    const int grow = row + (VALUE ? part * 128 : 0);
+    const int gchunk = chunk + (VALUE ? 0 : part * kChunks);
+    const uint4 v = *reinterpret_cast<const uint4*>(codes + ((size_t)gchunk * kRowsAll + grow) * 16);
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+    unsigned char* dst = slot + (chunk * kPer / 64) * (kNR * 128) + row * 128;
+    const int c16 = (chunk * kPer % 64) / 8, sw = row & 7;
+    uint32_t sz = 0;
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      const int col = gchunk * kPer + q * kWord;  // first column of the word
+      __half2 c[kWord / 2];
+      unpack_word<BITS>(w[q], c);
+      uint32_t x[kWord / 2];
+      if (BYCOL) {
+        // K: table row = token group of `row`; V: channel group of `row`
+        const int g = grow >> gshift, base = g * (VALUE ? kTile : D) + col;
+        const uint16_t* ts = reinterpret_cast<const uint16_t*>(table) + base;
+#pragma unroll
+        for (int hf = 0; hf < kWord / 8; ++hf) {
+          const uint4 s4 = *reinterpret_cast<const uint4*>(ts + 8 * hf);
+          const uint4 z4 = *reinterpret_cast<const uint4*>(ts + nsz + 8 * hf);
+          x[4 * hf] = as_u32(__hfma2(c[4 * hf], as_h2(s4.x), as_h2(z4.x)));
+          x[4 * hf + 1] = as_u32(__hfma2(c[4 * hf + 1], as_h2(s4.y), as_h2(z4.y)));
+          x[4 * hf + 2] = as_u32(__hfma2(c[4 * hf + 2], as_h2(s4.z), as_h2(z4.z)));
+          x[4 * hf + 3] = as_u32(__hfma2(c[4 * hf + 3], as_h2(s4.w), as_h2(z4.w)));
+        }
+      } else {
+        if (q == 0 || (BITS == 2 && q == 2)) {  // a group is at least 32 columns
+          const int g = col >> gshift;
+          const int e = VALUE ? g * D + grow : grow * (D >> gshift) + g;
+          sz = reinterpret_cast<const uint32_t*>(table)[e];
+        }
+        const __half2 s2 = as_h2(__byte_perm(sz, 0, 0x1010)), z2 = as_h2(__byte_perm(sz, 0, 0x3232));
+#pragma unroll
+        for (int k = 0; k < kWord / 2; ++k) x[k] = as_u32(__hfma2(c[k], s2, z2));
+      }
+#pragma unroll
+      for (int hf = 0; hf < kWord / 8; ++hf)
+        *reinterpret_cast<uint4*>(dst + (((c16 + q * (kWord / 8) + hf) ^ sw) << 4)) =
+            make_uint4(x[4 * hf], x[4 * hf + 1], x[4 * hf + 2], x[4 * hf + 3]);
+    }
+  }
+}
+
+// ------------------------------------------------------------- the kernel
+
+template <int BITS, int D, int NT>
+__global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const Params P) {
+  constexpr int kAhead = NT == 2 ? 1 : 2;             // score tiles issued ahead of their PV, per row tile
+  constexpr int kChunks = D / 64;                     // 64-channel chunks of a Q row
+  constexpr int kParts = D > 128 ? D / 128 : 1;       // slots of a K or V tile
+  constexpr int kSlotCh = kChunks / kParts;
+  constexpr int kSlot = slot_bytes(D), kSlots = slots_of(D, NT);
+  constexpr int kDq = dequant_groups(NT);             // dequantising warpgroups
+  constexpr int kSoftWarps = 4 * NT, kDqWarps = 4 * kDq;
+  static_assert(NT + kDq + 1 == kThreads / 128, "warpgroups");
+  const RowAttnParams& p = P.r;
+  extern __shared__ __align__(1024) unsigned char smem[];
+  unsigned char* q_s = smem;
+  unsigned char* ring = smem + q_bytes(D, NT);
+  Aux* aux = reinterpret_cast<Aux*>(ring + kSlots * kSlot);
+  unsigned char* tables = reinterpret_cast<unsigned char*>(aux) + kAuxBytes;  // [kDq][2]
+  unsigned char* raw = tables + kDq * 2 * P.table_bytes;
+  volatile int* fail = &aux->fail;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int tok_tile = kTile / p.gq, tok_cta = tok_tile * NT;
+  const uint64_t limit = (p.flags & KVQ_FLAG_TEST_STALL) ? 50ull * 1000 * 1000 : 2ull * 1000 * 1000 * 1000;
+  const int nsz = kBlockTokens * D >> P.gshift;
+
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // the merge may be launched; it waits for this grid
+  if (warp == 15 && lane == 0) {
+    for (int i = 0; i < P.units; ++i) {
+      mbar_init(&aux->raw_full[i], 1);
+      mbar_init(&aux->raw_empty[i], 4);
+    }
+    for (int i = 0; i < 4; ++i) {
+      mbar_init(&aux->full[i], 4);
+      mbar_init(&aux->empty[i], 1);
+      mbar_init(&aux->seg_full[i], 1);
+      mbar_init(&aux->seg_empty[i], kSoftWarps + kDqWarps + 2);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&aux->prep[i], 4);
+      mbar_init(&aux->s[i], 1);
+      mbar_init(&aux->p[i], 4);
+    }
+    mbar_init(&aux->q, kSoftWarps);
+    mbar_init(&aux->sums, 1);
+    mbar_init(&aux->done, 1);
+    aux->fail = 0;
+    fence_barrier_init();
+  }
+  __syncwarp();
+  if (warp == 14) {
+    tmem_alloc(&aux->tmem, 512);
+    tmem_relinquish();
+  }
+  // (the ring is not in use yet: the scan's scratch)
+  find_place<kThreads>(p, tok_cta, blockIdx.x, gridDim.x, reinterpret_cast<long long*>(ring), &aux->start, aux->range,
+                       blockIdx.x == 0);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = aux->tmem;
+  const long long s0 = aux->range[0], s1 = aux->range[1];
+
+  if (s1 > s0) {
+    auto wait = [&](uint64_t* bar, uint32_t parity) -> bool {
+      if (mbar_wait_bounded<true>(bar, parity, fail, limit)) return true;
+      *fail = 1;
+      return false;
+    };
+    // The next segment, read by every lane of a consuming warp.
+    auto next_segment = [&](int k, Segment& g) -> bool {
+      if (!__all_sync(0xffffffffu, wait(&aux->seg_full[k & 3], (k >> 2) & 1))) return false;
+      g = aux->seg[k & 3];
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&aux->seg_empty[k & 3]);
+      return g.tiles >= 0;
+    };
+
+    if (warp < kSoftWarps) {
+      // ------------------------------------------------------------ softmax
+      if (NT == 2) setmaxnreg_inc<184>();
+      else setmaxnreg_inc<208>();
+      const int i = warp >> 2, r = tid & 127;
+      const uint32_t lanes = (uint32_t)(warp & 3) << 21;
+      const uint32_t t_o = tmem + lanes + 256 + i * D;
+      int uses = 0;  // score tiles of this row tile so far
+      Segment g;
+      for (int k = 0; next_segment(k, g); ++k) {
+        const int tok0 = g.tile * tok_cta, ntok = min(tok_cta, g.n - tok0);
+        const int rows_i = max(0, min(tok_tile, ntok - i * tok_tile)) * p.gq;
+        const bool mine = r < rows_i, any = (warp & 3) * 32 < rows_i;
+        const int tok = tok0 + i * tok_tile + r / p.gq, head = g.kvh * p.gq + r % p.gq;
+        const int pos = g.len - g.n + tok;
+        // Q row -> fp16, channels in operand order.  bf16 rows are scaled by a
+        // power of two that brings the largest magnitude to [2^13, 2^14): eight
+        // significant bits down to 2^-30 of it, nothing overflows.
+        float c = p.scale_log2;
+        if (g.tiles > 0) {
+          const uint4* src = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p.q.data) +
+                                                            (long long)(g.first + tok) * p.q.st + head * p.q.sh);
+          float mul = 1.f;
+          if (mine && !p.fp16) {
+            uint32_t most = 0;
+#pragma unroll 8
+            for (int e = 0; e < D / 8; ++e) {
+              const uint4 v = src[e];
+              most = __vmaxu2(most, __vmaxu2(__vmaxu2(v.x & 0x7fff7fffu, v.y & 0x7fff7fffu),
+                                             __vmaxu2(v.z & 0x7fff7fffu, v.w & 0x7fff7fffu)));
+            }
+            const int ex = (int)(max(most & 0xffffu, most >> 16) >> 7);  // biased exponent
+            if (ex > 0 && ex < 255) {
+              const int up = min(13 + 127 - ex, 100);
+              mul = __uint_as_float((uint32_t)(up + 127) << 23);
+              c *= __uint_as_float((uint32_t)(127 - up) << 23);
+            }
+          }
+          if (any) {
+#pragma unroll 2
+            for (int e = 0; e < D / 16; ++e) {
+              float f[16];
+#pragma unroll
+              for (int hf = 0; hf < 2; ++hf) {
+                const uint4 v = mine ? src[2 * e + hf] : make_uint4(0u, 0u, 0u, 0u);
+                const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                  if (p.fp16) {
+                    const float2 h = __half22float2(as_h2(w[j]));
+                    f[8 * hf + 2 * j] = h.x;
+                    f[8 * hf + 2 * j + 1] = h.y;
+                  } else {
+                    f[8 * hf + 2 * j] = __uint_as_float(w[j] << 16) * mul;
+                    f[8 * hf + 2 * j + 1] = __uint_as_float(w[j] & 0xffff0000u) * mul;
+                  }
+                }
+              }
+              unsigned char* dst = q_s + (i * kChunks + e / 4) * 16384 + r * 128;
+#pragma unroll
+              for (int hf = 0; hf < 2; ++hf) {
+                uint32_t o[4];
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                  o[j] = rows::round2<true>(f[element_at<BITS>(8 * hf + 2 * j)], f[element_at<BITS>(8 * hf + 2 * j + 1)]);
+                *reinterpret_cast<uint4*>(dst + (((e % 4 * 2 + hf) ^ (r & 7)) << 4)) = make_uint4(o[0], o[1], o[2], o[3]);
+              }
+            }
+          }
+          fence_proxy_async_smem();
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&aux->q);
+        RowState st;
+        bool ok = true;
+        if (rows_i > 0) {
+          for (int j = 0; j < g.tiles && ok; ++j, ++uses) {
+            const int buf = NT == 2 ? i : uses & 1;
+            ok = __all_sync(0xffffffffu, wait(&aux->s[buf], (NT == 2 ? uses : uses >> 1) & 1));
+            if (!ok) break;
+            tc_fence_after();
+            if (any) {
+              const int seen = !mine ? kTile : (p.causal ? min(g.len, pos + 1) : g.len) - (g.top - j) * kTile;
+              rows::softmax_tile<D, true>(tmem + lanes + 128 * buf, t_o, c, seen, j == 0, st,
+                                          [](int x) { return element_at<BITS>(x); },
+                                          [&] {
+                                            if (NT == 1) {
+                                              wait(&aux->sums, (uses - 1) & 1);
+                                              __syncwarp();
+                                              tc_fence_after();
+                                            }
+                                          });
+            }
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&aux->p[buf]);
+          }
+        }
+        ok = ok && __all_sync(0xffffffffu, wait(&aux->done, k & 1));
+        if (!ok) break;
+        if (any) {
+          tc_fence_after();
+          const bool seen_any = st.l > 0.f || isnan(st.l);
+          const float inv = seen_any ? 1.f / st.l : 0.f;
+          const float lse2 = seen_any ? st.m * c + log2f(st.l) - rows::shift_log2<true>() : -INFINITY;
+          const long long row = (long long)(g.first + tok) * p.num_q_heads + head;
+          const size_t prow = (size_t)max(g.slot, 0) * (NT * kTile) + i * kTile + r;
+#pragma unroll
+          for (int cc = 0; cc < D / 32; ++cc) {
+            uint32_t o[32];
+            tmem_ld_32x32b_x32(t_o + 32 * cc, o);
+            tc_wait_ld();
+            if (!mine) continue;
+            float x[32];
+#pragma unroll
+            for (int e = 0; e < 32; ++e) x[e] = seen_any ? __uint_as_float(o[e]) * inv : 0.f;
+            if (g.slot >= 0) {
+              float4* dst = reinterpret_cast<float4*>(P.part_o + prow * D + 32 * cc);
+#pragma unroll
+              for (int e = 0; e < 8; ++e) dst[e] = make_float4(x[4 * e], x[4 * e + 1], x[4 * e + 2], x[4 * e + 3]);
+            } else {
+              uint4* dst = reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.out) + row * D + 32 * cc);
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                uint32_t w[4];
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                  w[j] = p.fp16 ? rows::round2<true>(x[8 * e + 2 * j], x[8 * e + 2 * j + 1])
+                                : rows::round2<false>(x[8 * e + 2 * j], x[8 * e + 2 * j + 1]);
+                dst[e] = make_uint4(w[0], w[1], w[2], w[3]);
+              }
+            }
+          }
+          if (mine) {
+            if (g.slot >= 0) P.part_lse[prow] = lse2;
+            else if (p.lse != nullptr) p.lse[row] = lse2 * 0.6931471805599453f;
+          }
+          tc_fence_before();  // the accumulators are read before the next segment's products
+        }
+      }
+    } else if (warp < kSoftWarps + kDqWarps) {
+      // -------------------------------------------------- dequantisation
+      if (NT == 2) setmaxnreg_dec<88>();
+      else setmaxnreg_dec<104>();
+      const int me = (warp - kSoftWarps) >> 2;  // this warpgroup takes units me, me + kDq, ...
+      int u = 0, did = 0;
+      bool ok = true;
+      auto unit = [&](bool value) {  // the next K or V block
+        if (ok && u % kDq == me) {
+          const int slot_r = u % P.units;
+          unsigned char* src = raw + slot_r * P.unit_bytes;
+          unsigned char* table = tables + (me * 2 + (did & 1)) * P.table_bytes;
+          ok = __all_sync(0xffffffffu, wait(&aux->raw_full[slot_r], (u / P.units) & 1));
+          const bool by_column = value ? p.v_scheme == KVQ_TOKENWISE : p.k_scheme == KVQ_CHANNELWISE;
+          if (ok) {
+            const uint16_t* s = reinterpret_cast<const uint16_t*>(src + kBlockTokens * D * BITS / 8);
+            prepare_table<BITS>(s, s + nsz, nsz, by_column, value, D, P.gshift, aux->raw_bad[slot_r] != 0, table,
+                                p.dev_status);
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&aux->prep[me]);
+            ok = __all_sync(0xffffffffu, wait(&aux->prep[me], did & 1));
+          }
+          for (int part = 0; part < kParts && ok; ++part) {
+            const int n = u * kParts + part, sl = n % kSlots, round = n / kSlots;
+            if (round > 0) ok = __all_sync(0xffffffffu, wait(&aux->empty[sl], (round - 1) & 1));
+            if (!ok) break;
+            unsigned char* dst = ring + sl * kSlot;
+            if (value) {
+              if (by_column) dequant_part<BITS, D, true, true>(src, table, nsz, part, P.gshift, dst);
+              else dequant_part<BITS, D, true, false>(src, table, nsz, part, P.gshift, dst);
+            } else {
+              if (by_column) dequant_part<BITS, D, false, true>(src, table, nsz, part, P.gshift, dst);
+              else dequant_part<BITS, D, false, false>(src, table, nsz, part, P.gshift, dst);
+            }
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&aux->full[sl]);
+          }
+          if (ok && lane == 0) mbar_arrive(&aux->raw_empty[slot_r]);
+          ++did;
+        }
+        ++u;
+      };
+      Segment g;
+      for (int k = 0; ok && next_segment(k, g); ++k) {
+        for (int j = -kAhead; j < g.tiles && ok; ++j) {
+#pragma unroll 1
+          for (int v = 1; v >= 0; --v) {
+            if (v == 1 && j >= 0) unit(true);
+            if (v == 0 && j + kAhead < g.tiles) unit(false);
+          }
+        }
+      }
+    } else {
+      if (NT == 2) setmaxnreg_dec<56>();
+      else setmaxnreg_dec<96>();
+      if (warp == 12) {
+        // ---------------------------------------------------------- copies
+        int u = 0;
+        bool ok = true;
+        Segment g;
+        for (int k = 0; ok && next_segment(k, g); ++k) {
+          int base = 0x7fffffff, ids = 0;  // page ids of key tiles base ... base + 31, one per lane
+          auto page_of = [&](int j) {
+            if (j < base || j >= base + 32) {
+              base = max(0, j - 29);  // K runs up to two tiles ahead (below) of V
+              const int t = min(base + lane, p.max_blocks - 1);
+              ids = p.page_table ? p.page_table[(size_t)g.b * p.max_blocks + t] : g.b * p.max_blocks + t;
+            }
+            return __shfl_sync(0xffffffffu, ids, j - base);
+          };
+          auto unit = [&](bool value, int j) {
+            const int sl = u % P.units, round = u / P.units;
+            const int page = page_of(j);
+            if (round > 0) ok = __all_sync(0xffffffffu, wait(&aux->raw_empty[sl], (round - 1) & 1));
+            const bool stall = (p.flags & KVQ_FLAG_TEST_STALL) && s0 == 0 && u == 0;  // test hook: the first is withheld
+            if (ok && lane == 0 && !stall) {
+              const bool bad = page < 0 || page >= p.num_pages;
+              if (bad) report(p.dev_status, KVQ_DEV_BAD_PAGE);
+              aux->raw_bad[sl] = bad;
+              const size_t blk = (size_t)(bad ? 0 : page) * p.num_kv_heads + g.kvh;
+              constexpr int kCodes = kBlockTokens * D * BITS / 8;
+              unsigned char* dst = raw + sl * P.unit_bytes;
+              mbar_arrive_expect_tx(&aux->raw_full[sl], kCodes + nsz * 4);
+              bulk_g2s(dst, (value ? p.v_codes : p.k_codes) + blk * kCodes, kCodes, &aux->raw_full[sl]);
+              bulk_g2s(dst + kCodes, (value ? p.v_scale : p.k_scale) + blk * nsz, nsz * 2, &aux->raw_full[sl]);
+              bulk_g2s(dst + kCodes + nsz * 2, (value ? p.v_zero : p.k_zero) + blk * nsz, nsz * 2, &aux->raw_full[sl]);
+            }
+            if (ok) ++u;
+          };
+          for (int j = -kAhead; j < g.tiles && ok; ++j) {
+#pragma unroll 1
+            for (int v = 1; v >= 0 && ok; --v) {
+              if (v == 1 && j >= 0) unit(true, g.top - j);
+              if (v == 0 && j + kAhead < g.tiles) unit(false, g.top - j - kAhead);
+            }
+          }
+        }
+        // copies in flight land before this CTA's shared memory is given up
+        for (int n = u > P.units ? u - P.units : 0; n < u; ++n) {
+          if ((p.flags & KVQ_FLAG_TEST_STALL) && s0 == 0 && n == 0) continue;
+          mbar_wait_bounded<true>(&aux->raw_full[n % P.units], (n / P.units) & 1, nullptr, limit);
+        }
+      } else if (warp == 13) {
+        // -------------------------------------------------------- products
+        constexpr uint32_t idesc_s = make_idesc(0, 0, 0, 0, 128, 128);
+        constexpr int kN = D < 128 ? D : 128;
+        constexpr uint32_t idesc_o = make_idesc(0, 0, 0, 0, 128, kN);
+        const uint32_t q_a = smem_u32(q_s), ring_a = smem_u32(ring);
+        auto scores = [&](int i, int buf, int n) {  // n: running number of the K tile's first slot
+#pragma unroll
+          for (int kk = 0; kk < D / 16; ++kk) {
+            const int cc = kk / 4, sl = (n + cc / kSlotCh) % kSlots;
+            mma_f16_ss(tmem + 128 * buf, make_smem_desc_sw128(q_a + (i * kChunks + cc) * 16384 + (kk % 4) * 32, 0),
+                       make_smem_desc_sw128(ring_a + sl * kSlot + (cc % kSlotCh) * 16384 + (kk % 4) * 32, 0), idesc_s,
+                       kk > 0);
+          }
+        };
+        auto values = [&](int i, int buf, int n, bool add) {
+#pragma unroll
+          for (int part = 0; part < kParts; ++part) {
+            const int sl = (n + part) % kSlots;
+#pragma unroll
+            for (int kk = 0; kk < kTile / 16; ++kk)
+              mma_f16_ts(tmem + 256 + i * D + part * 128, tmem + 128 * buf + 8 * kk,
+                         make_smem_desc_sw128(ring_a + sl * kSlot + (kk / 4) * (kN * 128) + (kk % 4) * 32, 0), idesc_o,
+                         add || kk > 0);
+          }
+        };
+        int n = 0;  // slots taken so far
+        int use0 = 0, use1 = 0;  // score tiles per buffer (two row tiles) or in all (one)
+        bool ok = true;
+        auto take = [&]() {
+          const int at = n;
+          for (int part = 0; part < kParts && ok; ++part, ++n) ok = wait(&aux->full[n % kSlots], (n / kSlots) & 1);
+          return at;
+        };
+        auto release = [&](int at) {
+          for (int part = 0; part < kParts; ++part) tc_commit(&aux->empty[(at + part) % kSlots]);
+        };
+        Segment g;
+        for (int k = 0; ok && next_segment(k, g); ++k) {
+          if (lane == 0) {
+            const int ntok = min(tok_cta, g.n - g.tile * tok_cta);
+            const int act = NT == 2 && ntok > tok_tile ? 2 : 1;
+            ok = wait(&aux->q, k & 1);
+            tc_fence_after();
+            int issued = 0;
+#pragma unroll 1
+            for (int j = 0; j < kAhead && j < g.tiles && ok; ++j) {
+              const int ks = take();
+              if (!ok) break;
+#pragma unroll 1
+              for (int i = 0; i < act; ++i) {
+                const int buf = NT == 2 ? i : (use0 + j) & 1;
+                scores(i, buf, ks);
+                tc_commit(&aux->s[buf]);
+              }
+              release(ks);
+              ++issued;
+            }
+#pragma unroll 1
+            for (int j = 0; j < g.tiles && ok; ++j) {
+              const int vs = take();
+              const bool more = j + kAhead < g.tiles;
+              int ks = 0;
+#pragma unroll 1
+              for (int i = 0; i < act && ok; ++i) {
+                const int use = NT == 2 && i == 1 ? use1 : use0;
+                const int buf = NT == 2 ? i : use & 1;
+                ok = wait(&aux->p[buf], (NT == 2 ? use : use >> 1) & 1);
+                if (!ok) break;
+                tc_fence_after();
+                values(i, buf, vs, j > 0);
+                if (NT == 1) tc_commit(&aux->sums);
+                if (i == act - 1) release(vs);
+                if (more) {
+                  if (i == 0) ks = take();  // after the first PV: with head dim 256 K needs slots that V gives up
+                  if (!ok) break;
+                  scores(i, buf, ks);
+                  tc_commit(&aux->s[buf]);
+                }
+                if (NT == 2 && i == 1) ++use1;
+                else ++use0;
+              }
+              if (ok && more) release(ks);
+            }
+            tc_commit(&aux->done);
+            mbar_wait_bounded<true>(&aux->done, k & 1, nullptr, limit);  // also: nothing in flight at the end
+          }
+          ok = __shfl_sync(0xffffffffu, (int)ok, 0) != 0;
+        }
+        __syncwarp();
+      } else if (warp == 14 && lane == 0) {
+        // ---------------------------------------------------------- segments
+        Place at = aux->start;
+        uint32_t bad = 0;
+        Seq s = load_seq(p, at.b, &bad);
+        long long left = s1 - s0;
+        bool first = true, ok = true;
+        for (int k = 0; ok; ++k) {
+          if (k >= 4) ok = wait(&aux->seg_empty[k & 3], ((k >> 2) - 1) & 1);
+          if (!ok) break;
+          Segment g;
+          g.tiles = -1;
+          if (left > 0) {
+            const int w = key_tiles(s, at.t, tok_cta, p.causal), steps = max(1, w);
+            const int take = (int)min(left, (long long)(steps - at.x));
+            g.kvh = at.h; g.first = s.first; g.n = s.n; g.len = s.len; g.tile = at.t; g.b = at.b;
+            g.top = w - 1 - at.x;
+            g.tiles = min(take, w);  // 0: nothing to see
+            g.slot = at.x == 0 && take == steps ? -1 : 2 * (int)blockIdx.x + (first ? 0 : 1);
+            left -= take;
+            first = false;
+          }
+          aux->seg[k & 3] = g;
+          mbar_arrive(&aux->seg_full[k & 3]);
+          if (g.tiles < 0) break;
+          if (left > 0) {  // the next tile with rows
+            at.x = 0;
+            ++at.t;
+            while (at.t * tok_cta >= s.n) {
+              at.t = 0;
+              if (++at.b == p.batch) { at.b = 0; ++at.h; }
+              s = load_seq(p, at.b, &bad);
+            }
+          }
+        }
+      }
+    }
+  }
+  __syncwarp();
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 14) tmem_dealloc(tmem, 512);
+  if (tid == 0 && aux->fail) report(p.dev_status, KVQ_DEV_TIMEOUT);
+}
+
+template <int BITS, int D, int NT>
+cudaError_t launch_instance(const Params& p, int grid, size_t smem, cudaStream_t stream) {
+  cudaError_t e =
+      cudaFuncSetAttribute(chunk_kernel<BITS, D, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  if (e != cudaSuccess) return e;
+  chunk_kernel<BITS, D, NT><<<grid, kThreads, smem, stream>>>(p);
+  return cudaGetLastError();
+}
+
+}  // namespace chunk
+}  // namespace kvq

@@ -6,7 +6,7 @@
 #include <cmath>
 #include <cstdint>
 
-#include "attn_rows.h"
+#include "chunk_attn.h"
 
 namespace kvq {
 namespace {
@@ -131,7 +131,7 @@ KVQ_API kvq_status kvq_chunk_workspace_size(const kvq_chunk_desc* d, size_t* byt
   kvq_status s = check_chunk(d);
   if (s != KVQ_OK) return s;
   if (bytes == nullptr) return KVQ_ERR_INVALID_ARG;
-  *bytes = 256;
+  *bytes = chunk_plan(d->cache.head_dim, d->batch, d->total_tokens, d->num_q_heads, d->cache.num_kv_heads).total;
   return KVQ_OK;
 }
 
@@ -151,10 +151,9 @@ KVQ_API kvq_status kvq_chunk_attn(const kvq_chunk_desc* d, const kvq_rows* q, co
   for (const void* ptr : words)
     if (!aligned4(ptr)) return KVQ_ERR_INVALID_ARG;
   if (page_table == nullptr && (long long)d->batch * d->max_blocks > d->cache.num_pages) return KVQ_ERR_INVALID_ARG;
-  size_t need = 0;
-  s = kvq_chunk_workspace_size(d, &need);
-  if (s != KVQ_OK) return s;
-  if (workspace == nullptr || (reinterpret_cast<uintptr_t>(workspace) & 255u) != 0 || workspace_bytes < need)
+  const ChunkPlan plan =
+      chunk_plan(d->cache.head_dim, d->batch, d->total_tokens, d->num_q_heads, d->cache.num_kv_heads);
+  if (workspace == nullptr || (reinterpret_cast<uintptr_t>(workspace) & 255u) != 0 || workspace_bytes < plan.total)
     return KVQ_ERR_WORKSPACE;
   s = check_device(nullptr);
   if (s != KVQ_OK) return s;
@@ -169,7 +168,7 @@ KVQ_API kvq_status kvq_chunk_attn(const kvq_chunk_desc* d, const kvq_rows* q, co
   p.k_scheme = d->cache.k_scheme; p.v_scheme = d->cache.v_scheme; p.max_blocks = d->max_blocks;
   p.num_pages = d->cache.num_pages; p.causal = d->causal; p.fp16 = d->dtype == KVQ_FP16;
   p.scale_log2 = scale_log2(d->sm_scale, p.head_dim); p.flags = d->flags;
-  return launch_row_attn_simple(p, true, static_cast<cudaStream_t>(stream)) == cudaSuccess ? KVQ_OK : KVQ_ERR_CUDA;
+  return launch_chunk_attn(p, plan, workspace, static_cast<cudaStream_t>(stream)) == cudaSuccess ? KVQ_OK : KVQ_ERR_CUDA;
 }
 
 }  // extern "C"

@@ -252,3 +252,16 @@ def test_many_sequences():
     total = [n + int(x) for n, x in zip(new, torch.randint(0, 140, (700,), generator=g))]
     s = Setup(2, (0, 1), 64, 64, 1, 4, new=new, total=total, seed=16)
     s.check(only=[0, 1, 31, 32, 33, 64, 500, 698, 699])
+
+
+@pytest.mark.parametrize("dim", [64, 128, 256])
+@pytest.mark.parametrize("new", [(3, 2), (400, 300)])
+def test_withheld_copies_time_out(dim, new):
+    """A copy that never arrives ends in a status, not in a hang; the next call
+    is right again."""
+    import bit_quantized_kv_decode_gb300 as kvq
+    s = Setup(4, (1, 0), dim, 64, 2, 4, new=new, total=(900, 700), seed=17)
+    s.call(flags=kvq.FLAG_TEST_STALL)
+    assert int(s.status.item()) & kvq.DEV_TIMEOUT
+    s.status.zero_()
+    s.check()
