@@ -20,6 +20,21 @@ namespace rows {
 constexpr int kTile = 128;          // rows of a tile, and keys of a tile
 constexpr float kRescaleLog2 = 8.f;  // a row's reference maximum moves when its scores exceed it by this (log2 units)
 
+// Waits for a barrier's phase, at most `tries` times a suspended try (20 us at
+// most each, counted and not timed: the waits are in every role's inner loop,
+// and their code has to stay small), or until *fail is set; sets *fail when it
+// gives up.
+__device__ __forceinline__ bool bounded_wait(uint64_t* bar, uint32_t parity, volatile int* fail, int tries) {
+  if (mbar_try_wait(bar, parity)) return true;  // (a first try without the hint: 7% on long prompts)
+  while (!mbar_try_wait_sleep(bar, parity, 20000u))
+    if (*fail != 0 || --tries < 0) {
+      *fail = 1;
+      return false;
+    }
+  return true;
+}
+constexpr int kTries = 1 << 21, kTestTries = 1 << 12;  // under the stall flag: a test's patience
+
 // fp32 pairs in one register pair: the FMA pipe takes both at once.
 __device__ __forceinline__ uint64_t pair(float a, float b) {
   uint64_t r;
@@ -105,19 +120,18 @@ template <int D, bool FP16, class Perm, class Ready>
 __device__ __forceinline__ void softmax_tile(uint32_t t_s, uint32_t t_o, float c, int seen, bool first, RowState& st,
                                              Perm perm, Ready sums_ready) {
   uint32_t s[kTile];
+  float mx[4];
 #pragma unroll
-  for (int i = 0; i < 4; ++i) tmem_ld_32x32b_x32(t_s + 32 * i, s + 32 * i);
+  for (int i = 0; i < 4; ++i) mx[i] = tmem_ld_max_32x32b_x32(t_s + 32 * i, s + 32 * i);
   tc_wait_ld();
-  if (__any_sync(0xffffffffu, seen < kTile)) {
+  if (__builtin_expect(__any_sync(0xffffffffu, seen < kTile), 0)) {  // hidden scores: out of the row and of its maximum
 #pragma unroll
-    for (int i = 0; i < kTile; ++i) s[i] = i < seen ? s[i] : 0xff800000u;
-  }
-  float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+    for (int i = 0; i < 4; ++i) mx[i] = -INFINITY;
 #pragma unroll
-  for (int i = 0; i < kTile; i += 8) {
-#pragma unroll
-    for (int j = 0; j < 4; ++j)
-      mx[j] = fmaxf(fmaxf(mx[j], __uint_as_float(s[i + 2 * j])), __uint_as_float(s[i + 2 * j + 1]));
+    for (int i = 0; i < kTile; ++i) {
+      s[i] = i < seen ? s[i] : 0xff800000u;
+      mx[i & 3] = fmaxf(mx[i & 3], __uint_as_float(s[i]));
+    }
   }
   const float mt = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
   const bool grow = (mt - st.m) * c > kRescaleLog2;  // also the row's first finite score (m = -inf)
@@ -127,7 +141,7 @@ __device__ __forceinline__ void softmax_tile(uint32_t t_s, uint32_t t_o, float c
     st.m = mt;
     st.l *= alpha;
   }
-  if (!first && __any_sync(0xffffffffu, grow)) {
+  if (__builtin_expect(!first && __any_sync(0xffffffffu, grow), 0)) {
     sums_ready();
     scale_rows<D>(t_o, alpha);
   }
@@ -154,6 +168,31 @@ __device__ __forceinline__ void softmax_tile(uint32_t t_s, uint32_t t_o, float c
   unpair(add2(sum0, sum1), x, y);
   st.l += x + y;
   tc_wait_st();
+}
+
+// The MMAs of one product of 128-row tiles, issued by one thread.  (Loops and
+// not straight-line code: the issuing thread runs through it alone, and each
+// line of code that it has to fetch delays the tensor cores.)
+//
+// S = Q K^T: `chunks` chunks of 64 channels of Q (16 KB each) and K; a, b: low
+// descriptor words.
+template <int CHUNKS>
+__device__ __forceinline__ void issue_scores(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc, bool add) {
+#pragma unroll 1
+  for (int c = 0; c < CHUNKS; ++c, a += 1024, b += 1024) {
+#pragma unroll
+    for (int k = 0; k < 4; ++k) mma_f16_ss_sw128(d, a + 2 * k, b + 2 * k, idesc, add || c + k > 0);
+  }
+}
+// O += P V: P (tensor-memory columns from a) times V in 8 steps of 16 tokens,
+// four steps `step` descriptor units apart and then `half` on to the next four.
+__device__ __forceinline__ void issue_values(uint32_t d, uint32_t a, uint32_t b, uint32_t step, uint32_t half,
+                                             uint32_t idesc, bool add) {
+#pragma unroll 1
+  for (int c = 0; c < 2; ++c, a += 32, b += half) {
+#pragma unroll
+    for (int k = 0; k < 4; ++k) mma_f16_ts_sw128(d, a + 8 * k, b + step * k, idesc, add || c + k > 0);
+  }
 }
 
 // lse in natural units.

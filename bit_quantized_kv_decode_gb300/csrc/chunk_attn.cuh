@@ -243,7 +243,7 @@ __device__ __forceinline__ void dequant_part(const unsigned char* codes, const u
   constexpr int kChunks = kCols / kPer;
   constexpr int kWord = 32 / BITS;                       // codes of a word
   const int t = threadIdx.x & 127;
-#pragma unroll
+#pragma unroll 1
   for (int i = 0; i < kNR * kChunks / 128; ++i) {
     const int piece = t + 128 * i, row = piece % kNR, chunk = piece / kNR;
     const int grow = row + (VALUE ? part * 128 : 0);
@@ -312,7 +312,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const Params P) {
   volatile int* fail = &aux->fail;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int tok_tile = kTile / p.gq, tok_cta = tok_tile * NT;
-  const uint64_t limit = (p.flags & KVQ_FLAG_TEST_STALL) ? 50ull * 1000 * 1000 : 2ull * 1000 * 1000 * 1000;
+  const int tries = (p.flags & KVQ_FLAG_TEST_STALL) ? rows::kTestTries : rows::kTries;
   const int nsz = kBlockTokens * D >> P.gshift;
 
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // the merge may be launched; it waits for this grid
@@ -354,9 +354,11 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const Params P) {
 
   if (s1 > s0) {
     auto wait = [&](uint64_t* bar, uint32_t parity) -> bool {
-      if (mbar_wait_bounded<true>(bar, parity, fail, limit)) return true;
-      *fail = 1;
-      return false;
+      return rows::bounded_wait(bar, parity, fail, tries);
+    };
+    // The same after a failure too: what is in flight must land.
+    auto drain = [&](uint64_t* bar, uint32_t parity) {
+      for (int i = 0; i < tries && !mbar_try_wait_sleep(bar, parity, 20000u); ++i) {}
     };
     // The next segment, read by every lane of a consuming warp.
     auto next_segment = [&](int k, Segment& g) -> bool {
@@ -554,10 +556,8 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const Params P) {
       for (int k = 0; ok && next_segment(k, g); ++k) {
         for (int j = -kAhead; j < g.tiles && ok; ++j) {
 #pragma unroll 1
-          for (int v = 1; v >= 0; --v) {
-            if (v == 1 && j >= 0) unit(true);
-            if (v == 0 && j + kAhead < g.tiles) unit(false);
-          }
+          for (int v = 1; v >= 0; --v)
+            if (v ? j >= 0 : j + kAhead < g.tiles) unit(v != 0);
         }
       }
     } else {
@@ -599,16 +599,14 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const Params P) {
           };
           for (int j = -kAhead; j < g.tiles && ok; ++j) {
 #pragma unroll 1
-            for (int v = 1; v >= 0 && ok; --v) {
-              if (v == 1 && j >= 0) unit(true, g.top - j);
-              if (v == 0 && j + kAhead < g.tiles) unit(false, g.top - j - kAhead);
-            }
+            for (int v = 1; v >= 0 && ok; --v)
+              if (v ? j >= 0 : j + kAhead < g.tiles) unit(v != 0, g.top - (v ? j : j + kAhead));
           }
         }
         // copies in flight land before this CTA's shared memory is given up
         for (int n = u > P.units ? u - P.units : 0; n < u; ++n) {
           if ((p.flags & KVQ_FLAG_TEST_STALL) && s0 == 0 && n == 0) continue;
-          mbar_wait_bounded<true>(&aux->raw_full[n % P.units], (n / P.units) & 1, nullptr, limit);
+          drain(&aux->raw_full[n % P.units], (n / P.units) & 1);
         }
       } else if (warp == 13) {
         // -------------------------------------------------------- products
@@ -617,24 +615,17 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const Params P) {
         constexpr uint32_t idesc_o = make_idesc(0, 0, 0, 0, 128, kN);
         const uint32_t q_a = smem_u32(q_s), ring_a = smem_u32(ring);
         auto scores = [&](int i, int buf, int n) {  // n: running number of the K tile's first slot
-#pragma unroll
-          for (int kk = 0; kk < D / 16; ++kk) {
-            const int cc = kk / 4, sl = (n + cc / kSlotCh) % kSlots;
-            mma_f16_ss(tmem + 128 * buf, make_smem_desc_sw128(q_a + (i * kChunks + cc) * 16384 + (kk % 4) * 32, 0),
-                       make_smem_desc_sw128(ring_a + sl * kSlot + (cc % kSlotCh) * 16384 + (kk % 4) * 32, 0), idesc_s,
-                       kk > 0);
-          }
+#pragma unroll 1
+          for (int part = 0; part < kParts; ++part)
+            rows::issue_scores<kSlotCh>(tmem + 128 * buf,
+                                        make_desc_sw128_lo(q_a + (i * kChunks + part * kSlotCh) * 16384, 0),
+                                        make_desc_sw128_lo(ring_a + (n + part) % kSlots * kSlot, 0), idesc_s, part > 0);
         };
         auto values = [&](int i, int buf, int n, bool add) {
-#pragma unroll
-          for (int part = 0; part < kParts; ++part) {
-            const int sl = (n + part) % kSlots;
-#pragma unroll
-            for (int kk = 0; kk < kTile / 16; ++kk)
-              mma_f16_ts(tmem + 256 + i * D + part * 128, tmem + 128 * buf + 8 * kk,
-                         make_smem_desc_sw128(ring_a + sl * kSlot + (kk / 4) * (kN * 128) + (kk % 4) * 32, 0), idesc_o,
-                         add || kk > 0);
-          }
+#pragma unroll 1
+          for (int part = 0; part < kParts; ++part)  // V rows are channels: 64 tokens to a chunk of kN rows
+            rows::issue_values(tmem + 256 + i * D + part * 128, tmem + 128 * buf,
+                               make_desc_sw128_lo(ring_a + (n + part) % kSlots * kSlot, 0), 2, kN * 8, idesc_o, add);
         };
         int n = 0;  // slots taken so far
         int use0 = 0, use1 = 0;  // score tiles per buffer (two row tiles) or in all (one)
@@ -695,7 +686,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const Params P) {
               if (ok && more) release(ks);
             }
             tc_commit(&aux->done);
-            mbar_wait_bounded<true>(&aux->done, k & 1, nullptr, limit);  // also: nothing in flight at the end
+            drain(&aux->done, k & 1);  // also: nothing in flight at the end
           }
           ok = __shfl_sync(0xffffffffu, (int)ok, 0) != 0;
         }

@@ -270,11 +270,11 @@ prompt_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__
     // the first `mend` tiles of the walk hold tokens that some row must not see
     const int clean = p.causal ? (tok0 + 1) / kTile : n / kTile;  // key tiles below this are seen whole by every row
     const int mend = tiles - min(clean, tiles);
-    const uint64_t limit = (p.flags & KVQ_FLAG_TEST_STALL) ? 50ull * 1000 * 1000 : 2ull * 1000 * 1000 * 1000;
-    auto wait = [&](uint64_t* bar, uint32_t parity) -> bool {
-      if (mbar_wait_bounded<true>(bar, parity, fail, limit)) return true;
-      *fail = 1;
-      return false;
+    const int tries = (p.flags & KVQ_FLAG_TEST_STALL) ? kTestTries : kTries;
+    auto wait = [&](uint64_t* bar, uint32_t parity) { return bounded_wait(bar, parity, fail, tries); };
+    // the same after a failure too: what is in flight must land
+    auto drain = [&](uint64_t* bar, uint32_t parity) {
+      for (int i = 0; i < tries && !mbar_try_wait_sleep(bar, parity, 20000u); ++i) {}
     };
 
     // Registers: 384 threads x 168 at launch; the softmax warpgroups take 208
@@ -334,8 +334,8 @@ prompt_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__
       // copies in flight land before this CTA's shared memory is given up
       const int from = issued > Sh::kSlots ? issued - Sh::kSlots : 0;
       for (int k = from; k < issued; ++k)
-        mbar_wait_bounded<true>(&aux->full[k % Sh::kSlots], (k / Sh::kSlots) & 1, nullptr, limit);
-      mbar_wait_bounded<true>(&aux->q, 0, nullptr, limit);
+        drain(&aux->full[k % Sh::kSlots], (k / Sh::kSlots) & 1);
+      drain(&aux->q, 0);
     } else if (warp == 9) {
       // ------------------------------------------------------------ products
       if (lane == 0) {
@@ -348,26 +348,20 @@ prompt_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__
         bool ok = wait(&aux->q, 0);
         // S of row tile i <- Q_i K^T with K in the slots from `sl`
         auto scores = [&](int i, int buf, int sl) {
-          const uint32_t d = tmem + 128 * buf;
-#pragma unroll
-          for (int k = 0; k < D / 16; ++k) {
-            const int c = k / 4, part = c / Sh::kSlotCh;
-            int s = sl + part;
-            if (s >= Sh::kSlots) s -= Sh::kSlots;
-            mma_f16_ss(d, make_smem_desc_sw128(q_a + (i * Sh::kChunks + c) * 16384 + (k % 4) * 32, 0),
-                       make_smem_desc_sw128(ring_a + s * Sh::kSlotBytes + (c % Sh::kSlotCh) * 16384 + (k % 4) * 32, 0),
-                       idesc_s, k > 0);
+#pragma unroll 1
+          for (int part = 0; part < Sh::kParts; ++part) {
+            issue_scores<Sh::kSlotCh>(tmem + 128 * buf,
+                                      make_desc_sw128_lo(q_a + (i * Sh::kChunks + part * Sh::kSlotCh) * 16384, 0),
+                                      make_desc_sw128_lo(ring_a + sl * Sh::kSlotBytes, 0), idesc_s, part > 0);
+            if (++sl == Sh::kSlots) sl = 0;
           }
         };
         auto values = [&](int i, int buf, int sl, bool add) {
-#pragma unroll
-          for (int part = 0; part < Sh::kParts; ++part) {
-            int s = sl + part;
-            if (s >= Sh::kSlots) s -= Sh::kSlots;
-#pragma unroll
-            for (int k = 0; k < kTile / 16; ++k)
-              mma_f16_ts(tmem + 256 + i * D + part * 128, tmem + 128 * buf + 8 * k,
-                         make_smem_desc_sw128(ring_a + s * Sh::kSlotBytes + k * 2048, 16384), idesc_o, add || k > 0);
+#pragma unroll 1
+          for (int part = 0; part < Sh::kParts; ++part) {  // V rows are tokens: 16 of them are 2 KB on
+            issue_values(tmem + 256 + i * D + part * 128, tmem + 128 * buf,
+                         make_desc_sw128_lo(ring_a + sl * Sh::kSlotBytes, 16384), 128, 512, idesc_o, add);
+            if (++sl == Sh::kSlots) sl = 0;
           }
         };
         auto take = [&](int& sl) {  // the next tile's slots, loaded
@@ -419,7 +413,7 @@ prompt_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__
           if (ok && more) release(ks);
         }
         tc_commit(&aux->done);
-        mbar_wait_bounded<true>(&aux->done, 0, nullptr, limit);  // nothing in flight when tensor memory is freed
+        drain(&aux->done, 0);  // nothing in flight when tensor memory is freed
       }
       __syncwarp();
     }
