@@ -1,0 +1,469 @@
+// Quantise and append a chunk of new tokens to the packed K and V caches.
+//
+// One CTA per (block touched, KV head, 128-channel slab, K or V); sequence b
+// touches blocks seq_lens[b] / 128 to (seq_lens[b] + n - 1) / 128.  The tile
+// (128 tokens x 64 or 128 channels) is read once into registers: a thread has 4
+// neighbouring channels of 16 (or, 64 channels wide, 8) consecutive tokens, so
+// rows are read as 8-byte (fp32: 16-byte) pieces of full lines, a channel-wise
+// group is reduced in registers and across warps, a token-wise one across the
+// lanes that share the token, and V's codes, packed along tokens, come out of
+// one thread's registers as whole 32- or 64-bit words.  The packed block is
+// put together in shared memory and written in 16-byte pieces.
+//
+// The work is one pass over the rows: it is bound by memory where the
+// arithmetic per value stays below about ten instructions.  The code of a value
+// is clamp(rint(fl(fl(x - z) / s))) (IEEE fp32), taken without the division:
+// with d = fl(x - z) and r = fl(1 / s), q = d r is within 2^-22 of d / s
+// relatively, that is within 2^-18 for codes up to 15, so rint(q) is the code
+// unless q lies within 2^-16 of a half; a thread that meets such a value does
+// its values of that group again with the division.  q <= 2^b - 1 up to
+// rounding, because s was rounded up, and q >= 0, because z was rounded down.
+#include <cuda_fp16.h>
+
+#include "attn_rows.h"
+
+namespace kvq {
+namespace {
+
+constexpr int kThreads = 256, kWarps = 8;
+
+__device__ __forceinline__ float min_nan(float a, float b) {
+  float r;
+  asm("min.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ float max_nan(float a, float b) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
+
+struct Group {
+  float s, z, r;  // scale, offset, 1 / scale (0: every code is 0)
+  uint16_t s_bits, z_bits;
+  bool ok;
+};
+// Scale and offset of a group with minimum mn and maximum mx (NaN where a
+// value is NaN; mn > mx: no value at all).
+__device__ __forceinline__ Group group_of_range(float mn, float mx, float qmax) {
+  Group g{0.f, 0.f, 0.f, 0, 0, true};
+  if (mn > mx) return g;
+  const __half zh = __float2half_rd(mn);
+  const float z = __half2float(zh), width = __fsub_rn(mx, z);
+  const __half sh = width != 0.f ? __float2half_ru(__fdiv_rn(width, qmax)) : __float2half_rn(0.f);
+  // not finite, or past the fp16 range (a NaN minimum or maximum gives a NaN here)
+  g.ok = fabsf(mn) < INFINITY && fabsf(mx) < INFINITY && !__hisinf(zh) && !__hisinf(sh);
+  if (!g.ok) return g;
+  g.s = __half2float(sh);
+  g.z = z;
+  g.r = g.s > 0.f ? __frcp_rn(g.s) : 0.f;
+  g.s_bits = __half_as_ushort(sh);
+  g.z_bits = __half_as_ushort(zh);
+  return g;
+}
+
+constexpr float kMagic = 12582912.f;       // 1.5 x 2^23: adding it leaves rint in the low bits
+constexpr uint32_t kMagicBits = 0x4b400000u;
+
+// The code of x plus kMagicBits; *far grows to the largest distance from an
+// integer met so far.
+__device__ __forceinline__ uint32_t code_fast(float x, float z, float r, float* far) {
+  const float d = __fsub_rn(x, z);
+  const float y = __fmaf_rn(d, r, kMagic);
+  *far = fmaxf(*far, fabsf(__fmaf_rn(d, r, -__fsub_rn(y, kMagic))));
+  return __float_as_uint(y);
+}
+__device__ __forceinline__ uint32_t code_exact(float x, float s, float z, float qmax) {
+  if (s == 0.f) return kMagicBits;
+  const float t = fminf(fmaxf(rintf(__fdiv_rn(__fsub_rn(x, z), s)), 0.f), qmax);
+  return kMagicBits + (uint32_t)t;
+}
+constexpr float kNearHalf = 0.5f - 1.f / 65536.f;
+
+// Four neighbouring values at `at` (elements).
+template <typename T>
+struct Raw;
+template <>
+struct Raw<float> {
+  float4 v;
+  __device__ __forceinline__ void load(const void* p, long long at) {
+    v = __ldg(reinterpret_cast<const float4*>(static_cast<const float*>(p) + at));
+  }
+  __device__ __forceinline__ float4 get() const { return v; }
+};
+struct Raw16 {
+  uint2 v;
+  __device__ __forceinline__ void load(const void* p, long long at) {
+    v = __ldg(reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(p) + at));
+  }
+};
+struct Bf16Tag {};
+template <>
+struct Raw<Bf16Tag> : Raw16 {
+  __device__ __forceinline__ float4 get() const {
+    return make_float4(__uint_as_float(v.x << 16), __uint_as_float(v.x & 0xffff0000u), __uint_as_float(v.y << 16),
+                       __uint_as_float(v.y & 0xffff0000u));
+  }
+};
+template <>
+struct Raw<__half> : Raw16 {
+  __device__ __forceinline__ float4 get() const {
+    const float2 a = __half22float2(*reinterpret_cast<const __half2*>(&v.x));
+    const float2 b = __half22float2(*reinterpret_cast<const __half2*>(&v.y));
+    return make_float4(a.x, a.y, b.x, b.y);
+  }
+};
+
+template <typename T, int BITS, int W>  // W: channels of the slab
+__global__ void __launch_bounds__(kThreads, 2) append_chunk_kernel(const AppendParams p) {
+  constexpr int kLanes = W / 4;                 // lanes that share a token
+  constexpr int kTok = 16 * kLanes / 32;        // tokens of a thread (16 or 8)
+  constexpr int kPer = 128 / BITS;              // codes of a 16-byte piece
+  constexpr int kPieces = W * BITS;             // 16-byte pieces of the slab's block: 128 W BITS / 128
+  constexpr float kMax = (float)((1 << BITS) - 1);
+  // packed block: K [chunk][128 tokens], V [chunk][W channels], a piece of padding per chunk against bank conflicts
+  __shared__ __align__(16) unsigned char packed[(kPieces + W * BITS / 64 + 8) * 16];
+  __shared__ float lo_s[kWarps][W], hi_s[kWarps][W];  // channel-wise: ranges per warp, then s / z (as [group][W])
+  __shared__ __align__(16) uint16_t s_out[128 * 4], z_out[128 * 4];
+  __shared__ int warp_sum[kWarps], found[4];
+  const int D = p.head_dim;
+  const int h = blockIdx.y, which = blockIdx.z & 1, slab = blockIdx.z >> 1;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const bool lead = h == 0 && blockIdx.z == 0;
+
+  // ---- which sequence and block: a scan over the blocks that the sequences touch
+  {
+    int rank = blockIdx.x;
+    if (tid == 0) found[0] = -1;
+    for (int b0 = 0; b0 < p.batch; b0 += kThreads) {
+      const int b = b0 + tid;
+      int blocks = 0, len = 0;
+      SeqRows s{0, 0, false};
+      bool bad = false;
+      if (b < p.batch) {
+        s = seq_rows(p.cu, b, p.total);
+        len = p.seq_lens[b];
+        bad = s.bad || len < 0 || (long long)len + s.n > (long long)p.max_blocks * kBlockTokens;
+        blocks = bad ? 0 : s.n == 0 ? 1 : (len + s.n - 1) / kBlockTokens - len / kBlockTokens + 1;
+        if (bad && lead && blockIdx.x == 0) report(p.dev_status, KVQ_DEV_BAD_SEQ_LEN);
+      }
+      int incl = blocks;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int v = __shfl_up_sync(0xffffffffu, incl, o);
+        if (lane >= o) incl += v;
+      }
+      if (lane == 31) warp_sum[warp] = incl;
+      __syncthreads();
+      int before = 0, all = 0;
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w) {
+        if (w < warp) before += warp_sum[w];
+        all += warp_sum[w];
+      }
+      const int i = rank - (before + incl - blocks);  // block of sequence b
+      if (i >= 0 && i < blocks) {
+        found[0] = b;
+        found[1] = i;
+      }
+      __syncthreads();
+      if (rank < all) break;
+      rank -= all;
+    }
+  }
+  const int b = found[0], nth = found[1];
+  if (b < 0) return;
+  const SeqRows s = seq_rows(p.cu, b, p.total);
+  const int len = p.seq_lens[b], end = len + s.n;
+  const int j = len / kBlockTokens + nth, t0 = j * kBlockTokens;
+  const int nv = min(kBlockTokens, end - t0);  // rows of this block
+  const int from = min(max(len - t0, 0), nv);  // ... that were there before
+  const bool tokenwise = p.scheme[which] == KVQ_TOKENWISE;
+  const size_t win_at = ((size_t)b * p.num_kv_heads + h) * kBlockTokens * D + slab * W;
+  const float* win = p.window[which] ? p.window[which] + win_at : nullptr;
+  const int sub = lane / kLanes, ch = (lane % kLanes) * 4;  // this thread's channels ch ... ch + 3
+  const int tok = warp * 16 + sub * kTok;                   // ... and tokens tok ... tok + kTok - 1
+  const Rows& rows = p.x[which];
+  const long long at0 = (long long)h * rows.sh + slab * W + ch;
+
+  // ---- the rows, in fp32
+  float x[kTok][4];
+  {
+    Raw<T> raw[kTok];
+#pragma unroll
+    for (int i = 0; i < kTok; ++i) {
+      const int t = tok + i;
+      if (t >= from && t < nv) raw[i].load(rows.data, (long long)(s.first + t0 + t - len) * rows.st + at0);
+    }
+#pragma unroll
+    for (int i = 0; i < kTok; ++i) {
+      const int t = tok + i;
+      float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (t >= from && t < nv) v = raw[i].get();
+      else if (t < from && !tokenwise) v = *reinterpret_cast<const float4*>(win + (size_t)t * D + ch);
+      x[i][0] = v.x; x[i][1] = v.y; x[i][2] = v.z; x[i][3] = v.w;
+    }
+  }
+
+  // ---- the window of the new partial last block.  Only its sequence's first
+  //      block reads the window, and does so (above) before it is written here.
+  if (win != nullptr) {
+    float* wout = p.window_out[which] + win_at;
+    const int last = end / kBlockTokens * kBlockTokens;  // the partial block's first position
+    if (nth == 0) {
+      if (last != t0) {
+        if (!tokenwise) __syncthreads();  // every thread has its rows of the old window
+        for (int e = tid; e < (end - last) * kLanes; e += kThreads) {
+          const int t = e / kLanes, c = (e % kLanes) * 4;
+          Raw<T> raw;
+          raw.load(rows.data, (long long)(s.first + last + t - len) * rows.st + (long long)h * rows.sh + slab * W + c);
+          *reinterpret_cast<float4*>(wout + (size_t)t * D + c) = raw.get();
+        }
+      } else if (nv < kBlockTokens) {
+#pragma unroll
+        for (int i = 0; i < kTok; ++i) {
+          const int t = tok + i;
+          if (t < nv && (t >= from || wout != win)) {
+            float4 v = make_float4(x[i][0], x[i][1], x[i][2], x[i][3]);
+            if (t < from && tokenwise) v = *reinterpret_cast<const float4*>(win + (size_t)t * D + ch);
+            *reinterpret_cast<float4*>(wout + (size_t)t * D + ch) = v;
+          }
+        }
+      }
+    }
+  }
+  if (s.n == 0) return;
+  const int page = p.page_table ? p.page_table[(size_t)b * p.max_blocks + j] : b * p.max_blocks + j;
+  if (page < 0 || page >= p.num_pages) {
+    if (lead && tid == 0) report(p.dev_status, KVQ_DEV_BAD_PAGE);
+    return;
+  }
+  const int G = p.group, gps = W / G;  // channel groups of a token in this slab (token-wise)
+  const int nsz = kBlockTokens * D / G;
+  const size_t blk = (size_t)page * p.num_kv_heads + h;
+
+  // K, one token of this thread: 4 codes (with kMagicBits each) -> their 16 or 8 bits of the token's row
+  auto put_k = [&](int t, uint32_t a, uint32_t bb, uint32_t c, uint32_t d) {
+    const uint32_t w = (a - kMagicBits) | (bb - kMagicBits) << BITS | (c - kMagicBits) << 2 * BITS |
+                       (d - kMagicBits) << 3 * BITS;
+    unsigned char* at = packed + ((ch / kPer) * 129 + t) * 16 + (ch % kPer) * BITS / 8;
+    if (BITS == 4) *reinterpret_cast<uint16_t*>(at) = (uint16_t)w;
+    else *at = (unsigned char)w;
+  };
+  // V, one channel of this thread: kTok codes of BITS bits along the row
+  auto put_v = [&](int c, uint64_t w) {
+    unsigned char* at = packed + ((tok / kPer) * (W + 1) + ch + c) * 16 + (tok % kPer) * BITS / 8;
+    if (kTok * BITS == 64) *reinterpret_cast<uint64_t*>(at) = w;
+    else if (kTok * BITS == 32) *reinterpret_cast<uint32_t*>(at) = (uint32_t)w;
+    else *reinterpret_cast<uint16_t*>(at) = (uint16_t)w;
+  };
+  uint64_t vw[4] = {0, 0, 0, 0};  // V: the thread's codes so far, per channel
+  auto add_v = [&](int c, int i, uint32_t y) { vw[c] |= (uint64_t)(y - kMagicBits) << (i * BITS); };
+
+  if (tokenwise) {
+    const int glanes = G / 4;  // lanes of a group
+#pragma unroll
+    for (int i = 0; i < kTok; ++i) {
+      const int t = tok + i;
+      float mn = min_nan(min_nan(x[i][0], x[i][1]), min_nan(x[i][2], x[i][3]));
+      float mx = max_nan(max_nan(x[i][0], x[i][1]), max_nan(x[i][2], x[i][3]));
+      for (int o = 1; o < glanes; o <<= 1) {
+        mn = min_nan(mn, __shfl_xor_sync(0xffffffffu, mn, o));
+        mx = max_nan(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+      }
+      const bool live = t >= from && t < nv;
+      Group g = group_of_range(mn, mx, kMax);
+      if (!live) g = Group{0.f, 0.f, 0.f, 0, 0, true};
+      const bool first = ch % G == 0;
+      if (!g.ok && first) report(p.dev_status, KVQ_DEV_NONFINITE);
+      if (first) {
+        s_out[t * gps + ch / G] = g.s_bits;
+        z_out[t * gps + ch / G] = g.z_bits;
+      }
+      uint32_t y[4];
+      float far = 0.f;
+#pragma unroll
+      for (int c = 0; c < 4; ++c) y[c] = code_fast(x[i][c], g.z, g.r, &far);
+      if (!(far < kNearHalf)) {
+#pragma unroll
+        for (int c = 0; c < 4; ++c) y[c] = code_exact(x[i][c], g.s, g.z, kMax);
+      }
+      if (g.r == 0.f) y[0] = y[1] = y[2] = y[3] = kMagicBits;  // width zero, not finite, or no token
+      if (which == 0) {
+        put_k(t, y[0], y[1], y[2], y[3]);
+      } else {
+#pragma unroll
+        for (int c = 0; c < 4; ++c) add_v(c, i, y[c]);
+      }
+    }
+  } else {
+    // ranges of this thread's tokens per channel, then across the warps (and
+    // half-warps) of the group's tokens
+    float mn[4], mx[4];
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+      mn[c] = INFINITY;
+      mx[c] = -INFINITY;
+    }
+#pragma unroll
+    for (int i = 0; i < kTok; ++i) {
+      if (tok + i < nv) {
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          mn[c] = min_nan(mn[c], x[i][c]);
+          mx[c] = max_nan(mx[c], x[i][c]);
+        }
+      }
+    }
+    if (kLanes < 32) {  // both halves of the warp hold the same channels
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        mn[c] = min_nan(mn[c], __shfl_xor_sync(0xffffffffu, mn[c], 16));
+        mx[c] = max_nan(mx[c], __shfl_xor_sync(0xffffffffu, mx[c], 16));
+      }
+    }
+    *reinterpret_cast<float4*>(&lo_s[warp][ch]) = make_float4(mn[0], mn[1], mn[2], mn[3]);
+    *reinterpret_cast<float4*>(&hi_s[warp][ch]) = make_float4(mx[0], mx[1], mx[2], mx[3]);
+    __syncthreads();
+    const int gw = G / 16, groups = kBlockTokens / G;  // warps of a token group, token groups
+    Group mine[2];                                     // groups * W / 256 <= 2 groups of a thread
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      const int e = tid + k * kThreads;
+      if (e < groups * W) {
+        const int g = e / W, c = e % W;
+        float a = INFINITY, z = -INFINITY;
+        for (int w = g * gw; w < (g + 1) * gw; ++w) {
+          a = min_nan(a, lo_s[w][c]);
+          z = max_nan(z, hi_s[w][c]);
+        }
+        mine[k] = group_of_range(a, z, kMax);
+        if (!mine[k].ok) report(p.dev_status, KVQ_DEV_NONFINITE);
+        s_out[e] = mine[k].s_bits;
+        z_out[e] = mine[k].z_bits;
+      }
+    }
+    __syncthreads();
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      const int e = tid + k * kThreads;
+      if (e < groups * W) {
+        lo_s[e / W][e % W] = mine[k].s;
+        hi_s[e / W][e % W] = mine[k].z;
+      }
+    }
+    __syncthreads();
+    const int g = warp * 16 / G;
+    const float4 s4 = *reinterpret_cast<const float4*>(&lo_s[g][ch]);
+    const float4 z4 = *reinterpret_cast<const float4*>(&hi_s[g][ch]);
+    const float sc[4] = {s4.x, s4.y, s4.z, s4.w}, zc[4] = {z4.x, z4.y, z4.z, z4.w};
+    float rc[4], far = 0.f;
+#pragma unroll
+    for (int c = 0; c < 4; ++c) rc[c] = sc[c] > 0.f ? __frcp_rn(sc[c]) : 0.f;
+    uint32_t y[kTok][4];
+#pragma unroll
+    for (int i = 0; i < kTok; ++i) {
+      const bool live = tok + i < nv;
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        // a channel whose codes are all zero takes z for its values
+        y[i][c] = code_fast(live && sc[c] > 0.f ? x[i][c] : zc[c], zc[c], rc[c], &far);
+      }
+    }
+    if (!(far < kNearHalf)) {
+#pragma unroll
+      for (int i = 0; i < kTok; ++i)
+#pragma unroll
+        for (int c = 0; c < 4; ++c) y[i][c] = tok + i < nv ? code_exact(x[i][c], sc[c], zc[c], kMax) : kMagicBits;
+    }
+#pragma unroll
+    for (int i = 0; i < kTok; ++i) {
+      if (which == 0) {
+        put_k(tok + i, y[i][0], y[i][1], y[i][2], y[i][3]);
+      } else {
+#pragma unroll
+        for (int c = 0; c < 4; ++c) add_v(c, i, y[i][c]);
+      }
+    }
+  }
+  if (which == 1) {
+#pragma unroll
+    for (int c = 0; c < 4; ++c) put_v(c, vw[c]);
+  }
+  __syncthreads();
+
+  // ---- out: the slab's pieces of the block (K: chunks of every token, V: rows of every chunk)
+  const int keep = tokenwise ? from : 0;  // earlier tokens keep their codes, s and z
+  uint8_t* dst = p.codes[which] + blk * (size_t)(kBlockTokens * D * BITS / 8);
+  if (which == 0) {
+    for (int e = tid; e < kPieces; e += kThreads) {
+      const int chunk = e >> 7, t = e & 127;
+      if (t >= keep)
+        *reinterpret_cast<uint4*>(dst + ((size_t)(slab * (W / kPer) + chunk) * kBlockTokens + t) * 16) =
+            *reinterpret_cast<const uint4*>(packed + (chunk * 129 + t) * 16);
+    }
+  } else {
+    for (int e = tid; e < kPieces; e += kThreads) {
+      const int chunk = e / W, r = e % W, t = chunk * kPer;
+      if (t + kPer <= keep) continue;
+      uint4 v = *reinterpret_cast<const uint4*>(packed + (chunk * (W + 1) + r) * 16);
+      uint4* at = reinterpret_cast<uint4*>(dst + ((size_t)chunk * D + slab * W + r) * 16);
+      if (t < keep) {
+        const uint4 was = *at;
+        const uint32_t old[4] = {was.x, was.y, was.z, was.w};
+        uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const int n = min(max((keep - t) * BITS - 32 * k, 0), 32);  // bits to keep
+          const uint32_t mask = n == 32 ? 0xffffffffu : (1u << n) - 1u;
+          w[k] = (w[k] & ~mask) | (old[k] & mask);
+        }
+        v = make_uint4(w[0], w[1], w[2], w[3]);
+      }
+      *at = v;
+    }
+  }
+  uint16_t* so = p.scale[which] + blk * nsz;
+  uint16_t* zo = p.zero[which] + blk * nsz;
+  if (tokenwise) {  // entry token * (D / G) + group
+    for (int e = tid + keep * gps; e < kBlockTokens * gps; e += kThreads) {
+      const int t = e / gps, at = t * (D / G) + slab * gps + e - t * gps;
+      so[at] = s_out[e];
+      zo[at] = z_out[e];
+    }
+  } else {  // entry token group * D + channel
+    for (int e = tid; e < kBlockTokens / G * W; e += kThreads) {
+      const int at = e / W * D + slab * W + e % W;
+      so[at] = s_out[e];
+      zo[at] = z_out[e];
+    }
+  }
+}
+
+template <typename T>
+cudaError_t launch(const AppendParams& p, cudaStream_t stream) {
+  // blocks touched: one per sequence, one more where a chunk of two tokens or
+  // more can cross into the next, one more for every 128 tokens past that
+  const long long two = p.batch < p.total / 2 ? p.batch : p.total / 2;
+  const long long blocks = p.batch + two + (p.total - 2 * two) / kBlockTokens;
+  const int w = p.head_dim < 128 ? p.head_dim : 128;
+  const dim3 grid((unsigned)blocks, (unsigned)p.num_kv_heads, (unsigned)(2 * (p.head_dim / w)));
+  if (p.bits == 4) {
+    if (w == 64) append_chunk_kernel<T, 4, 64><<<grid, kThreads, 0, stream>>>(p);
+    else append_chunk_kernel<T, 4, 128><<<grid, kThreads, 0, stream>>>(p);
+  } else {
+    if (w == 64) append_chunk_kernel<T, 2, 64><<<grid, kThreads, 0, stream>>>(p);
+    else append_chunk_kernel<T, 2, 128><<<grid, kThreads, 0, stream>>>(p);
+  }
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_append_chunk(const AppendParams& p, cudaStream_t stream) {
+  if (p.dtype == KVQ_FP32) return launch<float>(p, stream);
+  if (p.dtype == KVQ_FP16) return launch<__half>(p, stream);
+  return launch<Bf16Tag>(p, stream);
+}
+
+}  // namespace kvq

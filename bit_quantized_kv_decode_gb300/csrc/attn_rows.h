@@ -41,7 +41,6 @@ __device__ __forceinline__ SeqRows seq_rows(const int32_t* cu, int b, int total)
   return {bad ? 0 : a, bad ? 0 : e - a, bad};
 }
 
-cudaError_t launch_row_attn_simple(const RowAttnParams& p, bool cached, cudaStream_t stream);
 
 cudaError_t launch_prompt_attn(const RowAttnParams& p, cudaStream_t stream);
 

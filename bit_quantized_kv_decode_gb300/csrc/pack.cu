@@ -15,7 +15,7 @@
 
 #include <cstdint>
 
-#include "attn_rows.h"
+#include "kvq_internal.h"
 
 namespace kvq {
 
@@ -82,21 +82,11 @@ __device__ __forceinline__ bool block_geometry(const PackParams& p, int b, int j
   return true;
 }
 
-// Where one block goes: its codes and s / z arrays and the group rule.
-struct BlockOut {
-  uint8_t* codes;
-  uint16_t *scale, *zero;
-  uint32_t* dev_status;
-  int bits, head_dim, group, which;
-  bool tokenwise;
-};
-
-// Quantize and pack the block whose rows [0, nv) lie in shared memory as fp32
-// (rows of D + 1 floats).  s / z of a block: token-wise, entry
-// t * (D / G) + g for channels [gG, gG + G) of token t; channel-wise, entry
-// k * D + c for channel c over block tokens [kG, kG + G).  Rows below `from`
-// (token-wise only) keep the codes, s and z that the block already has.
-__device__ void quantize_block(const BlockOut& p, int from, int nv, unsigned char* smem_raw) {
+// Quantize and pack one block of KV head h: the nv valid token rows at src
+// (fp32, D channels each) into page `page`.  s / z of a block: token-wise,
+// entry t * (D / G) + g for channels [gG, gG + G) of token t; channel-wise,
+// entry k * D + c for channel c over block tokens [kG, kG + G).
+__device__ void pack_block(const PackParams& p, const float* src, int page, int nv, int h, unsigned char* smem_raw) {
   const int D = p.head_dim, G = p.group, pitch = D + 1;
   float* xs = reinterpret_cast<float*>(smem_raw);                                    // [128][D + 1]
   uint8_t* cs = reinterpret_cast<uint8_t*>(xs + kBlockTokens * pitch);              // [128 tok][D ch]
@@ -106,14 +96,22 @@ __device__ void quantize_block(const BlockOut& p, int from, int nv, unsigned cha
   const int qmax = (1 << p.bits) - 1;
   const int nsz = kBlockTokens * D / G;
 
+  // Stage the valid tokens of the tile (rows t < nv).
+  for (int i = tid; i < nv * (D / 4); i += kThreads) {
+    int t = i / (D / 4), c4 = (i % (D / 4)) * 4;
+    float4 v = *reinterpret_cast<const float4*>(src + (size_t)t * D + c4);
+    float* row = xs + t * pitch + c4;
+    row[0] = v.x; row[1] = v.y; row[2] = v.z; row[3] = v.w;
+  }
   for (int i = tid; i < kBlockTokens * D / 4; i += kThreads) reinterpret_cast<uint32_t*>(cs)[i] = 0u;
   for (int i = tid; i < nsz; i += kThreads) { s_out[i] = 0; z_out[i] = 0; }  // groups without valid values
   __syncthreads();
 
-  if (p.tokenwise) {
+  const bool tokenwise = (p.which == 0 ? p.k_scheme : p.v_scheme) == KVQ_TOKENWISE;
+  if (tokenwise) {
     // groups of G channels of token t; one warp per token, lane holds channels lane + 32 k
     const int gpt = D / G, kpg = G / 32;  // groups per token, 32-channel slices per group
-    for (int t = from + warp; t < nv; t += kThreads / 32) {
+    for (int t = warp; t < nv; t += kThreads / 32) {
       for (int g = 0; g < gpt; ++g) {
         float v[4];
         bool fin = true;
@@ -172,9 +170,10 @@ __device__ void quantize_block(const BlockOut& p, int from, int nv, unsigned cha
   const int per_chunk = 128 / bits;  // columns per 16-byte chunk: 32 (INT4) or 64 (INT2)
   const int nrows = p.which == 0 ? kBlockTokens : D, ncols = p.which == 0 ? D : kBlockTokens;
   const int nchunk = ncols / per_chunk;
+  const size_t blk = (size_t)page * p.num_kv_heads + h;
+  uint8_t* dst = p.codes + blk * (size_t)(kBlockTokens * D * bits / 8);
   for (int i = tid; i < nchunk * nrows; i += kThreads) {
     int k = i / nrows, r = i % nrows;
-    if (p.which == 0 && r < from) continue;
     uint32_t w[4] = {0u, 0u, 0u, 0u};
     for (int e = 0; e < per_chunk; ++e) {
       int col = k * per_chunk + e;
@@ -183,42 +182,12 @@ __device__ void quantize_block(const BlockOut& p, int from, int nv, unsigned cha
       int bitpos = e * bits;
       w[bitpos >> 5] |= code << (bitpos & 31);
     }
-    uint4* dst = reinterpret_cast<uint4*>(p.codes + (size_t)i * 16);
-    if (p.which == 1 && k * per_chunk < from) {  // V: earlier tokens of this row
-      const uint4 was = *dst;
-      const uint32_t old[4] = {was.x, was.y, was.z, was.w};
-      const int keep = (from - k * per_chunk) * bits;  // bits of the chunk to keep
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const int n = min(max(keep - 32 * j, 0), 32);
-        const uint32_t mask = n == 32 ? 0xffffffffu : (1u << n) - 1u;
-        w[j] = (w[j] & ~mask) | (old[j] & mask);
-      }
-    }
-    *dst = make_uint4(w[0], w[1], w[2], w[3]);
+    *reinterpret_cast<uint4*>(dst + (size_t)i * 16) = make_uint4(w[0], w[1], w[2], w[3]);
   }
-  for (int i = tid + from * (D / G); i < nsz; i += kThreads) {
-    p.scale[i] = s_out[i];
-    p.zero[i] = z_out[i];
+  for (int i = tid; i < nsz; i += kThreads) {
+    p.scale[blk * nsz + i] = s_out[i];
+    p.zero[blk * nsz + i] = z_out[i];
   }
-}
-
-// Quantize and pack one block of KV head h: the nv valid token rows at src
-// (fp32, D channels each) into page `page`.
-__device__ void pack_block(const PackParams& p, const float* src, int page, int nv, int h, unsigned char* smem_raw) {
-  const int D = p.head_dim, pitch = D + 1, nsz = kBlockTokens * D / p.group;
-  float* xs = reinterpret_cast<float*>(smem_raw);
-  for (int i = threadIdx.x; i < nv * (D / 4); i += kThreads) {
-    int t = i / (D / 4), c4 = (i % (D / 4)) * 4;
-    float4 v = *reinterpret_cast<const float4*>(src + (size_t)t * D + c4);
-    float* row = xs + t * pitch + c4;
-    row[0] = v.x; row[1] = v.y; row[2] = v.z; row[3] = v.w;
-  }
-  const size_t blk = (size_t)page * p.num_kv_heads + h;
-  const BlockOut o{p.codes + blk * (size_t)(kBlockTokens * D * p.bits / 8), p.scale + blk * nsz, p.zero + blk * nsz,
-                   p.dev_status, p.bits, D, p.group, p.which,
-                   (p.which == 0 ? p.k_scheme : p.v_scheme) == KVQ_TOKENWISE};
-  quantize_block(o, 0, nv, smem_raw);
 }
 
 __global__ void __launch_bounds__(kThreads) pack_kernel(PackParams p) {
@@ -255,69 +224,6 @@ __global__ void __launch_bounds__(kThreads) append_kernel(PackParams p) {
   for (int c = threadIdx.x; c < D; c += kThreads) win[(size_t)r * D + c] = xn[c];
   __syncthreads();  // the new row is visible to the whole CTA
   pack_block(p, win, page, r + 1, h, smem_raw);
-}
-
-// Append a chunk of new tokens: one CTA per (block touched, KV head, K or V).
-// Sequence b touches blocks seq_lens[b] / 128 to (seq_lens[b] + n - 1) / 128.
-// The CTA of its first block also writes window_out, after it has read the
-// window's rows of that block (window_out may be the window).
-__global__ void __launch_bounds__(kThreads) append_chunk_kernel(const AppendParams p) {
-  extern __shared__ __align__(16) unsigned char smem_raw[];
-  const int h = blockIdx.y, which = blockIdx.z, tid = threadIdx.x;
-  const int D = p.head_dim, pitch = D + 1, nsz = kBlockTokens * D / p.group;
-  const bool lead = h == 0 && which == 0 && tid == 0;
-  int i = blockIdx.x, b = 0, len = 0;
-  SeqRows s{};
-  for (; b < p.batch; ++b) {  // the sequence and block of this CTA
-    s = seq_rows(p.cu, b, p.total);
-    len = p.seq_lens[b];
-    const bool bad = s.bad || len < 0 || (long long)len + s.n > (long long)p.max_blocks * kBlockTokens;
-    if (bad && i == 0 && lead) report(p.dev_status, KVQ_DEV_BAD_SEQ_LEN);
-    const int blocks = bad || s.n == 0 ? 1 : (len + s.n - 1) / kBlockTokens - len / kBlockTokens + 1;
-    if (i < blocks) {
-      if (bad) return;
-      break;
-    }
-    i -= blocks;
-  }
-  if (b == p.batch) return;
-  const int end = len + s.n, j = len / kBlockTokens + i, t0 = j * kBlockTokens;
-  const int nv = min(kBlockTokens, end - t0);       // rows of this block
-  const int from = min(max(len - t0, 0), nv);       // ... that were there before
-  const float* win = p.window[which] ? p.window[which] + ((size_t)b * p.num_kv_heads + h) * kBlockTokens * D : nullptr;
-  float* xs = reinterpret_cast<float*>(smem_raw);
-  auto value = [&](int pos, int c) -> float {  // new token at position pos
-    const long long at = (s.first + pos - len) * p.x[which].st + h * p.x[which].sh + c;
-    if (p.dtype == KVQ_FP32) return static_cast<const float*>(p.x[which].data)[at];
-    const uint16_t w = static_cast<const uint16_t*>(p.x[which].data)[at];
-    return p.dtype == KVQ_FP16 ? __half2float(__ushort_as_half(w)) : __uint_as_float((uint32_t)w << 16);
-  };
-  for (int e = tid; e < nv * D; e += kThreads) {
-    const int t = e / D, c = e % D;
-    if (t >= from) xs[t * pitch + c] = value(t0 + t, c);
-    else if (win != nullptr) xs[t * pitch + c] = win[t * D + c];
-  }
-  __syncthreads();
-  if (i == 0 && win != nullptr) {
-    float* wout = p.window_out[which] + ((size_t)b * p.num_kv_heads + h) * kBlockTokens * D;
-    const int last = end / kBlockTokens * kBlockTokens;  // first position of the new partial block
-    for (int e = tid; e < (end - last) * D; e += kThreads) {
-      const int t = e / D, c = e % D;
-      if (last == t0 && t < from && wout == win) continue;
-      wout[e] = last == t0 ? xs[t * pitch + c] : value(last + t, c);
-    }
-  }
-  if (s.n == 0) return;
-  const int page = p.page_table ? p.page_table[(size_t)b * p.max_blocks + j] : b * p.max_blocks + j;
-  if (page < 0 || page >= p.num_pages) {
-    if (lead) report(p.dev_status, KVQ_DEV_BAD_PAGE);
-    return;
-  }
-  const size_t blk = (size_t)page * p.num_kv_heads + h;
-  const BlockOut o{p.codes[which] + blk * (size_t)(kBlockTokens * D * p.bits / 8), p.scale[which] + blk * nsz,
-                   p.zero[which] + blk * nsz, p.dev_status, p.bits, D, p.group, which,
-                   p.scheme[which] == KVQ_TOKENWISE};
-  quantize_block(o, o.tokenwise ? from : 0, nv, smem_raw);
 }
 
 __global__ void __launch_bounds__(kThreads) dequant_kernel(DequantParams p) {
@@ -387,16 +293,6 @@ cudaError_t launch_append(const PackParams& p, cudaStream_t stream) {
   if (e != cudaSuccess) return e;
   dim3 grid(p.num_kv_heads, p.batch);
   append_kernel<<<grid, kThreads, smem, stream>>>(p);
-  return cudaGetLastError();
-}
-
-cudaError_t launch_append_chunk(const AppendParams& p, cudaStream_t stream) {
-  const size_t smem = pack_smem_bytes(p.head_dim, p.group);
-  cudaError_t e = cudaFuncSetAttribute(append_chunk_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-  if (e != cudaSuccess) return e;
-  // blocks touched: n tokens lie in at most n / 128 + 2 blocks
-  dim3 grid(p.total / kBlockTokens + 2 * p.batch, p.num_kv_heads, 2);
-  append_chunk_kernel<<<grid, kThreads, smem, stream>>>(p);
   return cudaGetLastError();
 }
 
