@@ -268,64 +268,118 @@ def merge(o_parts: torch.Tensor, lse_parts: torch.Tensor, out: Optional[torch.Te
     return out, lse
 
 
+# ---------------------------------------------------------------------------
+# Operators over rows of new tokens.  A serving step makes several of these
+# calls per layer, so the wrappers test what has to hold in a few expressions
+# and work out what to say only when something does not.
+# ---------------------------------------------------------------------------
+
 _DTYPES = {torch.bfloat16: _lib.BF16, torch.float16: _lib.FP16, torch.float32: _lib.FP32}
+_HALF = (torch.bfloat16, torch.float16)
+_STATUS = (torch.int32, torch.uint32)
+_SCALES = (torch.float16, torch.int16, torch.uint16)
 
 
-def _rows(t: torch.Tensor, name: str, dtypes, heads: Optional[int] = None, dim: Optional[int] = None,
-          tokens: Optional[int] = None) -> Rows:
+def _rows(t: torch.Tensor, name: str, dtypes, tokens=None, heads=None, dim=None) -> Rows:
     """A [tokens, heads, head_dim] tensor as the library reads it where it lies:
     channels contiguous, token and head strides multiples of 16 bytes."""
+    if isinstance(t, torch.Tensor) and t.is_cuda and t.dim() == 3 and t.dtype in dtypes:
+        n, h, d = t.shape
+        if (tokens is None or n == tokens) and (heads is None or h == heads) and (dim is None or d == dim) and \
+                not (t.requires_grad and torch.is_grad_enabled()):
+            st, sh, sc = t.stride()
+            if n == 1:
+                st = h * d  # a single token's (head's) stride is free
+            if h == 1:
+                sh = d
+            ptr = t.data_ptr()
+            unit = 3 if t.dtype is torch.float32 else 7
+            if sc == 1 and st >= d and sh >= d and not (st | sh) & unit and not ptr & 15:
+                return Rows(ptr, st, sh)
+            if n == 0 or h == 0 or d == 0:
+                return Rows(None, 0, 0)
+    raise ValueError(_why_not_rows(t, name, dtypes, tokens, heads, dim))
+
+
+def _why_not_rows(t, name, dtypes, tokens, heads, dim) -> str:
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
-        raise ValueError(f"{name} must be a CUDA tensor")
+        return f"{name} must be a CUDA tensor"
     if t.dtype not in dtypes:
-        raise ValueError(f"{name} must have dtype {' or '.join(str(d) for d in dtypes)}, got {t.dtype}")
+        return f"{name} must have dtype {' or '.join(str(d) for d in dtypes)}, got {t.dtype}"
     if t.dim() != 3:
-        raise ValueError(f"{name} must be [tokens, heads, head_dim], got {t.dim()} dimensions")
+        return f"{name} must be [tokens, heads, head_dim], got {t.dim()} dimensions"
     for what, got, want in (("tokens", t.shape[0], tokens), ("heads", t.shape[1], heads), ("channels", t.shape[2], dim)):
         if want is not None and got != want:
-            raise ValueError(f"{name} must have {want} {what}, got {got}")
+            return f"{name} must have {want} {what}, got {got}"
     if t.requires_grad and torch.is_grad_enabled():
-        raise ValueError(f"{name} requires a gradient: this operator has no backward pass (use torch.no_grad())")
-    if t.numel() == 0:
-        return Rows(None, 0, 0)
-    unit = 16 // t.element_size()
-    st = t.stride(0) if t.shape[0] > 1 else t.shape[1] * t.shape[2]  # a single token's (head's) stride is free
-    sh = t.stride(1) if t.shape[1] > 1 else t.shape[2]
-    if t.stride(2) != 1 or st < t.shape[2] or sh < t.shape[2] or st % unit or sh % unit or t.data_ptr() % 16:
-        raise ValueError(f"{name} must have contiguous channels, token and head strides that are multiples of 16 bytes "
-                         f"(at least head_dim elements) and a 16-byte aligned start; got strides {tuple(t.stride())}")
-    return Rows(t.data_ptr(), st, sh)
+        return f"{name} requires a gradient: this operator has no backward pass (use torch.no_grad())"
+    return (f"{name} must have contiguous channels, token and head strides that are multiples of 16 bytes (at least "
+            f"head_dim elements) and a 16-byte aligned start; got strides {tuple(t.stride())}")
 
 
-def _same_device(device, **tensors):
-    for name, t in tensors.items():
-        for x in t if isinstance(t, (tuple, list)) else (t,):
-            if x is not None and x.device != device:
-                raise ValueError(f"{name} is on {x.device}, q (or k_new) on {device}")
+def _ptr(t, name: str, dtypes, numel: int, device: int):
+    """Address of an optional contiguous tensor of that many elements on that device."""
+    if t is None:
+        return None
+    if t.dtype in dtypes and t.numel() == numel and t.get_device() == device and t.is_contiguous():
+        return t.data_ptr()
+    _need(t, name, dtypes, numel)
+    raise ValueError(f"{name} is on {t.device}, the rows are on cuda:{device}")
 
 
-def _outputs(q: torch.Tensor, out, lse, return_lse: bool):
-    T, Hq, D = q.shape
+def _starts(cu_seqlens, device: int):
+    """(batch, address) of the row offsets."""
+    if isinstance(cu_seqlens, torch.Tensor) and cu_seqlens.dim() == 1:
+        n = cu_seqlens.numel()
+        if n >= 2:
+            return n - 1, _ptr(cu_seqlens, "cu_seqlens", (torch.int32,), n, device)
+    raise ValueError("cu_seqlens must be int32 [batch + 1]")
+
+
+def _blocks_per_sequence(batch: int, page_table, max_blocks, device: int, what: str):
+    """(max_blocks, page table address)."""
+    if page_table is not None:
+        if page_table.dim() != 2 or page_table.shape[0] != batch:
+            raise ValueError("page_table must be int32 [batch, max_blocks]")
+        mb = page_table.shape[1]
+        return mb, _ptr(page_table, "page_table", (torch.int32,), batch * mb, device)
+    if max_blocks is None:
+        raise ValueError(f"{what} needs page_table, or max_blocks for a contiguous cache")
+    return int(max_blocks), None
+
+
+def _cache_ptrs(desc: CacheDesc, name: str, cache, device: int):
+    codes, scale, zero = cache
+    blocks = desc.num_pages * desc.num_kv_heads * BLOCK_TOKENS * desc.head_dim
+    n = blocks // (desc.group_size or 128)
+    return (_ptr(codes, name + " codes", (torch.uint8,), blocks * desc.bits // 8, device),
+            _ptr(scale, name + " scale", _SCALES, n, device), _ptr(zero, name + " zero", _SCALES, n, device))
+
+
+def _outputs(q: torch.Tensor, T: int, Hq: int, D: int, out, lse, return_lse: bool, device: int):
+    """(out, lse, their addresses); what is not given is made."""
     if out is None:
-        out = torch.empty(T, Hq, D, dtype=q.dtype, device=q.device)
-    _need(out, "out", q.dtype, T * Hq * D)
-    if lse is None and return_lse:
-        lse = torch.empty(T, Hq, dtype=torch.float32, device=q.device)
-    if lse is not None:
-        _need(lse, "lse", torch.float32, T * Hq)
-    return out, lse
+        out = torch.empty((T, Hq, D), dtype=q.dtype, device=q.device)
+        po = out.data_ptr()
+    else:
+        po = _ptr(out, "out", (q.dtype,), T * Hq * D, device)
+    if lse is None:
+        if not return_lse:
+            return out, None, po, None
+        lse = torch.empty((T, Hq), dtype=torch.float32, device=q.device)
+        return out, lse, po, lse.data_ptr()
+    return out, lse, po, _ptr(lse, "lse", (torch.float32,), T * Hq, device)
 
 
-def _starts(cu_seqlens: torch.Tensor) -> int:
-    _need(cu_seqlens, "cu_seqlens", torch.int32)
-    if cu_seqlens.dim() != 1 or cu_seqlens.numel() < 2:
-        raise ValueError("cu_seqlens must be int32 [batch + 1]")
-    return cu_seqlens.numel() - 1
-
-
-def _check_status(dev_status):
-    if dev_status is not None:
-        _need(dev_status, "dev_status", (torch.int32, torch.uint32), 1)
+def _launch(device: int, what: str, fn, *args):
+    """fn(*args, stream) with the rows' device current, on its current stream."""
+    if torch.cuda.current_device() == device:
+        st = fn(*args, torch._C._cuda_getCurrentRawStream(device))
+    else:
+        with torch.cuda.device(device):
+            st = fn(*args, torch._C._cuda_getCurrentRawStream(device))
+    if st != _lib.KVQ_OK:
+        _lib.check(st, what)
 
 
 def prompt_attn(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu_seqlens: torch.Tensor, causal: bool = True,
@@ -336,20 +390,20 @@ def prompt_attn(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu_seqlens: t
     in rows [cu_seqlens[b], cu_seqlens[b + 1]).  Returns out [T, Hq, D] in q's
     type, and with return_lse (or an lse buffer) also lse fp32 [T, Hq].  Rows
     outside every sequence are left as they were.  Inference only."""
-    half = (torch.bfloat16, torch.float16)
-    qr = _rows(q, "q", half)
+    qr = _rows(q, "q", _HALF)
     T, Hq, D = q.shape
-    kr = _rows(k, "k", (q.dtype,), dim=D, tokens=T)
-    vr = _rows(v, "v", (q.dtype,), heads=k.shape[1], dim=D, tokens=T)
-    B = _starts(cu_seqlens)
-    _check_status(dev_status)
-    _same_device(q.device, k=k, v=v, cu_seqlens=cu_seqlens, out=out, lse=lse, dev_status=dev_status)
-    out, lse = _outputs(q, out, lse, return_lse)
-    d = PromptDesc(_DTYPES[q.dtype], D, Hq, k.shape[1], B, T, int(bool(causal)), sm_scale, flags)
-    with torch.cuda.device(q.device):
-        st = library().kvq_prompt_attn(ctypes.byref(d), ctypes.byref(qr), ctypes.byref(kr), ctypes.byref(vr),
-                                       _p(cu_seqlens), _p(out), _p(lse), _p(dev_status), _stream())
-    _lib.check(st, "kvq_prompt_attn")
+    dt = (q.dtype,)
+    kr = _rows(k, "k", dt, T, None, D)
+    Hkv = k.shape[1]
+    vr = _rows(v, "v", dt, T, Hkv, D)
+    dev = q.get_device()
+    if k.get_device() != dev or v.get_device() != dev:
+        raise ValueError(f"q, k and v are on {q.device}, {k.device} and {v.device}")
+    B, pcu = _starts(cu_seqlens, dev)
+    out, lse, po, pl = _outputs(q, T, Hq, D, out, lse, return_lse, dev)
+    d = PromptDesc(_DTYPES[q.dtype], D, Hq, Hkv, B, T, 1 if causal else 0, sm_scale, flags)
+    _launch(dev, "kvq_prompt_attn", library().kvq_prompt_attn, ctypes.byref(d), ctypes.byref(qr), ctypes.byref(kr),
+            ctypes.byref(vr), pcu, po, pl, _ptr(dev_status, "dev_status", _STATUS, 1, dev))
     return out if lse is None else (out, lse)
 
 
@@ -365,57 +419,39 @@ def append_chunk(desc: CacheDesc, k_new: torch.Tensor, v_new: torch.Tensor, cu_s
     sequence's partial last block, as for append; they are updated in place
     unless *_window_out is given, and a token-wise cache may do without.  The
     caller advances seq_lens afterwards.  Returns (k_cache, v_cache)."""
-    kinds = (torch.bfloat16, torch.float16, torch.float32)
-    kr = _rows(k_new, "k_new", kinds, desc.num_kv_heads, desc.head_dim)
+    H, D = desc.num_kv_heads, desc.head_dim
+    kr = _rows(k_new, "k_new", _DTYPES, None, H, D)
     T = k_new.shape[0]
-    vr = _rows(v_new, "v_new", (k_new.dtype,), desc.num_kv_heads, desc.head_dim, T)
-    B = _starts(cu_seqlens)
-    _need(seq_lens, "seq_lens", torch.int32, B)
-    if page_table is not None:
-        mb = _geometry(B, 1, None, page_table, None)
-    elif max_blocks is not None:
-        mb = int(max_blocks)
-    else:
-        raise ValueError("append_chunk needs page_table or max_blocks")
-    cb, sb = cache_bytes(desc)
-    for name, cache in (("k_cache", k_cache), ("v_cache", v_cache)):
-        codes, scale, zero = cache
-        _need(codes, name + " codes", torch.uint8, cb)
-        _need(scale, name + " scale", (torch.float16, torch.int16, torch.uint16), sb // 2)
-        _need(zero, name + " zero", (torch.float16, torch.int16, torch.uint16), sb // 2)
+    vr = _rows(v_new, "v_new", (k_new.dtype,), T, H, D)
+    dev = k_new.get_device()
+    if v_new.get_device() != dev:
+        raise ValueError(f"k_new is on {k_new.device}, v_new on {v_new.device}")
+    B, pcu = _starts(cu_seqlens, dev)
+    mb, pt = _blocks_per_sequence(B, page_table, max_blocks, dev, "append_chunk")
+    if seq_lens is None:
+        raise ValueError("seq_lens must be int32 [batch]")
     windows = []
     for name, w, o, scheme in (("k_window", k_window, k_window_out, desc.k_scheme),
                                ("v_window", v_window, v_window_out, desc.v_scheme)):
-        if w is None and (o is not None or scheme == CHANNELWISE):
-            raise ValueError(f"{name} is required (a channel-wise group runs along the block's tokens)")
-        for n, x in ((name, w), (name + "_out", o)):
-            if x is not None:
-                _need(x, n, torch.float32)
-                if tuple(x.shape) != (B, desc.num_kv_heads, BLOCK_TOKENS, desc.head_dim):
-                    raise ValueError(f"{n} must be fp32 [batch, num_kv_heads, 128, head_dim]")
-        windows.append((w, w if o is None else o))
-    (kw, kwo), (vw, vwo) = windows
-    _check_status(dev_status)
-    _same_device(k_new.device, v_new=v_new, cu_seqlens=cu_seqlens, seq_lens=seq_lens, page_table=page_table,
-                 k_cache=k_cache, v_cache=v_cache, windows=(kw, kwo, vw, vwo), dev_status=dev_status)
-    with torch.cuda.device(k_new.device):
-        st = library().kvq_append_chunk(ctypes.byref(desc), _DTYPES[k_new.dtype], ctypes.byref(kr), ctypes.byref(vr),
-                                        B, T, _p(cu_seqlens), _p(seq_lens), _p(page_table), mb, _p(kw), _p(vw),
-                                        _p(kwo), _p(vwo), *(_p(t) for t in (*k_cache, *v_cache)), _p(dev_status),
-                                        _stream())
-    _lib.check(st, "kvq_append_chunk")
+        if w is None:
+            if o is not None or scheme == CHANNELWISE:
+                raise ValueError(f"{name} is required (a channel-wise group runs along the block's tokens)")
+            windows += [None, None]
+            continue
+        size = B * H * BLOCK_TOKENS * D
+        pw = _ptr(w, name, (torch.float32,), size, dev)
+        windows += [pw, pw if o is None else _ptr(o, name + "_out", (torch.float32,), size, dev)]
+    kw, kwo, vw, vwo = windows
+    _launch(dev, "kvq_append_chunk", library().kvq_append_chunk, ctypes.byref(desc), _DTYPES[k_new.dtype],
+            ctypes.byref(kr), ctypes.byref(vr), B, T, pcu, _ptr(seq_lens, "seq_lens", (torch.int32,), B, dev), pt, mb,
+            kw, vw, kwo, vwo, *_cache_ptrs(desc, "k_cache", k_cache, dev), *_cache_ptrs(desc, "v_cache", v_cache, dev),
+            _ptr(dev_status, "dev_status", _STATUS, 1, dev))
     return k_cache, v_cache
-
-
-def _chunk_desc(desc: CacheDesc, dtype, batch, total_tokens, num_q_heads, max_blocks, causal=True, sm_scale=0.0,
-                flags=0) -> ChunkDesc:
-    return ChunkDesc(desc, _DTYPES[dtype], batch, total_tokens, num_q_heads, max_blocks, int(bool(causal)), sm_scale,
-                     flags)
 
 
 def chunk_workspace_size(desc: CacheDesc, batch: int, total_tokens: int, num_q_heads: int, max_blocks: int) -> int:
     """Workspace bytes of a chunk_attn call with these sizes."""
-    d = _chunk_desc(desc, torch.bfloat16, batch, total_tokens, num_q_heads, max_blocks)
+    d = ChunkDesc(desc, _lib.BF16, batch, total_tokens, num_q_heads, max_blocks, 1, 0.0, 0)
     n = ctypes.c_size_t()
     _lib.check(library().kvq_chunk_workspace_size(ctypes.byref(d), ctypes.byref(n)), "kvq_chunk_workspace_size")
     return n.value
@@ -431,35 +467,24 @@ def chunk_attn(desc: CacheDesc, q: torch.Tensor, k_cache, v_cache, cu_seqlens: t
     [cu_seqlens[b], cu_seqlens[b + 1]), the last of them at position
     seq_lens[b] - 1.  Returns out [T, Hq, D] in q's type, and with return_lse
     (or an lse buffer) also lse fp32 [T, Hq].  Inference only."""
-    qr = _rows(q, "q", (torch.bfloat16, torch.float16), dim=desc.head_dim)
+    D = desc.head_dim
+    qr = _rows(q, "q", _HALF, None, None, D)
     T, Hq, _ = q.shape
-    B = _starts(cu_seqlens)
-    if page_table is not None:
-        mb = _geometry(B, 1, seq_lens, page_table, None)
-    else:
-        if max_blocks is None:
-            raise ValueError("max_blocks is required for a contiguous cache")
-        mb = int(max_blocks)
-    _need(seq_lens, "seq_lens", torch.int32, B)
-    cb, sb = cache_bytes(desc)
-    for name, cache in (("k_cache", k_cache), ("v_cache", v_cache)):
-        codes, scale, zero = cache
-        _need(codes, name + " codes", torch.uint8, cb)
-        _need(scale, name + " scale", (torch.float16, torch.int16, torch.uint16), sb // 2)
-        _need(zero, name + " zero", (torch.float16, torch.int16, torch.uint16), sb // 2)
-    _check_status(dev_status)
-    _same_device(q.device, cu_seqlens=cu_seqlens, seq_lens=seq_lens, page_table=page_table, k_cache=k_cache,
-                 v_cache=v_cache, out=out, lse=lse, workspace=workspace, dev_status=dev_status)
-    out, lse = _outputs(q, out, lse, return_lse)
-    d = _chunk_desc(desc, q.dtype, B, T, Hq, mb, causal, sm_scale, flags)
-    with torch.cuda.device(q.device):
-        if workspace is None:
-            n = ctypes.c_size_t()
-            _lib.check(library().kvq_chunk_workspace_size(ctypes.byref(d), ctypes.byref(n)), "kvq_chunk_workspace_size")
-            workspace = torch.empty(n.value, dtype=torch.uint8, device=q.device)
-        _need(workspace, "workspace", torch.uint8)
-        st = library().kvq_chunk_attn(ctypes.byref(d), ctypes.byref(qr), *(_p(t) for t in (*k_cache, *v_cache)),
-                                      _p(cu_seqlens), _p(seq_lens), _p(page_table), _p(out), _p(lse), _p(workspace),
-                                      workspace.numel(), _p(dev_status), _stream())
-    _lib.check(st, "kvq_chunk_attn")
+    dev = q.get_device()
+    B, pcu = _starts(cu_seqlens, dev)
+    mb, pt = _blocks_per_sequence(B, page_table, max_blocks, dev, "chunk_attn")
+    if seq_lens is None:
+        raise ValueError("seq_lens must be int32 [batch]")
+    pk, pv = _cache_ptrs(desc, "k_cache", k_cache, dev), _cache_ptrs(desc, "v_cache", v_cache, dev)
+    out, lse, po, pl = _outputs(q, T, Hq, D, out, lse, return_lse, dev)
+    d = ChunkDesc(desc, _DTYPES[q.dtype], B, T, Hq, mb, 1 if causal else 0, sm_scale, flags)
+    if workspace is None:
+        n = ctypes.c_size_t()
+        _lib.check(library().kvq_chunk_workspace_size(ctypes.byref(d), ctypes.byref(n)), "kvq_chunk_workspace_size")
+        workspace = torch.empty(n.value, dtype=torch.uint8, device=q.device)
+    size = workspace.numel()
+    _launch(dev, "kvq_chunk_attn", library().kvq_chunk_attn, ctypes.byref(d), ctypes.byref(qr), *pk, *pv, pcu,
+            _ptr(seq_lens, "seq_lens", (torch.int32,), B, dev), pt, po, pl,
+            _ptr(workspace, "workspace", (torch.uint8,), size, dev), size,
+            _ptr(dev_status, "dev_status", _STATUS, 1, dev))
     return out if lse is None else (out, lse)
