@@ -14,9 +14,9 @@
 // arithmetic per value stays below about ten instructions.  The code of a value
 // is clamp(rint(fl(fl(x - z) / s))) (IEEE fp32), taken without the division:
 // with d = fl(x - z) and r = fl(1 / s), q = d r is within 2^-22 of d / s
-// relatively, that is within 2^-18 for codes up to 15, so rint(q) is the code
-// unless q lies within 2^-16 of a half; a thread that meets such a value does
-// its values of that group again with the division.  q <= 2^b - 1 up to
+// relatively, that is within 2^-18 for codes up to 15 (and fl(d / s) within 2^-20 of d / s), so rint(q) is the code
+// unless q lies within 2^-18 of a half; a thread that meets such a value does
+// all its values again with the division.  q <= 2^b - 1 up to
 // rounding, because s was rounded up, and q >= 0, because z was rounded down.
 #include <cuda_fp16.h>
 
@@ -39,46 +39,72 @@ __device__ __forceinline__ float max_nan(float a, float b) {
 }
 
 struct Group {
-  float s, z, r;  // scale, offset, 1 / scale (0: every code is 0)
+  float s, z;  // s NaN: the group is refused (not finite, or past the fp16 range) and left zero
   uint16_t s_bits, z_bits;
-  bool ok;
 };
 // Scale and offset of a group with minimum mn and maximum mx (NaN where a
 // value is NaN; mn > mx: no value at all).
 __device__ __forceinline__ Group group_of_range(float mn, float mx, float qmax) {
-  Group g{0.f, 0.f, 0.f, 0, 0, true};
+  Group g{0.f, 0.f, 0, 0};
   if (mn > mx) return g;
   const __half zh = __float2half_rd(mn);
   const float z = __half2float(zh), width = __fsub_rn(mx, z);
   const __half sh = width != 0.f ? __float2half_ru(__fdiv_rn(width, qmax)) : __float2half_rn(0.f);
-  // not finite, or past the fp16 range (a NaN minimum or maximum gives a NaN here)
-  g.ok = fabsf(mn) < INFINITY && fabsf(mx) < INFINITY && !__hisinf(zh) && !__hisinf(sh);
-  if (!g.ok) return g;
-  g.s = __half2float(sh);
-  g.z = z;
-  g.r = g.s > 0.f ? __frcp_rn(g.s) : 0.f;
-  g.s_bits = __half_as_ushort(sh);
-  g.z_bits = __half_as_ushort(zh);
-  return g;
+  if (!(fabsf(mn) < INFINITY) || !(fabsf(mx) < INFINITY) || __hisinf(zh) || __hisinf(sh)) {
+    g.s = NAN;
+    return g;
+  }
+  return Group{__half2float(sh), z, __half_as_ushort(sh), __half_as_ushort(zh)};
 }
+// What the codes of a group are made with: its scale's reciprocal, 0 where
+// every code is 0.
+__device__ __forceinline__ float reciprocal(float s) { return s > 0.f ? __frcp_rn(s) : 0.f; }
 
 constexpr float kMagic = 12582912.f;       // 1.5 x 2^23: adding it leaves rint in the low bits
 constexpr uint32_t kMagicBits = 0x4b400000u;
 
-// The code of x plus kMagicBits; *far grows to the largest distance from an
-// integer met so far.
-__device__ __forceinline__ uint32_t code_fast(float x, float z, float r, float* far) {
+// The code of x plus kMagicBits.  Fast: *far grows to the largest distance
+// from an integer met so far.
+template <bool EXACT>
+__device__ __forceinline__ uint32_t code_of(float x, float s, float z, float r, float qmax, float* far) {
   const float d = __fsub_rn(x, z);
+  if (EXACT) {
+    if (!(s > 0.f)) return kMagicBits;
+    return kMagicBits + (uint32_t)fminf(fmaxf(rintf(__fdiv_rn(d, s)), 0.f), qmax);
+  }
   const float y = __fmaf_rn(d, r, kMagic);
   *far = fmaxf(*far, fabsf(__fmaf_rn(d, r, -__fsub_rn(y, kMagic))));
   return __float_as_uint(y);
 }
-__device__ __forceinline__ uint32_t code_exact(float x, float s, float z, float qmax) {
-  if (s == 0.f) return kMagicBits;
-  const float t = fminf(fmaxf(rintf(__fdiv_rn(__fsub_rn(x, z), s)), 0.f), qmax);
-  return kMagicBits + (uint32_t)t;
+struct Fast { static constexpr bool value = false; };
+struct Exact { static constexpr bool value = true; };
+constexpr float kNearHalf = 0.5f - 1.f / 262144.f;
+
+// Reductions over the lanes of a group of LG lanes for N values a lane at
+// once, halving the values held at each exchange: afterwards lane l of the
+// group holds value v[0], number l >> log2(LG / N) (LG >= N), or the N / LG
+// values from l * N / LG on.
+template <int N, bool MAX>
+__device__ __forceinline__ void reduce_group(float (&v)[N], int lg) {
+  int o = lg >> 1;
+#pragma unroll
+  for (int n = N; n > 1; n >>= 1) {
+    if (o > 0) {
+      const bool upper = (threadIdx.x & o) != 0;
+#pragma unroll
+      for (int i = 0; i < n / 2; ++i) {
+        const float keep = upper ? v[i + n / 2] : v[i];
+        const float got = __shfl_xor_sync(0xffffffffu, upper ? v[i] : v[i + n / 2], o);
+        v[i] = MAX ? max_nan(keep, got) : min_nan(keep, got);
+      }
+      o >>= 1;
+    }
+  }
+  for (; o > 0; o >>= 1) {
+    const float got = __shfl_xor_sync(0xffffffffu, v[0], o);
+    v[0] = MAX ? max_nan(v[0], got) : min_nan(v[0], got);
+  }
 }
-constexpr float kNearHalf = 0.5f - 1.f / 65536.f;
 
 // Four neighbouring values at `at` (elements).
 template <typename T>
@@ -123,7 +149,9 @@ __global__ void __launch_bounds__(kThreads, 2) append_chunk_kernel(const AppendP
   constexpr float kMax = (float)((1 << BITS) - 1);
   // packed block: K [chunk][128 tokens], V [chunk][W channels], a piece of padding per chunk against bank conflicts
   __shared__ __align__(16) unsigned char packed[(kPieces + W * BITS / 64 + 8) * 16];
-  __shared__ float lo_s[kWarps][W], hi_s[kWarps][W];  // channel-wise: ranges per warp, then s / z (as [group][W])
+  // channel-wise: ranges per warp, then s / z (as [group][W]); token-wise: s, z of every (token, group)
+  __shared__ __align__(16) float ranges[2][kWarps][W];
+  float(*lo_s)[W] = ranges[0], (*hi_s)[W] = ranges[1];
   __shared__ __align__(16) uint16_t s_out[128 * 4], z_out[128 * 4];
   __shared__ int warp_sum[kWarps], found[4];
   const int D = p.head_dim;
@@ -242,62 +270,82 @@ __global__ void __launch_bounds__(kThreads, 2) append_chunk_kernel(const AppendP
   const int nsz = kBlockTokens * D / G;
   const size_t blk = (size_t)page * p.num_kv_heads + h;
 
-  // K, one token of this thread: 4 codes (with kMagicBits each) -> their 16 or 8 bits of the token's row
-  auto put_k = [&](int t, uint32_t a, uint32_t bb, uint32_t c, uint32_t d) {
-    const uint32_t w = (a - kMagicBits) | (bb - kMagicBits) << BITS | (c - kMagicBits) << 2 * BITS |
-                       (d - kMagicBits) << 3 * BITS;
+  // Where codes go.  K, one token: the thread's 4 codes are 16 (8) bits of the
+  // token's row; kMagicBits is zero there, so the codes are summed in place.
+  auto put_k = [&](int t, const uint32_t (&y)[4]) {
+    const uint32_t w = y[0] + (y[1] << BITS) + (y[2] << 2 * BITS) + (y[3] << 3 * BITS);
     unsigned char* at = packed + ((ch / kPer) * 129 + t) * 16 + (ch % kPer) * BITS / 8;
     if (BITS == 4) *reinterpret_cast<uint16_t*>(at) = (uint16_t)w;
     else *at = (unsigned char)w;
   };
-  // V, one channel of this thread: kTok codes of BITS bits along the row
-  auto put_v = [&](int c, uint64_t w) {
-    unsigned char* at = packed + ((tok / kPer) * (W + 1) + ch + c) * 16 + (tok % kPer) * BITS / 8;
-    if (kTok * BITS == 64) *reinterpret_cast<uint64_t*>(at) = w;
-    else if (kTok * BITS == 32) *reinterpret_cast<uint32_t*>(at) = (uint32_t)w;
-    else *reinterpret_cast<uint16_t*>(at) = (uint16_t)w;
+  // V, one channel: kTok codes along the row, up to 32 bits to a word.
+  constexpr int kWordTok = 32 / BITS < kTok ? 32 / BITS : kTok, kWords = kTok / kWordTok;
+  constexpr uint32_t kWordMagic = [] {
+    uint32_t m = 0;
+    for (int i = 0; i < kWordTok; ++i) m += kMagicBits << (i * BITS);
+    return m;
+  }();
+  auto put_v = [&](const uint32_t (&acc)[kWords][4]) {
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+      unsigned char* at = packed + ((tok / kPer) * (W + 1) + ch + c) * 16 + (tok % kPer) * BITS / 8;
+      if (kWords == 2) *reinterpret_cast<uint2*>(at) = make_uint2(acc[0][c] - kWordMagic, acc[kWords - 1][c] - kWordMagic);
+      else if (kTok * BITS == 32) *reinterpret_cast<uint32_t*>(at) = acc[0][c] - kWordMagic;
+      else *reinterpret_cast<uint16_t*>(at) = (uint16_t)(acc[0][c] - kWordMagic);
+    }
   };
-  uint64_t vw[4] = {0, 0, 0, 0};  // V: the thread's codes so far, per channel
-  auto add_v = [&](int c, int i, uint32_t y) { vw[c] |= (uint64_t)(y - kMagicBits) << (i * BITS); };
+  float far = 0.f;
 
   if (tokenwise) {
-    const int glanes = G / 4;  // lanes of a group
+    // ranges of the thread's tokens over its 4 channels, then over the group's lanes
+    const int lg = G / 4, gl = lane & (lg - 1);  // lanes of a group, place in it
+    float mn[kTok], mx[kTok];
 #pragma unroll
     for (int i = 0; i < kTok; ++i) {
-      const int t = tok + i;
-      float mn = min_nan(min_nan(x[i][0], x[i][1]), min_nan(x[i][2], x[i][3]));
-      float mx = max_nan(max_nan(x[i][0], x[i][1]), max_nan(x[i][2], x[i][3]));
-      for (int o = 1; o < glanes; o <<= 1) {
-        mn = min_nan(mn, __shfl_xor_sync(0xffffffffu, mn, o));
-        mx = max_nan(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-      }
-      const bool live = t >= from && t < nv;
-      Group g = group_of_range(mn, mx, kMax);
-      if (!live) g = Group{0.f, 0.f, 0.f, 0, 0, true};
-      const bool first = ch % G == 0;
-      if (!g.ok && first) report(p.dev_status, KVQ_DEV_NONFINITE);
-      if (first) {
-        s_out[t * gps + ch / G] = g.s_bits;
-        z_out[t * gps + ch / G] = g.z_bits;
-      }
-      uint32_t y[4];
-      float far = 0.f;
+      mn[i] = min_nan(min_nan(x[i][0], x[i][1]), min_nan(x[i][2], x[i][3]));
+      mx[i] = max_nan(max_nan(x[i][0], x[i][1]), max_nan(x[i][2], x[i][3]));
+    }
+    reduce_group<kTok, false>(mn, lg);
+    reduce_group<kTok, true>(mx, lg);
+    float2* sz = reinterpret_cast<float2*>(ranges);  // [token][group]: at most 128 x W / 32 pairs, 4 W floats of 16 W
+    const int each = kTok / lg > 1 ? kTok / lg : 1, share = lg / kTok > 1 ? lg / kTok : 1;
 #pragma unroll
-      for (int c = 0; c < 4; ++c) y[c] = code_fast(x[i][c], g.z, g.r, &far);
-      if (!(far < kNearHalf)) {
-#pragma unroll
-        for (int c = 0; c < 4; ++c) y[c] = code_exact(x[i][c], g.s, g.z, kMax);
-      }
-      if (g.r == 0.f) y[0] = y[1] = y[2] = y[3] = kMagicBits;  // width zero, not finite, or no token
-      if (which == 0) {
-        put_k(t, y[0], y[1], y[2], y[3]);
-      } else {
-#pragma unroll
-        for (int c = 0; c < 4; ++c) add_v(c, i, y[c]);
+    for (int k = 0; k < 2; ++k) {
+      if (k < each && gl % share == 0) {
+        const int t = tok + (each > 1 ? gl * each + k : gl / share);
+        const bool live = t >= from && t < nv;
+        const Group g = live ? group_of_range(mn[k], mx[k], kMax) : Group{0.f, 0.f, 0, 0};
+        if (isnan(g.s)) report(p.dev_status, KVQ_DEV_NONFINITE);
+        const int e = t * gps + ch / G;
+        sz[e] = make_float2(g.s, g.z);
+        s_out[e] = g.s_bits;
+        z_out[e] = g.z_bits;
       }
     }
+    __syncwarp();  // a group's lanes are one warp's
+    auto emit = [&](auto exact) {
+      uint32_t acc[kWords][4] = {};
+#pragma unroll
+      for (int i = 0; i < kTok; ++i) {
+        const float2 g = sz[(tok + i) * gps + ch / G];
+        const float r = reciprocal(g.x);
+        if (isnan(g.x)) far = 1.f;
+        uint32_t y[4];
+#pragma unroll
+        for (int c = 0; c < 4; ++c) y[c] = code_of<decltype(exact)::value>(x[i][c], g.x, g.y, r, kMax, &far);
+        if (which == 0) {
+          put_k(tok + i, y);
+        } else {
+#pragma unroll
+          for (int c = 0; c < 4; ++c) acc[i / kWordTok][c] += y[c] << (i % kWordTok * BITS);
+        }
+      }
+      if (which == 1) put_v(acc);
+    };
+    emit(Fast{});
+    if (!(far < kNearHalf)) emit(Exact{});
   } else {
-    // ranges of this thread's tokens per channel, then across the warps (and
+    // ranges of the thread's tokens per channel, then across the warps (and
     // half-warps) of the group's tokens
     float mn[4], mx[4];
 #pragma unroll
@@ -338,7 +386,7 @@ __global__ void __launch_bounds__(kThreads, 2) append_chunk_kernel(const AppendP
           z = max_nan(z, hi_s[w][c]);
         }
         mine[k] = group_of_range(a, z, kMax);
-        if (!mine[k].ok) report(p.dev_status, KVQ_DEV_NONFINITE);
+        if (isnan(mine[k].s)) report(p.dev_status, KVQ_DEV_NONFINITE);
         s_out[e] = mine[k].s_bits;
         z_out[e] = mine[k].z_bits;
       }
@@ -357,38 +405,38 @@ __global__ void __launch_bounds__(kThreads, 2) append_chunk_kernel(const AppendP
     const float4 s4 = *reinterpret_cast<const float4*>(&lo_s[g][ch]);
     const float4 z4 = *reinterpret_cast<const float4*>(&hi_s[g][ch]);
     const float sc[4] = {s4.x, s4.y, s4.z, s4.w}, zc[4] = {z4.x, z4.y, z4.z, z4.w};
-    float rc[4], far = 0.f;
+    float rc[4];
 #pragma unroll
-    for (int c = 0; c < 4; ++c) rc[c] = sc[c] > 0.f ? __frcp_rn(sc[c]) : 0.f;
-    uint32_t y[kTok][4];
-#pragma unroll
-    for (int i = 0; i < kTok; ++i) {
-      const bool live = tok + i < nv;
-#pragma unroll
-      for (int c = 0; c < 4; ++c) {
-        // a channel whose codes are all zero takes z for its values
-        y[i][c] = code_fast(live && sc[c] > 0.f ? x[i][c] : zc[c], zc[c], rc[c], &far);
-      }
+    for (int c = 0; c < 4; ++c) {
+      rc[c] = reciprocal(sc[c]);
+      if (isnan(sc[c])) far = 1.f;
     }
-    if (!(far < kNearHalf)) {
+    if (nv < kBlockTokens) {  // tokens past the end have code 0
 #pragma unroll
       for (int i = 0; i < kTok; ++i)
+        if (tok + i >= nv) {
 #pragma unroll
-        for (int c = 0; c < 4; ++c) y[i][c] = tok + i < nv ? code_exact(x[i][c], sc[c], zc[c], kMax) : kMagicBits;
+          for (int c = 0; c < 4; ++c) x[i][c] = zc[c];
+        }
     }
+    auto emit = [&](auto exact) {
+      uint32_t acc[kWords][4] = {};
 #pragma unroll
-    for (int i = 0; i < kTok; ++i) {
-      if (which == 0) {
-        put_k(tok + i, y[i][0], y[i][1], y[i][2], y[i][3]);
-      } else {
+      for (int i = 0; i < kTok; ++i) {
+        uint32_t y[4];
 #pragma unroll
-        for (int c = 0; c < 4; ++c) add_v(c, i, y[i][c]);
+        for (int c = 0; c < 4; ++c) y[c] = code_of<decltype(exact)::value>(x[i][c], sc[c], zc[c], rc[c], kMax, &far);
+        if (which == 0) {
+          put_k(tok + i, y);
+        } else {
+#pragma unroll
+          for (int c = 0; c < 4; ++c) acc[i / kWordTok][c] += y[c] << (i % kWordTok * BITS);
+        }
       }
-    }
-  }
-  if (which == 1) {
-#pragma unroll
-    for (int c = 0; c < 4; ++c) put_v(c, vw[c]);
+      if (which == 1) put_v(acc);
+    };
+    emit(Fast{});
+    if (!(far < kNearHalf)) emit(Exact{});
   }
   __syncthreads();
 
