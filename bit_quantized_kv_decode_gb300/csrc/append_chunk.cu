@@ -12,15 +12,20 @@
 //
 // The work is one pass over the rows: it is bound by memory where the
 // arithmetic per value stays below about ten instructions.  The code of a value
-// is clamp(rint(fl(fl(x - z) / s))) (IEEE fp32), taken without the division:
-// with d = fl(x - z) and r = fl(1 / s), q = d r is within 2^-22 of d / s
-// relatively, that is within 2^-18 for codes up to 15 (and fl(d / s) within 2^-20 of d / s), so rint(q) is the code
-// unless q lies within 2^-18 of a half; a thread that meets such a value does
-// all its values again with the division.  q <= 2^b - 1 up to
-// rounding, because s was rounded up, and q >= 0, because z was rounded down.
+// is clamp(rint(fl(fl(x - z) / s))) in IEEE fp32.  With d = fl(x - z) and
+// r = fl(1 / s) once per group, the quotient is corrected once after
+// Markstein ("Computation of elementary functions on the IBM RISC System/6000
+// processor", 1990): q = fl(d r), q' = fma(fma(-q, s, d), r, q) is fl(d / s),
+// since s, an fp16 number, has no all-ones fp32 significand (checked for every
+// s and the 13 fp32 numbers nearest to each half of a code); adding 1.5 x 2^23
+// then rounds it to the nearest even integer.  No clamp is needed: q' >= 0,
+// because z was rounded down, and at most 2^b - 1 up to rounding, because s
+// was rounded up.  (Deciding by d r alone and dividing where it lies near a
+// half was slower: coarse 16-bit values meet exact halves 0.07% of the time,
+// in three warps of four.)
 #include <cuda_fp16.h>
 
-#include "attn_rows.h"
+#include "attn_core.cuh"
 
 namespace kvq {
 namespace {
@@ -60,25 +65,19 @@ __device__ __forceinline__ Group group_of_range(float mn, float mx, float qmax) 
 // every code is 0.
 __device__ __forceinline__ float reciprocal(float s) { return s > 0.f ? __frcp_rn(s) : 0.f; }
 
-constexpr float kMagic = 12582912.f;       // 1.5 x 2^23: adding it leaves rint in the low bits
+constexpr float kMagic = 12582912.f;  // 1.5 x 2^23: adding it leaves rint in the low bits
 constexpr uint32_t kMagicBits = 0x4b400000u;
 
-// The code of x plus kMagicBits.  Fast: *far grows to the largest distance
-// from an integer met so far.
-template <bool EXACT>
-__device__ __forceinline__ uint32_t code_of(float x, float s, float z, float r, float qmax, float* far) {
-  const float d = __fsub_rn(x, z);
-  if (EXACT) {
-    if (!(s > 0.f)) return kMagicBits;
-    return kMagicBits + (uint32_t)fminf(fmaxf(rintf(__fdiv_rn(d, s)), 0.f), qmax);
-  }
-  const float y = __fmaf_rn(d, r, kMagic);
-  *far = fmaxf(*far, fabsf(__fmaf_rn(d, r, -__fsub_rn(y, kMagic))));
-  return __float_as_uint(y);
+// The codes of two values plus kMagicBits (r = 0: zero): the fp32 pipe takes
+// pairs, each half rounded as by itself.  zn, sn: -z, -s.
+__device__ __forceinline__ void code_pair(float x0, float x1, uint64_t sn, uint64_t zn, uint64_t r, uint32_t& y0,
+                                          uint32_t& y1) {
+  const uint64_t d = rows::add2(rows::pair(x0, x1), zn), q = rows::mul2(d, r);
+  float a, b;
+  rows::unpair(rows::add2(rows::fma2(rows::fma2(q, sn, d), r, q), rows::pair(kMagic, kMagic)), a, b);
+  y0 = __float_as_uint(a);
+  y1 = __float_as_uint(b);
 }
-struct Fast { static constexpr bool value = false; };
-struct Exact { static constexpr bool value = true; };
-constexpr float kNearHalf = 0.5f - 1.f / 262144.f;
 
 // Reductions over the lanes of a group of LG lanes for N values a lane at
 // once, halving the values held at each exchange: afterwards lane l of the
@@ -218,18 +217,29 @@ __global__ void __launch_bounds__(kThreads, 2) append_chunk_kernel(const AppendP
   float x[kTok][4];
   {
     Raw<T> raw[kTok];
+    if (from == 0 && nv == kBlockTokens) {  // a whole block of new tokens, as most are
 #pragma unroll
-    for (int i = 0; i < kTok; ++i) {
-      const int t = tok + i;
-      if (t >= from && t < nv) raw[i].load(rows.data, (long long)(s.first + t0 + t - len) * rows.st + at0);
-    }
+      for (int i = 0; i < kTok; ++i)
+        raw[i].load(rows.data, (long long)(s.first + t0 + tok + i - len) * rows.st + at0);
 #pragma unroll
-    for (int i = 0; i < kTok; ++i) {
-      const int t = tok + i;
-      float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-      if (t >= from && t < nv) v = raw[i].get();
-      else if (t < from && !tokenwise) v = *reinterpret_cast<const float4*>(win + (size_t)t * D + ch);
-      x[i][0] = v.x; x[i][1] = v.y; x[i][2] = v.z; x[i][3] = v.w;
+      for (int i = 0; i < kTok; ++i) {
+        const float4 v = raw[i].get();
+        x[i][0] = v.x; x[i][1] = v.y; x[i][2] = v.z; x[i][3] = v.w;
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < kTok; ++i) {
+        const int t = tok + i;
+        if (t >= from && t < nv) raw[i].load(rows.data, (long long)(s.first + t0 + t - len) * rows.st + at0);
+      }
+#pragma unroll
+      for (int i = 0; i < kTok; ++i) {
+        const int t = tok + i;
+        float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (t >= from && t < nv) v = raw[i].get();
+        else if (t < from && !tokenwise) v = *reinterpret_cast<const float4*>(win + (size_t)t * D + ch);
+        x[i][0] = v.x; x[i][1] = v.y; x[i][2] = v.z; x[i][3] = v.w;
+      }
     }
   }
 
@@ -294,8 +304,6 @@ __global__ void __launch_bounds__(kThreads, 2) append_chunk_kernel(const AppendP
       else *reinterpret_cast<uint16_t*>(at) = (uint16_t)(acc[0][c] - kWordMagic);
     }
   };
-  float far = 0.f;
-
   if (tokenwise) {
     // ranges of the thread's tokens over its 4 channels, then over the group's lanes
     const int lg = G / 4, gl = lane & (lg - 1);  // lanes of a group, place in it
@@ -307,7 +315,8 @@ __global__ void __launch_bounds__(kThreads, 2) append_chunk_kernel(const AppendP
     }
     reduce_group<kTok, false>(mn, lg);
     reduce_group<kTok, true>(mx, lg);
-    float2* sz = reinterpret_cast<float2*>(ranges);  // [token][group]: at most 128 x W / 32 pairs, 4 W floats of 16 W
+    float4* sz = reinterpret_cast<float4*>(ranges);  // [token][group] s, z, 1 / s: at most 128 x W / 32 of them
+    static_assert(sizeof(ranges) == 128 * (W / 32) * sizeof(float4), "table");
     const int each = kTok / lg > 1 ? kTok / lg : 1, share = lg / kTok > 1 ? lg / kTok : 1;
 #pragma unroll
     for (int k = 0; k < 2; ++k) {
@@ -317,33 +326,32 @@ __global__ void __launch_bounds__(kThreads, 2) append_chunk_kernel(const AppendP
         const Group g = live ? group_of_range(mn[k], mx[k], kMax) : Group{0.f, 0.f, 0, 0};
         if (isnan(g.s)) report(p.dev_status, KVQ_DEV_NONFINITE);
         const int e = t * gps + ch / G;
-        sz[e] = make_float2(g.s, g.z);
+        sz[e] = make_float4(g.s, g.z, reciprocal(g.s), 0.f);
         s_out[e] = g.s_bits;
         z_out[e] = g.z_bits;
       }
     }
     __syncwarp();  // a group's lanes are one warp's
-    auto emit = [&](auto exact) {
-      uint32_t acc[kWords][4] = {};
+    uint32_t acc[kWords][4] = {};
 #pragma unroll
-      for (int i = 0; i < kTok; ++i) {
-        const float2 g = sz[(tok + i) * gps + ch / G];
-        const float r = reciprocal(g.x);
-        if (isnan(g.x)) far = 1.f;
-        uint32_t y[4];
-#pragma unroll
-        for (int c = 0; c < 4; ++c) y[c] = code_of<decltype(exact)::value>(x[i][c], g.x, g.y, r, kMax, &far);
-        if (which == 0) {
-          put_k(tok + i, y);
-        } else {
-#pragma unroll
-          for (int c = 0; c < 4; ++c) acc[i / kWordTok][c] += y[c] << (i % kWordTok * BITS);
-        }
+    for (int i = 0; i < kTok; ++i) {
+      float4 g = sz[(tok + i) * gps + ch / G];
+      if (isnan(g.x)) {
+        g.x = 0.f;
+        x[i][0] = x[i][1] = x[i][2] = x[i][3] = 0.f;
       }
-      if (which == 1) put_v(acc);
-    };
-    emit(Fast{});
-    if (!(far < kNearHalf)) emit(Exact{});
+      uint32_t y[4];
+      const uint64_t sn = rows::pair(-g.x, -g.x), zn = rows::pair(-g.y, -g.y), r = rows::pair(g.z, g.z);
+      code_pair(x[i][0], x[i][1], sn, zn, r, y[0], y[1]);
+      code_pair(x[i][2], x[i][3], sn, zn, r, y[2], y[3]);
+      if (which == 0) {
+        put_k(tok + i, y);
+      } else {
+#pragma unroll
+        for (int c = 0; c < 4; ++c) acc[i / kWordTok][c] += y[c] << (i % kWordTok * BITS);
+      }
+    }
+    if (which == 1) put_v(acc);
   } else {
     // ranges of the thread's tokens per channel, then across the warps (and
     // half-warps) of the group's tokens
@@ -353,15 +361,24 @@ __global__ void __launch_bounds__(kThreads, 2) append_chunk_kernel(const AppendP
       mn[c] = INFINITY;
       mx[c] = -INFINITY;
     }
+    if (tok + kTok <= nv) {
 #pragma unroll
-    for (int i = 0; i < kTok; ++i) {
-      if (tok + i < nv) {
+      for (int i = 0; i < kTok; ++i)
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
           mn[c] = min_nan(mn[c], x[i][c]);
           mx[c] = max_nan(mx[c], x[i][c]);
         }
-      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < kTok; ++i)
+        if (tok + i < nv) {
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            mn[c] = min_nan(mn[c], x[i][c]);
+            mx[c] = max_nan(mx[c], x[i][c]);
+          }
+        }
     }
     if (kLanes < 32) {  // both halves of the warp hold the same channels
 #pragma unroll
@@ -404,12 +421,23 @@ __global__ void __launch_bounds__(kThreads, 2) append_chunk_kernel(const AppendP
     const int g = warp * 16 / G;
     const float4 s4 = *reinterpret_cast<const float4*>(&lo_s[g][ch]);
     const float4 z4 = *reinterpret_cast<const float4*>(&hi_s[g][ch]);
-    const float sc[4] = {s4.x, s4.y, s4.z, s4.w}, zc[4] = {z4.x, z4.y, z4.z, z4.w};
-    float rc[4];
+    float sc[4] = {s4.x, s4.y, s4.z, s4.w}, rc[4];
+    const float zc[4] = {z4.x, z4.y, z4.z, z4.w};
 #pragma unroll
     for (int c = 0; c < 4; ++c) {
+      if (isnan(sc[c])) {
+        sc[c] = 0.f;
+#pragma unroll
+        for (int i = 0; i < kTok; ++i) x[i][c] = 0.f;
+      }
       rc[c] = reciprocal(sc[c]);
-      if (isnan(sc[c])) far = 1.f;
+    }
+    uint64_t sn[2], zn[2], r2[2];
+#pragma unroll
+    for (int c = 0; c < 2; ++c) {
+      sn[c] = rows::pair(-sc[2 * c], -sc[2 * c + 1]);
+      zn[c] = rows::pair(-zc[2 * c], -zc[2 * c + 1]);
+      r2[c] = rows::pair(rc[2 * c], rc[2 * c + 1]);
     }
     if (nv < kBlockTokens) {  // tokens past the end have code 0
 #pragma unroll
@@ -419,24 +447,20 @@ __global__ void __launch_bounds__(kThreads, 2) append_chunk_kernel(const AppendP
           for (int c = 0; c < 4; ++c) x[i][c] = zc[c];
         }
     }
-    auto emit = [&](auto exact) {
-      uint32_t acc[kWords][4] = {};
+    uint32_t acc[kWords][4] = {};
 #pragma unroll
-      for (int i = 0; i < kTok; ++i) {
-        uint32_t y[4];
+    for (int i = 0; i < kTok; ++i) {
+      uint32_t y[4];
 #pragma unroll
-        for (int c = 0; c < 4; ++c) y[c] = code_of<decltype(exact)::value>(x[i][c], sc[c], zc[c], rc[c], kMax, &far);
-        if (which == 0) {
-          put_k(tok + i, y);
-        } else {
+      for (int c = 0; c < 4; c += 2) code_pair(x[i][c], x[i][c + 1], sn[c / 2], zn[c / 2], r2[c / 2], y[c], y[c + 1]);
+      if (which == 0) {
+        put_k(tok + i, y);
+      } else {
 #pragma unroll
-          for (int c = 0; c < 4; ++c) acc[i / kWordTok][c] += y[c] << (i % kWordTok * BITS);
-        }
+        for (int c = 0; c < 4; ++c) acc[i / kWordTok][c] += y[c] << (i % kWordTok * BITS);
       }
-      if (which == 1) put_v(acc);
-    };
-    emit(Fast{});
-    if (!(far < kNearHalf)) emit(Exact{});
+    }
+    if (which == 1) put_v(acc);
   }
   __syncthreads();
 
