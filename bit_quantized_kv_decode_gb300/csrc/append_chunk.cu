@@ -7,8 +7,15 @@
 // rows are read as 8-byte (fp32: 16-byte) pieces of full lines, a channel-wise
 // group is reduced in registers and across warps, a token-wise one across the
 // lanes that share the token, and V's codes, packed along tokens, come out of
-// one thread's registers as whole 32- or 64-bit words.  The packed block is
-// put together in shared memory and written in 16-byte pieces.
+// one thread's registers as whole words.  The packed block is put together in
+// shared memory and written in 16-byte pieces.
+//
+// Two kernels.  append_blocks_kernel takes the blocks that consist of new
+// 16-bit tokens alone: the tile stays in its 16-bit form (half the registers,
+// so more loads in flight), ranges are formed on 16-bit pairs.
+// append_edges_kernel takes the rest in fp32 -- the first and last block of a
+// chunk, with the window's rows and the tokens that stay, and every block of
+// fp32 rows.  They write disjoint places and run side by side.
 //
 // The work is one pass over the rows: it is bound by memory where the
 // arithmetic per value stays below about ten instructions.  The code of a value
@@ -30,7 +37,7 @@
 namespace kvq {
 namespace {
 
-constexpr int kThreads = 256, kWarps = 8;
+constexpr int kThreads = 256, kWarps = 8, kWarpTok = kBlockTokens / kWarps;  // tokens of a warp
 
 __device__ __forceinline__ float min_nan(float a, float b) {
   float r;
@@ -139,10 +146,110 @@ struct Raw<__half> : Raw16 {
   }
 };
 
-template <typename T, int BITS, int W>  // W: channels of the slab
-__global__ void __launch_bounds__(kThreads, 2) append_chunk_kernel(const AppendParams p) {
+// Tokens of sequence b's chunk and of its cache; a bad entry has no blocks.
+struct Chunk {
+  SeqRows rows;
+  int len;
+  bool bad;
+};
+__device__ __forceinline__ Chunk load_chunk(const AppendParams& p, int b) {
+  Chunk c;
+  c.rows = seq_rows(p.cu, b, p.total);
+  c.len = p.seq_lens[b];
+  c.bad = c.rows.bad || c.len < 0 || (long long)c.len + c.rows.n > (long long)p.max_blocks * kBlockTokens;
+  return c;
+}
+// Blocks of a sequence that a kernel takes, in order.  Whole: those of new
+// tokens alone.  Edges: the others (one for an empty chunk: its window).
+__device__ __forceinline__ int whole_blocks(const Chunk& c) {
+  return c.bad ? 0 : max(0, (c.len + c.rows.n) / kBlockTokens - (c.len + kBlockTokens - 1) / kBlockTokens);
+}
+__device__ __forceinline__ int touched_blocks(const Chunk& c) {
+  return c.bad ? 0 : c.rows.n == 0 ? 1 : (c.len + c.rows.n - 1) / kBlockTokens - c.len / kBlockTokens + 1;
+}
+enum Part { kWhole, kEdges, kEvery };
+template <Part PART>
+__device__ __forceinline__ int part_blocks(const Chunk& c) {
+  return PART == kWhole ? whole_blocks(c) : PART == kEdges ? touched_blocks(c) - whole_blocks(c) : touched_blocks(c);
+}
+
+// The sequence and block of the rank-th block that the kernel takes, by one
+// warp: found[0] = sequence (-1: none), found[1] = block, counted from the
+// sequence's first touched one.
+template <Part PART>
+__device__ __forceinline__ void find_block(const AppendParams& p, int rank, bool report_bad, int* found) {
+  const int lane = threadIdx.x & 31;
+  if (lane == 0) found[0] = -1;
+  __syncwarp();
+  for (int b0 = 0; b0 < p.batch; b0 += 32) {
+    const int b = b0 + lane;
+    Chunk c{};
+    c.bad = true;
+    int blocks = 0;
+    if (b < p.batch) {
+      c = load_chunk(p, b);
+      if (c.bad && report_bad) report(p.dev_status, KVQ_DEV_BAD_SEQ_LEN);
+      blocks = part_blocks<PART>(c);
+    }
+    int incl = blocks;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int v = __shfl_up_sync(0xffffffffu, incl, o);
+      if (lane >= o) incl += v;
+    }
+    const int i = rank - (incl - blocks);
+    if (i >= 0 && i < blocks) {
+      found[0] = b;
+      const int whole = whole_blocks(c), lead = c.len % kBlockTokens != 0 ? 1 : 0;  // an edge before the whole ones?
+      found[1] = PART == kWhole ? lead + i : PART == kEdges && i >= lead ? i + whole : i;
+    }
+    const int all = __shfl_sync(0xffffffffu, incl, 31);
+    if (rank < all && !report_bad) break;  // (the reporting CTA looks at every sequence)
+    rank -= all;
+  }
+}
+
+// Channel-wise groups of a tile, by the whole block: the warps' ranges in
+// `ranges` ([low, high][warp][channel]) become scales and offsets ([s,
+// z][token group][channel]); their 16-bit forms go to s_out, z_out.
+template <int BITS, int W>
+__device__ __forceinline__ void channel_groups(float (*ranges)[kWarps][W], int groups, int gw, uint16_t* s_out,
+                                               uint16_t* z_out, uint32_t* dev_status) {
+  const int tid = threadIdx.x;
+  Group mine[2];  // groups * W / 256 <= 2 of a thread
+  __syncthreads();
+#pragma unroll
+  for (int k = 0; k < 2; ++k) {
+    const int e = tid + k * kThreads;
+    if (e < groups * W) {
+      const int g = e / W, c = e % W;
+      float a = INFINITY, z = -INFINITY;
+      for (int w = g * gw; w < (g + 1) * gw; ++w) {
+        a = min_nan(a, ranges[0][w][c]);
+        z = max_nan(z, ranges[1][w][c]);
+      }
+      mine[k] = group_of_range(a, z, (float)((1 << BITS) - 1));
+      if (isnan(mine[k].s)) report(dev_status, KVQ_DEV_NONFINITE);
+      s_out[e] = mine[k].s_bits;
+      z_out[e] = mine[k].z_bits;
+    }
+  }
+  __syncthreads();
+#pragma unroll
+  for (int k = 0; k < 2; ++k) {
+    const int e = tid + k * kThreads;
+    if (e < groups * W) {
+      ranges[0][e / W][e % W] = mine[k].s;
+      ranges[1][e / W][e % W] = mine[k].z;
+    }
+  }
+  __syncthreads();
+}
+
+template <typename T, int BITS, int W, Part PART>  // W: channels of the slab
+__device__ __forceinline__ void append_edge(const AppendParams& p) {
   constexpr int kLanes = W / 4;                 // lanes that share a token
-  constexpr int kTok = 16 * kLanes / 32;        // tokens of a thread (16 or 8)
+  constexpr int kTok = kWarpTok * kLanes / 32;  // tokens of a thread (16 or 8)
   constexpr int kPer = 128 / BITS;              // codes of a 16-byte piece
   constexpr int kPieces = W * BITS;             // 16-byte pieces of the slab's block: 128 W BITS / 128
   constexpr float kMax = (float)((1 << BITS) - 1);
@@ -152,52 +259,13 @@ __global__ void __launch_bounds__(kThreads, 2) append_chunk_kernel(const AppendP
   __shared__ __align__(16) float ranges[2][kWarps][W];
   float(*lo_s)[W] = ranges[0], (*hi_s)[W] = ranges[1];
   __shared__ __align__(16) uint16_t s_out[128 * 4], z_out[128 * 4];
-  __shared__ int warp_sum[kWarps], found[4];
+  __shared__ int found[2];
   const int D = p.head_dim;
   const int h = blockIdx.y, which = blockIdx.z & 1, slab = blockIdx.z >> 1;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const bool lead = h == 0 && blockIdx.z == 0;
-
-  // ---- which sequence and block: a scan over the blocks that the sequences touch
-  {
-    int rank = blockIdx.x;
-    if (tid == 0) found[0] = -1;
-    for (int b0 = 0; b0 < p.batch; b0 += kThreads) {
-      const int b = b0 + tid;
-      int blocks = 0, len = 0;
-      SeqRows s{0, 0, false};
-      bool bad = false;
-      if (b < p.batch) {
-        s = seq_rows(p.cu, b, p.total);
-        len = p.seq_lens[b];
-        bad = s.bad || len < 0 || (long long)len + s.n > (long long)p.max_blocks * kBlockTokens;
-        blocks = bad ? 0 : s.n == 0 ? 1 : (len + s.n - 1) / kBlockTokens - len / kBlockTokens + 1;
-        if (bad && lead && blockIdx.x == 0) report(p.dev_status, KVQ_DEV_BAD_SEQ_LEN);
-      }
-      int incl = blocks;
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const int v = __shfl_up_sync(0xffffffffu, incl, o);
-        if (lane >= o) incl += v;
-      }
-      if (lane == 31) warp_sum[warp] = incl;
-      __syncthreads();
-      int before = 0, all = 0;
-#pragma unroll
-      for (int w = 0; w < kWarps; ++w) {
-        if (w < warp) before += warp_sum[w];
-        all += warp_sum[w];
-      }
-      const int i = rank - (before + incl - blocks);  // block of sequence b
-      if (i >= 0 && i < blocks) {
-        found[0] = b;
-        found[1] = i;
-      }
-      __syncthreads();
-      if (rank < all) break;
-      rank -= all;
-    }
-  }
+  if (warp == 0) find_block<PART>(p, blockIdx.x, lead && blockIdx.x == 0, found);
+  __syncthreads();
   const int b = found[0], nth = found[1];
   if (b < 0) return;
   const SeqRows s = seq_rows(p.cu, b, p.total);
@@ -209,7 +277,7 @@ __global__ void __launch_bounds__(kThreads, 2) append_chunk_kernel(const AppendP
   const size_t win_at = ((size_t)b * p.num_kv_heads + h) * kBlockTokens * D + slab * W;
   const float* win = p.window[which] ? p.window[which] + win_at : nullptr;
   const int sub = lane / kLanes, ch = (lane % kLanes) * 4;  // this thread's channels ch ... ch + 3
-  const int tok = warp * 16 + sub * kTok;                   // ... and tokens tok ... tok + kTok - 1
+  const int tok = warp * kWarpTok + sub * kTok;                   // ... and tokens tok ... tok + kTok - 1
   const Rows& rows = p.x[which];
   const long long at0 = (long long)h * rows.sh + slab * W + ch;
 
@@ -243,30 +311,29 @@ __global__ void __launch_bounds__(kThreads, 2) append_chunk_kernel(const AppendP
     }
   }
 
-  // ---- the window of the new partial last block.  Only its sequence's first
-  //      block reads the window, and does so (above) before it is written here.
-  if (win != nullptr) {
+  // ---- the window of the new partial last block.  The sequence's first block
+  //      reads the window's rows (above) where it was begun before, and then is
+  //      the one that writes the new ones; else its last block does.
+  const int last = end / kBlockTokens * kBlockTokens;  // the partial block's first position
+  if (win != nullptr && end > last) {
     float* wout = p.window_out[which] + win_at;
-    const int last = end / kBlockTokens * kBlockTokens;  // the partial block's first position
-    if (nth == 0) {
-      if (last != t0) {
-        if (!tokenwise) __syncthreads();  // every thread has its rows of the old window
-        for (int e = tid; e < (end - last) * kLanes; e += kThreads) {
-          const int t = e / kLanes, c = (e % kLanes) * 4;
-          Raw<T> raw;
-          raw.load(rows.data, (long long)(s.first + last + t - len) * rows.st + (long long)h * rows.sh + slab * W + c);
-          *reinterpret_cast<float4*>(wout + (size_t)t * D + c) = raw.get();
-        }
-      } else if (nv < kBlockTokens) {
+    if (last == t0 && (nth == 0 || len % kBlockTokens == 0)) {
 #pragma unroll
-        for (int i = 0; i < kTok; ++i) {
-          const int t = tok + i;
-          if (t < nv && (t >= from || wout != win)) {
-            float4 v = make_float4(x[i][0], x[i][1], x[i][2], x[i][3]);
-            if (t < from && tokenwise) v = *reinterpret_cast<const float4*>(win + (size_t)t * D + ch);
-            *reinterpret_cast<float4*>(wout + (size_t)t * D + ch) = v;
-          }
+      for (int i = 0; i < kTok; ++i) {
+        const int t = tok + i;
+        if (t < nv && (t >= from || wout != win)) {
+          float4 v = make_float4(x[i][0], x[i][1], x[i][2], x[i][3]);
+          if (t < from && tokenwise) v = *reinterpret_cast<const float4*>(win + (size_t)t * D + ch);
+          *reinterpret_cast<float4*>(wout + (size_t)t * D + ch) = v;
         }
+      }
+    } else if (nth == 0 && len % kBlockTokens != 0) {
+      if (!tokenwise) __syncthreads();  // every thread has its rows of the old window
+      for (int e = tid; e < (end - last) * kLanes; e += kThreads) {
+        const int t = e / kLanes, c = (e % kLanes) * 4;
+        Raw<T> raw;
+        raw.load(rows.data, (long long)(s.first + last + t - len) * rows.st + (long long)h * rows.sh + slab * W + c);
+        *reinterpret_cast<float4*>(wout + (size_t)t * D + c) = raw.get();
       }
     }
   }
@@ -301,7 +368,8 @@ __global__ void __launch_bounds__(kThreads, 2) append_chunk_kernel(const AppendP
       unsigned char* at = packed + ((tok / kPer) * (W + 1) + ch + c) * 16 + (tok % kPer) * BITS / 8;
       if (kWords == 2) *reinterpret_cast<uint2*>(at) = make_uint2(acc[0][c] - kWordMagic, acc[kWords - 1][c] - kWordMagic);
       else if (kTok * BITS == 32) *reinterpret_cast<uint32_t*>(at) = acc[0][c] - kWordMagic;
-      else *reinterpret_cast<uint16_t*>(at) = (uint16_t)(acc[0][c] - kWordMagic);
+      else if (kTok * BITS == 16) *reinterpret_cast<uint16_t*>(at) = (uint16_t)acc[0][c];  // (kMagicBits is zero there)
+      else *at = (unsigned char)acc[0][c];
     }
   };
   if (tokenwise) {
@@ -316,7 +384,7 @@ __global__ void __launch_bounds__(kThreads, 2) append_chunk_kernel(const AppendP
     reduce_group<kTok, false>(mn, lg);
     reduce_group<kTok, true>(mx, lg);
     float4* sz = reinterpret_cast<float4*>(ranges);  // [token][group] s, z, 1 / s: at most 128 x W / 32 of them
-    static_assert(sizeof(ranges) == 128 * (W / 32) * sizeof(float4), "table");
+    static_assert(sizeof(ranges) >= 128 * (W / 32) * sizeof(float4), "table");
     const int each = kTok / lg > 1 ? kTok / lg : 1, share = lg / kTok > 1 ? lg / kTok : 1;
 #pragma unroll
     for (int k = 0; k < 2; ++k) {
@@ -389,36 +457,9 @@ __global__ void __launch_bounds__(kThreads, 2) append_chunk_kernel(const AppendP
     }
     *reinterpret_cast<float4*>(&lo_s[warp][ch]) = make_float4(mn[0], mn[1], mn[2], mn[3]);
     *reinterpret_cast<float4*>(&hi_s[warp][ch]) = make_float4(mx[0], mx[1], mx[2], mx[3]);
-    __syncthreads();
-    const int gw = G / 16, groups = kBlockTokens / G;  // warps of a token group, token groups
-    Group mine[2];                                     // groups * W / 256 <= 2 groups of a thread
-#pragma unroll
-    for (int k = 0; k < 2; ++k) {
-      const int e = tid + k * kThreads;
-      if (e < groups * W) {
-        const int g = e / W, c = e % W;
-        float a = INFINITY, z = -INFINITY;
-        for (int w = g * gw; w < (g + 1) * gw; ++w) {
-          a = min_nan(a, lo_s[w][c]);
-          z = max_nan(z, hi_s[w][c]);
-        }
-        mine[k] = group_of_range(a, z, kMax);
-        if (isnan(mine[k].s)) report(p.dev_status, KVQ_DEV_NONFINITE);
-        s_out[e] = mine[k].s_bits;
-        z_out[e] = mine[k].z_bits;
-      }
-    }
-    __syncthreads();
-#pragma unroll
-    for (int k = 0; k < 2; ++k) {
-      const int e = tid + k * kThreads;
-      if (e < groups * W) {
-        lo_s[e / W][e % W] = mine[k].s;
-        hi_s[e / W][e % W] = mine[k].z;
-      }
-    }
-    __syncthreads();
-    const int g = warp * 16 / G;
+    const int gw = G / kWarpTok, groups = kBlockTokens / G;  // warps of a token group, token groups
+    channel_groups<BITS, W>(ranges, groups, gw, s_out, z_out, p.dev_status);
+    const int g = warp * kWarpTok / G;
     const float4 s4 = *reinterpret_cast<const float4*>(&lo_s[g][ch]);
     const float4 z4 = *reinterpret_cast<const float4*>(&hi_s[g][ch]);
     float sc[4] = {s4.x, s4.y, s4.z, s4.w}, rc[4];
@@ -512,22 +553,273 @@ __global__ void __launch_bounds__(kThreads, 2) append_chunk_kernel(const AppendP
   }
 }
 
+template <typename T, int BITS, int W, Part PART>
+__global__ void __launch_bounds__(kThreads, 2) append_edges_kernel(const AppendParams p) {
+  append_edge<T, BITS, W, PART>(p);
+  // launched beside append_blocks_kernel: what follows in the stream waits for
+  // this grid, which is not done before that one is
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+}
+
+// ------------------------------------------------------- whole blocks
+
+// 16-bit pairs: the smaller (larger) of each half, NaN if either is.
+template <typename T>
+__device__ __forceinline__ uint32_t min2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  if (sizeof(T) == sizeof(__half)) asm("min.NaN.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  else asm("min.NaN.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+template <typename T>
+__device__ __forceinline__ uint32_t max2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  if (sizeof(T) == sizeof(__half)) asm("max.NaN.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  else asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+template <typename T>
+__device__ __forceinline__ float2 wide(uint32_t v) {
+  if (sizeof(T) == sizeof(__half)) return __half22float2(*reinterpret_cast<const __half2*>(&v));
+  return make_float2(__uint_as_float(v << 16), __uint_as_float(v & 0xffff0000u));
+}
+
+// reduce_group's exchange for 16-bit pairs, the smaller of each half kept.
+template <typename T, int N>
+__device__ __forceinline__ void reduce_group2(uint32_t (&v)[N], int lg) {
+  int o = lg >> 1;
+#pragma unroll
+  for (int n = N; n > 1; n >>= 1) {
+    if (o > 0) {
+      const bool upper = (threadIdx.x & o) != 0;
+#pragma unroll
+      for (int i = 0; i < n / 2; ++i) {
+        const uint32_t keep = upper ? v[i + n / 2] : v[i];
+        v[i] = min2<T>(keep, __shfl_xor_sync(0xffffffffu, upper ? v[i] : v[i + n / 2], o));
+      }
+      o >>= 1;
+    }
+  }
+  for (; o > 0; o >>= 1) v[0] = min2<T>(v[0], __shfl_xor_sync(0xffffffffu, v[0], o));
+}
+
+template <typename T, int BITS, int W>
+__global__ void __launch_bounds__(kThreads, 3) append_blocks_kernel(const AppendParams p) {
+  constexpr int kLanes = W / 4, kTok = kWarpTok * kLanes / 32, kPer = 128 / BITS;
+  constexpr int kPieces = W * BITS;
+  constexpr float kMax = (float)((1 << BITS) - 1);
+  // packed block: K [chunk][128 tokens], a piece of padding per chunk; V
+  // [chunk][channel mod 4][channel / 4], two pieces of padding per plane: lanes,
+  // which have every fourth channel, then meet no bank twice, nor do the
+  // pieces as they are read
+  constexpr int kPlane = W / 4 + 2;
+  __shared__ __align__(16) unsigned char packed[BITS * 4 * kPlane * 16];
+  static_assert(BITS * 4 * kPlane >= kPieces + W / kPer, "K's padding fits too");
+  __shared__ __align__(16) float ranges[2][kWarps][W];
+  __shared__ __align__(16) uint16_t s_out[128 * 4], z_out[128 * 4];
+  __shared__ int found[2];
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // the edges' kernel runs beside this one
+  const int D = p.head_dim;
+  const int h = blockIdx.y, which = blockIdx.z & 1, slab = blockIdx.z >> 1;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  if (warp == 0) find_block<kWhole>(p, blockIdx.x, false, found);
+  __syncthreads();
+  const int b = found[0];
+  if (b < 0) return;
+  const int len = p.seq_lens[b], j = len / kBlockTokens + found[1];
+  const int page = p.page_table ? p.page_table[(size_t)b * p.max_blocks + j] : b * p.max_blocks + j;
+  const int ch = (lane % kLanes) * 4, tok = warp * kWarpTok + (lane / kLanes) * kTok;
+  uint2 x[kTok];
+  {
+    const long long row = (long long)p.cu[b] + j * kBlockTokens - len + tok;
+    const uint16_t* src = static_cast<const uint16_t*>(p.x[which].data) + row * p.x[which].st +
+                          (long long)h * p.x[which].sh + slab * W + ch;
+    const long long st = p.x[which].st;
+#pragma unroll
+    for (int i = 0; i < kTok; ++i, src += st) x[i] = __ldcs(reinterpret_cast<const uint2*>(src));
+  }
+  if (page < 0 || page >= p.num_pages) {
+    if (h == 0 && blockIdx.z == 0 && tid == 0) report(p.dev_status, KVQ_DEV_BAD_PAGE);
+    return;
+  }
+  const int G = p.group, gps = W / G, nsz = kBlockTokens * D / G;
+  const size_t blk = (size_t)page * p.num_kv_heads + h;
+  const bool tokenwise = p.scheme[which] == KVQ_TOKENWISE;
+
+  unsigned char* k_at = packed + ((ch / kPer) * 129 + tok) * 16 + (ch % kPer) * BITS / 8;
+  auto put_k = [&](int i, const uint32_t (&y)[4]) {
+    const uint32_t w = y[0] + (y[1] << BITS) + (y[2] << 2 * BITS) + (y[3] << 3 * BITS);
+    if (BITS == 4) *reinterpret_cast<uint16_t*>(k_at + i * 16) = (uint16_t)w;
+    else k_at[i * 16] = (unsigned char)w;
+  };
+  constexpr int kWordTok = 32 / BITS < kTok ? 32 / BITS : kTok, kWords = kTok / kWordTok;
+  constexpr uint32_t kWordMagic = [] {
+    uint32_t m = 0;
+    for (int i = 0; i < kWordTok; ++i) m += kMagicBits << (i * BITS);
+    return m;
+  }();
+  auto put_v = [&](const uint32_t (&acc)[kWords][4]) {
+    unsigned char* at = packed + ((tok / kPer) * 4 * kPlane + ch / 4) * 16 + (tok % kPer) * BITS / 8;
+#pragma unroll
+    for (int c = 0; c < 4; ++c, at += kPlane * 16) {
+      if (kWords == 2) *reinterpret_cast<uint2*>(at) = make_uint2(acc[0][c] - kWordMagic, acc[kWords - 1][c] - kWordMagic);
+      else if (kTok * BITS == 32) *reinterpret_cast<uint32_t*>(at) = acc[0][c] - kWordMagic;
+      else *reinterpret_cast<uint16_t*>(at) = (uint16_t)acc[0][c];  // (kMagicBits is zero there)
+    }
+  };
+  uint32_t acc[kWords][4] = {};
+  // the codes of token i of this thread; values of a refused group (s NaN) are taken as z = 0
+  auto emit = [&](int i, const uint64_t (&sn)[2], const uint64_t (&zn)[2], const uint64_t (&r)[2]) {
+    uint32_t y[4];
+    const float2 a = wide<T>(x[i].x), c = wide<T>(x[i].y);
+    code_pair(a.x, a.y, sn[0], zn[0], r[0], y[0], y[1]);
+    code_pair(c.x, c.y, sn[1], zn[1], r[1], y[2], y[3]);
+    if (which == 0) {
+      put_k(i, y);
+    } else {
+#pragma unroll
+      for (int k = 0; k < 4; ++k) acc[i / kWordTok][k] += y[k] << (i % kWordTok * BITS);
+    }
+  };
+
+  if (tokenwise) {
+    const int lg = G / 4, gl = lane & (lg - 1);
+    uint32_t v[kTok];  // the token's smallest value over this thread's channels, and its largest negated
+#pragma unroll
+    for (int i = 0; i < kTok; ++i) {
+      const uint32_t lo = min2<T>(x[i].x, x[i].y), hi = max2<T>(x[i].x, x[i].y) ^ 0x80008000u;
+      v[i] = min2<T>(__byte_perm(lo, hi, 0x5410), __byte_perm(lo, hi, 0x7632));
+    }
+    reduce_group2<T, kTok>(v, lg);
+    float4* sz = reinterpret_cast<float4*>(ranges);  // [token][group] -s, -z, 1 / s
+    static_assert(sizeof(ranges) >= 128 * (W / 32) * sizeof(float4), "table");
+    const int each = kTok / lg > 1 ? kTok / lg : 1, share = lg / kTok > 1 ? lg / kTok : 1;
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      if (k < each && gl % share == 0) {
+        const float2 range = wide<T>(v[k]);
+        const Group g = group_of_range(range.x, -range.y, kMax);
+        const int e = (tok + (each > 1 ? gl * each + k : gl / share)) * gps + ch / G;
+        if (isnan(g.s)) report(p.dev_status, KVQ_DEV_NONFINITE);
+        sz[e] = make_float4(-g.s, -g.z, reciprocal(g.s), 0.f);
+        s_out[e] = g.s_bits;
+        z_out[e] = g.z_bits;
+      }
+    }
+    __syncwarp();  // a group's lanes are one warp's
+#pragma unroll
+    for (int i = 0; i < kTok; ++i) {
+      float4 g = sz[(tok + i) * gps + ch / G];
+      if (isnan(g.x)) {
+        g.x = 0.f;
+        x[i] = make_uint2(0u, 0u);
+      }
+      const uint64_t sn = rows::pair(g.x, g.x), zn = rows::pair(g.y, g.y), r = rows::pair(g.z, g.z);
+      emit(i, {sn, sn}, {zn, zn}, {r, r});
+    }
+  } else {
+    uint2 lo = x[0], hi = x[0];
+#pragma unroll
+    for (int i = 1; i < kTok; ++i) {
+      lo = make_uint2(min2<T>(lo.x, x[i].x), min2<T>(lo.y, x[i].y));
+      hi = make_uint2(max2<T>(hi.x, x[i].x), max2<T>(hi.y, x[i].y));
+    }
+    if (kLanes < 32) {  // both halves of the warp hold the same channels
+      lo = make_uint2(min2<T>(lo.x, __shfl_xor_sync(0xffffffffu, lo.x, 16)),
+                      min2<T>(lo.y, __shfl_xor_sync(0xffffffffu, lo.y, 16)));
+      hi = make_uint2(max2<T>(hi.x, __shfl_xor_sync(0xffffffffu, hi.x, 16)),
+                      max2<T>(hi.y, __shfl_xor_sync(0xffffffffu, hi.y, 16)));
+    }
+    float2 a = wide<T>(lo.x), c = wide<T>(lo.y);
+    *reinterpret_cast<float4*>(&ranges[0][warp][ch]) = make_float4(a.x, a.y, c.x, c.y);
+    a = wide<T>(hi.x);
+    c = wide<T>(hi.y);
+    *reinterpret_cast<float4*>(&ranges[1][warp][ch]) = make_float4(a.x, a.y, c.x, c.y);
+    channel_groups<BITS, W>(ranges, kBlockTokens / G, G / kWarpTok, s_out, z_out, p.dev_status);
+    const int g = warp * kWarpTok / G;
+    const float4 s4 = *reinterpret_cast<const float4*>(&ranges[0][g][ch]);
+    const float4 z4 = *reinterpret_cast<const float4*>(&ranges[1][g][ch]);
+    float sc[4] = {s4.x, s4.y, s4.z, s4.w};
+    uint32_t keep[2] = {0xffffffffu, 0xffffffffu};
+    float rc[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      if (isnan(sc[k])) {
+        sc[k] = 0.f;
+        keep[k / 2] &= k & 1 ? 0x0000ffffu : 0xffff0000u;
+      }
+      rc[k] = reciprocal(sc[k]);
+    }
+    if ((keep[0] & keep[1]) != 0xffffffffu) {
+#pragma unroll
+      for (int i = 0; i < kTok; ++i) x[i] = make_uint2(x[i].x & keep[0], x[i].y & keep[1]);
+    }
+    const uint64_t sn[2] = {rows::pair(-sc[0], -sc[1]), rows::pair(-sc[2], -sc[3])};
+    const uint64_t zn[2] = {rows::pair(-z4.x, -z4.y), rows::pair(-z4.z, -z4.w)};
+    const uint64_t r[2] = {rows::pair(rc[0], rc[1]), rows::pair(rc[2], rc[3])};
+#pragma unroll
+    for (int i = 0; i < kTok; ++i) emit(i, sn, zn, r);
+  }
+  if (which == 1) put_v(acc);
+  __syncthreads();
+
+  uint8_t* dst = p.codes[which] + blk * (size_t)(kBlockTokens * D * BITS / 8);
+  if (which == 0) {
+    dst += (size_t)slab * (W / kPer) * kBlockTokens * 16;
+#pragma unroll
+    for (int e = tid; e < kPieces; e += kThreads)
+      *reinterpret_cast<uint4*>(dst + e * 16) = *reinterpret_cast<const uint4*>(packed + (e + (e >> 7)) * 16);
+  } else {
+#pragma unroll
+    for (int e = tid; e < kPieces; e += kThreads) {
+      const int chunk = e / W, r = e % W;
+      *reinterpret_cast<uint4*>(dst + ((size_t)chunk * D + slab * W + r) * 16) =
+          *reinterpret_cast<const uint4*>(packed + (chunk * 4 * kPlane + (r & 3) * kPlane + (r >> 2)) * 16);
+    }
+  }
+  uint16_t* so = p.scale[which] + blk * nsz;
+  uint16_t* zo = p.zero[which] + blk * nsz;
+  const int wide_gps = tokenwise ? gps : W, pitch = tokenwise ? D / G : D;  // entries of a row here, and in the cache
+  const int entries = kBlockTokens * W / G, shift = 31 - __clz(wide_gps);
+  for (int e = tid; e < entries; e += kThreads) {
+    const int at = (e >> shift) * pitch + slab * wide_gps + (e & (wide_gps - 1));
+    so[at] = s_out[e];
+    zo[at] = z_out[e];
+  }
+}
+
+template <typename T, int BITS, int W>
+cudaError_t launch_w(const AppendParams& p, cudaStream_t stream) {
+  constexpr bool kHalf = sizeof(Raw<T>) == 8;
+  const unsigned heads = (unsigned)p.num_kv_heads, planes = (unsigned)(2 * (p.head_dim / W));
+  const bool whole = kHalf && p.total >= kBlockTokens;  // there may be blocks of new tokens alone
+  if constexpr (kHalf) {
+    if (whole) {
+      append_blocks_kernel<T, BITS, W><<<dim3((unsigned)(p.total / kBlockTokens), heads, planes), kThreads, 0, stream>>>(p);
+      const cudaError_t e = cudaGetLastError();
+      if (e != cudaSuccess) return e;
+    }
+  }
+  // one edge per sequence, two where a chunk of two tokens or more can cross
+  // into the next block; every block: one more for each 128 tokens past that
+  const long long two = p.batch < p.total / 2 ? p.batch : p.total / 2;
+  const long long blocks = p.batch + two + (kHalf ? 0 : (p.total - 2 * two) / kBlockTokens);
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)blocks, heads, planes);
+  cfg.blockDim = dim3(kThreads);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = whole ? 1 : 0;
+  return cudaLaunchKernelEx(&cfg, append_edges_kernel<T, BITS, W, kHalf ? kEdges : kEvery>, p);
+}
+
 template <typename T>
 cudaError_t launch(const AppendParams& p, cudaStream_t stream) {
-  // blocks touched: one per sequence, one more where a chunk of two tokens or
-  // more can cross into the next, one more for every 128 tokens past that
-  const long long two = p.batch < p.total / 2 ? p.batch : p.total / 2;
-  const long long blocks = p.batch + two + (p.total - 2 * two) / kBlockTokens;
-  const int w = p.head_dim < 128 ? p.head_dim : 128;
-  const dim3 grid((unsigned)blocks, (unsigned)p.num_kv_heads, (unsigned)(2 * (p.head_dim / w)));
-  if (p.bits == 4) {
-    if (w == 64) append_chunk_kernel<T, 4, 64><<<grid, kThreads, 0, stream>>>(p);
-    else append_chunk_kernel<T, 4, 128><<<grid, kThreads, 0, stream>>>(p);
-  } else {
-    if (w == 64) append_chunk_kernel<T, 2, 64><<<grid, kThreads, 0, stream>>>(p);
-    else append_chunk_kernel<T, 2, 128><<<grid, kThreads, 0, stream>>>(p);
-  }
-  return cudaGetLastError();
+  if (p.bits == 4) return p.head_dim < 128 ? launch_w<T, 4, 64>(p, stream) : launch_w<T, 4, 128>(p, stream);
+  return p.head_dim < 128 ? launch_w<T, 2, 64>(p, stream) : launch_w<T, 2, 128>(p, stream);
 }
 
 }  // namespace
