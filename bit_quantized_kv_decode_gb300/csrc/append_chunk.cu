@@ -181,31 +181,39 @@ __device__ __forceinline__ void find_block(const AppendParams& p, int rank, bool
   const int lane = threadIdx.x & 31;
   if (lane == 0) found[0] = -1;
   __syncwarp();
-  for (int b0 = 0; b0 < p.batch; b0 += 32) {
-    const int b = b0 + lane;
-    Chunk c{};
-    c.bad = true;
-    int blocks = 0;
-    if (b < p.batch) {
-      c = load_chunk(p, b);
-      if (c.bad && report_bad) report(p.dev_status, KVQ_DEV_BAD_SEQ_LEN);
-      blocks = part_blocks<PART>(c);
-    }
-    int incl = blocks;
+  constexpr int kAt = 4;  // sequences of a lane at a time: their loads overlap
+  for (int b0 = 0; b0 < p.batch; b0 += 32 * kAt) {
+    Chunk c[kAt];
 #pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int v = __shfl_up_sync(0xffffffffu, incl, o);
-      if (lane >= o) incl += v;
+    for (int k = 0; k < kAt; ++k) {
+      const int b = b0 + 32 * k + lane;
+      c[k] = Chunk{{0, 0, false}, 0, true};
+      if (b < p.batch) {
+        c[k] = load_chunk(p, b);
+        if (c[k].bad && report_bad) report(p.dev_status, KVQ_DEV_BAD_SEQ_LEN);
+      }
     }
-    const int i = rank - (incl - blocks);
-    if (i >= 0 && i < blocks) {
-      found[0] = b;
-      const int whole = whole_blocks(c), lead = c.len % kBlockTokens != 0 ? 1 : 0;  // an edge before the whole ones?
-      found[1] = PART == kWhole ? lead + i : PART == kEdges && i >= lead ? i + whole : i;
+    int left = rank;
+#pragma unroll
+    for (int k = 0; k < kAt; ++k) {
+      if (b0 + 32 * k >= p.batch) break;
+      const int blocks = part_blocks<PART>(c[k]);
+      int incl = blocks;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int v = __shfl_up_sync(0xffffffffu, incl, o);
+        if (lane >= o) incl += v;
+      }
+      const int i = left - (incl - blocks);
+      if (i >= 0 && i < blocks) {
+        found[0] = b0 + 32 * k + lane;
+        const int whole = whole_blocks(c[k]), lead = c[k].len % kBlockTokens != 0 ? 1 : 0;  // an edge before the whole ones?
+        found[1] = PART == kWhole ? lead + i : PART == kEdges && i >= lead ? i + whole : i;
+      }
+      left -= __shfl_sync(0xffffffffu, incl, 31);
     }
-    const int all = __shfl_sync(0xffffffffu, incl, 31);
-    if (rank < all && !report_bad) break;  // (the reporting CTA looks at every sequence)
-    rank -= all;
+    if (left < 0 && !report_bad) break;  // (the reporting CTA looks at every sequence)
+    rank = left;
   }
 }
 
@@ -295,6 +303,16 @@ __device__ __forceinline__ void append_edge(const AppendParams& p) {
         x[i][0] = v.x; x[i][1] = v.y; x[i][2] = v.z; x[i][3] = v.w;
       }
     } else {
+      // all loads before the first use.  Earlier tokens: for a group along the
+      // tokens, or to be copied to another window.
+      const bool old = win != nullptr && (!tokenwise || p.window_out[which] != p.window[which]);
+#pragma unroll
+      for (int i = 0; i < kTok; ++i) {
+        const int t = tok + i;
+        float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (old && t < from) v = *reinterpret_cast<const float4*>(win + (size_t)t * D + ch);
+        x[i][0] = v.x; x[i][1] = v.y; x[i][2] = v.z; x[i][3] = v.w;
+      }
 #pragma unroll
       for (int i = 0; i < kTok; ++i) {
         const int t = tok + i;
@@ -303,10 +321,10 @@ __device__ __forceinline__ void append_edge(const AppendParams& p) {
 #pragma unroll
       for (int i = 0; i < kTok; ++i) {
         const int t = tok + i;
-        float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-        if (t >= from && t < nv) v = raw[i].get();
-        else if (t < from && !tokenwise) v = *reinterpret_cast<const float4*>(win + (size_t)t * D + ch);
-        x[i][0] = v.x; x[i][1] = v.y; x[i][2] = v.z; x[i][3] = v.w;
+        if (t >= from && t < nv) {
+          const float4 v = raw[i].get();
+          x[i][0] = v.x; x[i][1] = v.y; x[i][2] = v.z; x[i][3] = v.w;
+        }
       }
     }
   }
@@ -322,9 +340,7 @@ __device__ __forceinline__ void append_edge(const AppendParams& p) {
       for (int i = 0; i < kTok; ++i) {
         const int t = tok + i;
         if (t < nv && (t >= from || wout != win)) {
-          float4 v = make_float4(x[i][0], x[i][1], x[i][2], x[i][3]);
-          if (t < from && tokenwise) v = *reinterpret_cast<const float4*>(win + (size_t)t * D + ch);
-          *reinterpret_cast<float4*>(wout + (size_t)t * D + ch) = v;
+          *reinterpret_cast<float4*>(wout + (size_t)t * D + ch) = make_float4(x[i][0], x[i][1], x[i][2], x[i][3]);
         }
       }
     } else if (nth == 0 && len % kBlockTokens != 0) {
