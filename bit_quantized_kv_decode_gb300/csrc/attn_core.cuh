@@ -170,6 +170,68 @@ __device__ __forceinline__ void softmax_tile(uint32_t t_s, uint32_t t_o, float c
   tc_wait_st();
 }
 
+// softmax_tile in a rolled form: the scores are read twice, 32 columns at a
+// time (the maxima of all, then the probabilities), by loops of a few hundred
+// bytes of code.  For kernels whose other warps run code of their own at the
+// same time: the straight-line form then keeps missing the instruction cache.
+template <int D, bool FP16, class Perm, class Ready>
+__device__ __forceinline__ void softmax_tile_rolled(uint32_t t_s, uint32_t t_o, float c, int seen, bool first,
+                                                    RowState& st, Perm perm, Ready sums_ready) {
+  const bool hidden = __any_sync(0xffffffffu, seen < kTile);
+  float mt = -INFINITY;
+#pragma unroll 1
+  for (int b = 0; b < kTile; b += 32) {
+    uint32_t s[32];
+    float m = tmem_ld_max_32x32b_x32(t_s + b, s);
+    tc_wait_ld();
+    if (__builtin_expect(hidden, 0)) {
+      m = -INFINITY;
+#pragma unroll
+      for (int i = 0; i < 32; ++i) m = b + i < seen ? fmaxf(m, __uint_as_float(s[i])) : m;
+    }
+    mt = fmaxf(mt, m);
+  }
+  const bool grow = (mt - st.m) * c > kRescaleLog2;
+  float alpha = 1.f;
+  if (grow) {
+    alpha = ex2((st.m - mt) * c);
+    st.m = mt;
+    st.l *= alpha;
+  }
+  if (__builtin_expect(!first && __any_sync(0xffffffffu, grow), 0)) {
+    sums_ready();
+    scale_rows<D>(t_o, alpha);
+  }
+  const float off = (st.m == -INFINITY ? 0.f : -st.m * c) + shift_log2<FP16>();
+  const uint64_t c2 = pair(c, c), off2 = pair(off, off);
+  uint64_t sum0 = pair(0.f, 0.f), sum1 = sum0;
+#pragma unroll 1
+  for (int b = 0; b < kTile; b += 32) {  // (probabilities of these columns go where scores were read before)
+    uint32_t s[32], p[16];
+    tmem_ld_32x32b_x32(t_s + b, s);
+    tc_wait_ld();
+    if (__builtin_expect(hidden, 0)) {
+#pragma unroll
+      for (int i = 0; i < 32; ++i) s[i] = b + i < seen ? s[i] : 0xff800000u;
+    }
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+      float x, y;
+      unpair(fma2(pair(__uint_as_float(s[perm(2 * i)]), __uint_as_float(s[perm(2 * i + 1)])), c2, off2), x, y);
+      x = ex2(x);
+      y = ex2(y);
+      if (i & 1) sum1 = add2(sum1, pair(x, y));
+      else sum0 = add2(sum0, pair(x, y));
+      p[i] = round2<FP16>(x, y);
+    }
+    tmem_st_32x32b_x16(t_s + (b >> 1), p);
+  }
+  float x, y;
+  unpair(add2(sum0, sum1), x, y);
+  st.l += x + y;
+  tc_wait_st();
+}
+
 // The MMAs of one product of 128-row tiles, issued by one thread.  (Loops and
 // not straight-line code: the issuing thread runs through it alone, and each
 // line of code that it has to fetch delays the tensor cores.)

@@ -452,7 +452,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const Params P) {
             tc_fence_after();
             if (any) {
               const int seen = !mine ? kTile : (p.causal ? min(g.len, pos + 1) : g.len) - (g.top - j) * kTile;
-              rows::softmax_tile<D, true>(tmem + lanes + 128 * buf, t_o, c, seen, j == 0, st,
+              rows::softmax_tile_rolled<D, true>(tmem + lanes + 128 * buf, t_o, c, seen, j == 0, st,
                                           [](int x) { return element_at<BITS>(x); },
                                           [&] {
                                             if (NT == 1) {
