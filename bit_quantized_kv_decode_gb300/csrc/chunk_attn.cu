@@ -92,11 +92,12 @@ cudaError_t launch_chunk_attn(const RowAttnParams& p, const ChunkPlan& plan, voi
   P.gshift = p.group == 32 ? 5 : p.group == 64 ? 6 : 7;
   P.table_bytes = 4 * nsz;
   P.unit_bytes = kBlockTokens * p.head_dim * p.bits / 8 + 4 * nsz;
-  const int fixed = fixed_bytes(p.head_dim, plan.nt) + dequant_groups(plan.nt) * 2 * P.table_bytes;
+  const int groups = dequant_groups(p.head_dim, plan.nt);
+  const int fixed = fixed_bytes(p.head_dim, plan.nt) + groups * 2 * P.table_bytes;
   P.units = (kSmem - fixed) / P.unit_bytes;
   if (P.units > kMaxUnits) P.units = kMaxUnits;
-  P.units &= ~1;  // a unit's place in the ring belongs to one dequantising warpgroup
-  if (P.units < 2) return cudaErrorInvalidValue;
+  P.units -= P.units % groups;  // a unit's place in the ring belongs to one dequantising warpgroup
+  if (P.units < groups) return cudaErrorInvalidValue;
   const size_t smem = (size_t)fixed + (size_t)P.units * P.unit_bytes;
   cudaError_t e = p.bits == 2 ? launch_i2(p.head_dim, plan.nt, P, plan.grid, smem, stream)
                               : launch_i4(p.head_dim, plan.nt, P, plan.grid, smem, stream);

@@ -141,7 +141,7 @@ struct Aux {
   uint64_t raw_full[kMaxUnits], raw_empty[kMaxUnits];
   uint64_t full[4], empty[4];
   uint64_t seg_full[4], seg_empty[4];
-  uint64_t prep[2];
+  uint64_t prep[4];
   uint64_t s[2], p[2], q, sums, done;
   uint32_t tmem;
   int fail;
@@ -293,15 +293,20 @@ __device__ __forceinline__ void dequant_part(const unsigned char* codes, const u
 // ------------------------------------------------------------- the kernel
 
 template <int BITS, int D, int NT>
-__global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const Params P) {
+__global__ void __launch_bounds__(threads_of(D, NT), 1) chunk_kernel(const Params P) {
   constexpr int kAhead = NT == 2 ? 1 : 2;             // score tiles issued ahead of their PV, per row tile
   constexpr int kChunks = D / 64;                     // 64-channel chunks of a Q row
   constexpr int kParts = D > 128 ? D / 128 : 1;       // slots of a K or V tile
   constexpr int kSlotCh = kChunks / kParts;
   constexpr int kSlot = slot_bytes(D), kSlots = slots_of(D, NT);
-  constexpr int kDq = dequant_groups(NT);             // dequantising warpgroups
+  constexpr int kThreads = threads_of(D, NT), kDq = dequant_groups(D, NT);
   constexpr int kSoftWarps = 4 * NT, kDqWarps = 4 * kDq;
-  static_assert(NT + kDq + 1 == kThreads / 128, "warpgroups");
+  constexpr int kMisc = kSoftWarps + kDqWarps;        // first warp of the last warpgroup: copies, products, segments
+  // A warpgroup waits for a slot's release by the parity of its round, so the
+  // round before last must be known to be over: it has waited for slot
+  // (u - kDq + 1) kParts - 1 - kSlots before (its last unit), which must not
+  // be older than u kParts - 2 kSlots.
+  static_assert(kSlots >= (kDq - 1) * kParts + 1, "operand slots");
   const RowAttnParams& p = P.r;
   extern __shared__ __align__(1024) unsigned char smem[];
   unsigned char* q_s = smem;
@@ -316,7 +321,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const Params P) {
   const int nsz = kBlockTokens * D >> P.gshift;
 
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // the merge may be launched; it waits for this grid
-  if (warp == 15 && lane == 0) {
+  if (warp == kMisc + 3 && lane == 0) {
     for (int i = 0; i < P.units; ++i) {
       mbar_init(&aux->raw_full[i], 1);
       mbar_init(&aux->raw_empty[i], 4);
@@ -327,8 +332,8 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const Params P) {
       mbar_init(&aux->seg_full[i], 1);
       mbar_init(&aux->seg_empty[i], kSoftWarps + kDqWarps + 2);
     }
+    for (int i = 0; i < kDq; ++i) mbar_init(&aux->prep[i], 4);
     for (int i = 0; i < 2; ++i) {
-      mbar_init(&aux->prep[i], 4);
       mbar_init(&aux->s[i], 1);
       mbar_init(&aux->p[i], 4);
     }
@@ -339,7 +344,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const Params P) {
     fence_barrier_init();
   }
   __syncwarp();
-  if (warp == 14) {
+  if (warp == kMisc + 2) {
     tmem_alloc(&aux->tmem, 512);
     tmem_relinquish();
   }
@@ -371,8 +376,6 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const Params P) {
 
     if (warp < kSoftWarps) {
       // ------------------------------------------------------------ softmax
-      if (NT == 2) setmaxnreg_inc<184>();
-      else setmaxnreg_inc<208>();
       const int i = warp >> 2, r = tid & 127;
       const uint32_t lanes = (uint32_t)(warp & 3) << 21;
       const uint32_t t_o = tmem + lanes + 256 + i * D;
@@ -511,8 +514,6 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const Params P) {
       }
     } else if (warp < kSoftWarps + kDqWarps) {
       // -------------------------------------------------- dequantisation
-      if (NT == 2) setmaxnreg_dec<88>();
-      else setmaxnreg_dec<104>();
       const int me = (warp - kSoftWarps) >> 2;  // this warpgroup takes units me, me + kDq, ...
       int u = 0, did = 0;
       bool ok = true;
@@ -561,9 +562,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const Params P) {
         }
       }
     } else {
-      if (NT == 2) setmaxnreg_dec<56>();
-      else setmaxnreg_dec<96>();
-      if (warp == 12) {
+      if (warp == kMisc) {
         // ---------------------------------------------------------- copies
         int u = 0;
         bool ok = true;
@@ -608,7 +607,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const Params P) {
           if ((p.flags & KVQ_FLAG_TEST_STALL) && s0 == 0 && n == 0) continue;
           drain(&aux->raw_full[n % P.units], (n / P.units) & 1);
         }
-      } else if (warp == 13) {
+      } else if (warp == kMisc + 1) {
         // -------------------------------------------------------- products
         constexpr uint32_t idesc_s = make_idesc(0, 0, 0, 0, 128, 128);
         constexpr int kN = D < 128 ? D : 128;
@@ -691,7 +690,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const Params P) {
           ok = __shfl_sync(0xffffffffu, (int)ok, 0) != 0;
         }
         __syncwarp();
-      } else if (warp == 14 && lane == 0) {
+      } else if (warp == kMisc + 2 && lane == 0) {
         // ---------------------------------------------------------- segments
         Place at = aux->start;
         uint32_t bad = 0;
@@ -732,7 +731,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const Params P) {
   __syncwarp();
   tc_fence_before();
   __syncthreads();
-  if (warp == 14) tmem_dealloc(tmem, 512);
+  if (warp == kMisc + 2) tmem_dealloc(tmem, 512);
   if (tid == 0 && aux->fail) report(p.dev_status, KVQ_DEV_TIMEOUT);
 }
 
@@ -741,7 +740,7 @@ cudaError_t launch_instance(const Params& p, int grid, size_t smem, cudaStream_t
   cudaError_t e =
       cudaFuncSetAttribute(chunk_kernel<BITS, D, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   if (e != cudaSuccess) return e;
-  chunk_kernel<BITS, D, NT><<<grid, kThreads, smem, stream>>>(p);
+  chunk_kernel<BITS, D, NT><<<grid, threads_of(D, NT), smem, stream>>>(p);
   return cudaGetLastError();
 }
 

@@ -5,8 +5,7 @@
 namespace kvq {
 namespace chunk {
 
-constexpr int kThreads = 512;   // four warpgroups
-constexpr int kMaxUnits = 12;   // packed K or V blocks in flight per CTA, at most
+constexpr int kMaxUnits = 16;   // packed K or V blocks in flight per CTA, at most
 constexpr int kAuxBytes = 1024;
 
 struct Params {
@@ -22,7 +21,10 @@ struct Params {
 __host__ __device__ constexpr int slot_bytes(int D) { return 128 * (D < 128 ? D : 128) * 2; }
 __host__ __device__ constexpr int q_bytes(int D, int nt) { return nt * 128 * D * 2; }
 __host__ __device__ constexpr int slots_of(int D, int nt) { return D > 128 ? 3 : 4; }
-__host__ __device__ constexpr int dequant_groups(int nt) { return nt == 2 ? 1 : 2; }
+// Dequantising warpgroups: they take K and V blocks in turn.  (Their code is a
+// chain of shared-memory loads and stores, so it takes several to fill the SM.)
+__host__ __device__ constexpr int dequant_groups(int D, int nt) { return nt == 2 || D > 128 ? 2 : 4; }
+__host__ __device__ constexpr int threads_of(int D, int nt) { return 128 * (nt + dequant_groups(D, nt) + 1); }
 __host__ __device__ constexpr int fixed_bytes(int D, int nt) { return q_bytes(D, nt) + slots_of(D, nt) * slot_bytes(D) + kAuxBytes; }
 
 cudaError_t launch_i2(int head_dim, int nt, const Params& p, int grid, size_t smem, cudaStream_t stream);
