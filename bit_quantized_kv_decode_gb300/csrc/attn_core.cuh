@@ -170,24 +170,32 @@ __device__ __forceinline__ void softmax_tile(uint32_t t_s, uint32_t t_o, float c
   tc_wait_st();
 }
 
-// softmax_tile in a rolled form: the scores are read twice, 32 columns at a
-// time (the maxima of all, then the probabilities), by loops of a few hundred
+// softmax_tile in a rolled form, over the columns [col0, col1) (multiples of
+// 32): the scores are read 32 columns at a time, twice (the maxima of all,
+// downwards, then upwards for the probabilities), by loops of a few hundred
 // bytes of code.  For kernels whose other warps run code of their own at the
 // same time: the straight-line form then keeps missing the instruction cache.
-template <int D, bool FP16, class Perm, class Ready>
-__device__ __forceinline__ void softmax_tile_rolled(uint32_t t_s, uint32_t t_o, float c, int seen, bool first,
-                                                    RowState& st, Perm perm, Ready sums_ready) {
-  const bool hidden = __any_sync(0xffffffffu, seen < kTile);
+// Probabilities go to the columns from t_p on, which may be t_s: those of 32
+// scores take the place of 16 that were read before.  scores_read() is called
+// once the scores may be overwritten.
+template <int D, bool FP16, class Perm, class Ready, class Read>
+__device__ __forceinline__ void softmax_tile_rolled(uint32_t t_s, uint32_t t_p, uint32_t t_o, int col0, int col1, float c,
+                                                    int seen, bool first, RowState& st, Perm perm, Ready sums_ready,
+                                                    Read scores_read) {
+  const bool hidden = __any_sync(0xffffffffu, seen < col1);
+  uint32_t s[32];
   float mt = -INFINITY;
 #pragma unroll 1
-  for (int b = 0; b < kTile; b += 32) {
-    uint32_t s[32];
+  for (int b = col1 - 32; b >= col0; b -= 32) {
     float m = tmem_ld_max_32x32b_x32(t_s + b, s);
     tc_wait_ld();
     if (__builtin_expect(hidden, 0)) {
       m = -INFINITY;
 #pragma unroll
-      for (int i = 0; i < 32; ++i) m = b + i < seen ? fmaxf(m, __uint_as_float(s[i])) : m;
+      for (int i = 0; i < 32; ++i) {
+        s[i] = b + i < seen ? s[i] : 0xff800000u;
+        m = fmaxf(m, __uint_as_float(s[i]));
+      }
     }
     mt = fmaxf(mt, m);
   }
@@ -206,14 +214,17 @@ __device__ __forceinline__ void softmax_tile_rolled(uint32_t t_s, uint32_t t_o, 
   const uint64_t c2 = pair(c, c), off2 = pair(off, off);
   uint64_t sum0 = pair(0.f, 0.f), sum1 = sum0;
 #pragma unroll 1
-  for (int b = 0; b < kTile; b += 32) {  // (probabilities of these columns go where scores were read before)
-    uint32_t s[32], p[16];
-    tmem_ld_32x32b_x32(t_s + b, s);
-    tc_wait_ld();
-    if (__builtin_expect(hidden, 0)) {
+  for (int b = col0; b < col1; b += 32) {
+    uint32_t p[16];
+    if (b != col0) {  // (the first columns are still here)
+      tmem_ld_32x32b_x32(t_s + b, s);
+      tc_wait_ld();
+      if (__builtin_expect(hidden, 0)) {
 #pragma unroll
-      for (int i = 0; i < 32; ++i) s[i] = b + i < seen ? s[i] : 0xff800000u;
+        for (int i = 0; i < 32; ++i) s[i] = b + i < seen ? s[i] : 0xff800000u;
+      }
     }
+    if (b + 32 == col1) scores_read();
 #pragma unroll
     for (int i = 0; i < 16; ++i) {
       float x, y;
@@ -224,7 +235,7 @@ __device__ __forceinline__ void softmax_tile_rolled(uint32_t t_s, uint32_t t_o, 
       else sum0 = add2(sum0, pair(x, y));
       p[i] = round2<FP16>(x, y);
     }
-    tmem_st_32x32b_x16(t_s + (b >> 1), p);
+    tmem_st_32x32b_x16(t_p + (b >> 1), p);
   }
   float x, y;
   unpair(add2(sum0, sum1), x, y);

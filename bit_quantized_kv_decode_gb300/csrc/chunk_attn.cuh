@@ -10,6 +10,16 @@
 // alike, without a host round trip: every CTA works the cut out by itself from
 // cu_seqlens and seq_lens.
 //
+// Few rows (a tile of up to 64, one row tile to a CTA): a row's softmax would be
+// the work of one thread while three quarters of the lanes idle, and the
+// slowest link of a step.  The rows are laid out two or four times over
+// instead, in different quadrants of tensor memory; every copy forms the
+// probabilities of its own half or quarter of the key tile and leaves the rest
+// zero, with a maximum and a sum of its own, so that its accumulator rows are
+// the attention over its share of the tokens.  The copies are joined like the
+// parts of a cut tile, at the end of the segment, in shared memory.  The extra
+// MMA rows are free.  (64 ragged paged sequences, 8 tokens at most: @REP@.)
+//
 // A step: the block's packed codes, scales and offsets come in by bulk copies
 // (warp `copy`); a dequantising warpgroup turns them into fp16 operands in
 // shared memory (x_hat = s code + z, one rounding); S = Q K^T and O += P V run
@@ -142,7 +152,7 @@ struct Aux {
   uint64_t full[4], empty[4];
   uint64_t seg_full[4], seg_empty[4];
   uint64_t prep[4];
-  uint64_t s[2], p[2], q, sums, done;
+  uint64_t s[2], p[2], q, sums, done, s_free, join;
   uint32_t tmem;
   int fail;
   int raw_bad[kMaxUnits];
@@ -340,6 +350,8 @@ __global__ void __launch_bounds__(threads_of(D, NT), 1) chunk_kernel(const Param
     mbar_init(&aux->q, kSoftWarps);
     mbar_init(&aux->sums, 1);
     mbar_init(&aux->done, 1);
+    mbar_init(&aux->s_free, 4);
+    mbar_init(&aux->join, 4);
     aux->fail = 0;
     fence_barrier_init();
   }
@@ -361,6 +373,9 @@ __global__ void __launch_bounds__(threads_of(D, NT), 1) chunk_kernel(const Param
     auto wait = [&](uint64_t* bar, uint32_t parity) -> bool {
       return rows::bounded_wait(bar, parity, fail, tries);
     };
+    // Copies of the rows in a tile of `rows_n` rows (see above).
+    auto copies_of = [&](int rows_n) { return NT == 2 || rows_n > 64 ? 1 : rows_n > 32 ? 2 : 4; };
+    constexpr int kPCol = D > 128 ? 128 : 384;  // with copies: two buffers of probabilities, apart from the scores
     // The same after a failure too: what is in flight must land.
     auto drain = [&](uint64_t* bar, uint32_t parity) {
       for (int i = 0; i < tries && !mbar_try_wait_sleep(bar, parity, 20000u); ++i) {}
@@ -376,16 +391,22 @@ __global__ void __launch_bounds__(threads_of(D, NT), 1) chunk_kernel(const Param
 
     if (warp < kSoftWarps) {
       // ------------------------------------------------------------ softmax
+      // (registers at launch: 5 warpgroups x 96 of two row tiles, 6 x 80 of one;
+      // head dim 256: 4 x 128, enough as they are)
+      if (D <= 128) setmaxnreg_inc<NT == 2 ? 128 : 144>();
       const int i = warp >> 2, r = tid & 127;
       const uint32_t lanes = (uint32_t)(warp & 3) << 21;
       const uint32_t t_o = tmem + lanes + 256 + i * D;
-      int uses = 0;  // score tiles of this row tile so far
+      int uses = 0;         // score tiles of this row tile so far
+      uint32_t s_phase = 0, joins = 0;  // next phases of s[], of join
       Segment g;
       for (int k = 0; next_segment(k, g); ++k) {
         const int tok0 = g.tile * tok_cta, ntok = min(tok_cta, g.n - tok0);
         const int rows_i = max(0, min(tok_tile, ntok - i * tok_tile)) * p.gq;
-        const bool mine = r < rows_i, any = (warp & 3) * 32 < rows_i;
-        const int tok = tok0 + i * tok_tile + r / p.gq, head = g.kvh * p.gq + r % p.gq;
+        const int copies = copies_of(rows_i), share = kTile / copies;  // rows of a copy, and columns that it has
+        const int row_i = r & (share - 1), copy = r / share;
+        const bool mine = row_i < rows_i, any = ((warp & 3) * 32 & (share - 1)) < rows_i;
+        const int tok = tok0 + i * tok_tile + row_i / p.gq, head = g.kvh * p.gq + row_i % p.gq;
         const int pos = g.len - g.n + tok;
         // Q row -> fp16, channels in operand order.  bf16 rows are scaled by a
         // power of two that brings the largest magnitude to [2^13, 2^14): eight
@@ -447,73 +468,145 @@ __global__ void __launch_bounds__(threads_of(D, NT), 1) chunk_kernel(const Param
         if (lane == 0) mbar_arrive(&aux->q);
         RowState st;
         bool ok = true;
+        if (copies > 1 && g.tiles > 0) {  // the other copies' columns stay zero
+          uint32_t none[32];
+#pragma unroll
+          for (int e = 0; e < 32; ++e) none[e] = 0u;
+#pragma unroll
+          for (int e = 0; e < 4; ++e) tmem_st_32x32b_x32p(tmem + lanes + kPCol + 32 * e, none);
+          tc_wait_st();
+        }
         if (rows_i > 0) {
           for (int j = 0; j < g.tiles && ok; ++j, ++uses) {
-            const int buf = NT == 2 ? i : uses & 1;
-            ok = __all_sync(0xffffffffu, wait(&aux->s[buf], (NT == 2 ? uses : uses >> 1) & 1));
+            const int buf = NT == 2 ? i : copies > 1 ? 0 : j & 1;
+            ok = __all_sync(0xffffffffu, wait(&aux->s[buf], s_phase >> buf & 1));
             if (!ok) break;
+            s_phase ^= 1u << buf;
             tc_fence_after();
+            auto scores_read = [&] {
+              if (copies > 1) {
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&aux->s_free);
+              }
+            };
             if (any) {
               const int seen = !mine ? kTile : (p.causal ? min(g.len, pos + 1) : g.len) - (g.top - j) * kTile;
-              rows::softmax_tile_rolled<D, true>(tmem + lanes + 128 * buf, t_o, c, seen, j == 0, st,
-                                          [](int x) { return element_at<BITS>(x); },
-                                          [&] {
-                                            if (NT == 1) {
-                                              wait(&aux->sums, (uses - 1) & 1);
-                                              __syncwarp();
-                                              tc_fence_after();
-                                            }
-                                          });
+              rows::softmax_tile_rolled<D, true>(tmem + lanes + 128 * buf,
+                                                 copies > 1 ? tmem + lanes + kPCol + 64 * (j & 1) : tmem + lanes + 128 * buf,
+                                                 t_o, copy * share, copy * share + share, c, seen, j == 0, st,
+                                                 [](int x) { return element_at<BITS>(x); },
+                                                 [&] {
+                                                   if (NT == 1) {
+                                                     wait(&aux->sums, (uses - 1) & 1);
+                                                     __syncwarp();
+                                                     tc_fence_after();
+                                                   }
+                                                 },
+                                                 scores_read);
+            } else {
+              scores_read();
             }
             tc_fence_before();
             __syncwarp();
-            if (lane == 0) mbar_arrive(&aux->p[buf]);
+            if (lane == 0) mbar_arrive(&aux->p[NT == 2 ? i : j & 1]);
           }
         }
         ok = ok && __all_sync(0xffffffffu, wait(&aux->done, k & 1));
         if (!ok) break;
-        if (any) {
-          tc_fence_after();
-          const bool seen_any = st.l > 0.f || isnan(st.l);
-          const float inv = seen_any ? 1.f / st.l : 0.f;
-          const float lse2 = seen_any ? st.m * c + log2f(st.l) - rows::shift_log2<true>() : -INFINITY;
-          const long long row = (long long)(g.first + tok) * p.num_q_heads + head;
-          const size_t prow = (size_t)max(g.slot, 0) * (NT * kTile) + i * kTile + r;
+        tc_fence_after();
+        const bool seen_any = st.l > 0.f || isnan(st.l);
+        float f = seen_any ? 1.f / st.l : 0.f;  // of this row's sums in its output
+        float lse2 = seen_any ? st.m * c + log2f(st.l) - rows::shift_log2<true>() : -INFINITY;
+        const long long row = (long long)(g.first + tok) * p.num_q_heads + head;
+        const size_t prow = (size_t)max(g.slot, 0) * (NT * kTile) + i * kTile + row_i;
+        auto put = [&](int col, const float (&x)[32]) {  // 32 channels of this thread's row
+          if (g.slot >= 0) {
+            float4* dst = reinterpret_cast<float4*>(P.part_o + prow * D + col);
 #pragma unroll
-          for (int cc = 0; cc < D / 32; ++cc) {
-            uint32_t o[32];
-            tmem_ld_32x32b_x32(t_o + 32 * cc, o);
-            tc_wait_ld();
-            if (!mine) continue;
-            float x[32];
+            for (int e = 0; e < 8; ++e) dst[e] = make_float4(x[4 * e], x[4 * e + 1], x[4 * e + 2], x[4 * e + 3]);
+          } else {
+            uint4* dst = reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.out) + row * D + col);
 #pragma unroll
-            for (int e = 0; e < 32; ++e) x[e] = seen_any ? __uint_as_float(o[e]) * inv : 0.f;
-            if (g.slot >= 0) {
-              float4* dst = reinterpret_cast<float4*>(P.part_o + prow * D + 32 * cc);
+            for (int e = 0; e < 4; ++e) {
+              uint32_t w[4];
 #pragma unroll
-              for (int e = 0; e < 8; ++e) dst[e] = make_float4(x[4 * e], x[4 * e + 1], x[4 * e + 2], x[4 * e + 3]);
-            } else {
-              uint4* dst = reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.out) + row * D + 32 * cc);
-#pragma unroll
-              for (int e = 0; e < 4; ++e) {
-                uint32_t w[4];
-#pragma unroll
-                for (int j = 0; j < 4; ++j)
-                  w[j] = p.fp16 ? rows::round2<true>(x[8 * e + 2 * j], x[8 * e + 2 * j + 1])
-                                : rows::round2<false>(x[8 * e + 2 * j], x[8 * e + 2 * j + 1]);
-                dst[e] = make_uint4(w[0], w[1], w[2], w[3]);
-              }
+              for (int j = 0; j < 4; ++j)
+                w[j] = p.fp16 ? rows::round2<true>(x[8 * e + 2 * j], x[8 * e + 2 * j + 1])
+                              : rows::round2<false>(x[8 * e + 2 * j], x[8 * e + 2 * j + 1]);
+              dst[e] = make_uint4(w[0], w[1], w[2], w[3]);
             }
           }
-          if (mine) {
-            if (g.slot >= 0) P.part_lse[prow] = lse2;
-            else if (p.lse != nullptr) p.lse[row] = lse2 * 0.6931471805599453f;
+        };
+        auto sums = [&](int col, float (&x)[32]) {
+          uint32_t o[32];
+          tmem_ld_32x32b_x32(t_o + col, o);
+          tc_wait_ld();
+#pragma unroll
+          for (int e = 0; e < 32; ++e) x[e] = seen_any ? __uint_as_float(o[e]) * f : 0.f;
+        };
+        if (copies == 1) {
+          if (any) {
+#pragma unroll 1
+            for (int col = 0; col < D; col += 32) {
+              float x[32];
+              sums(col, x);
+              if (mine) put(col, x);
+            }
           }
-          tc_fence_before();  // the accumulators are read before the next segment's products
+        } else {
+          // Joined over the copies: the first one's warps add the others' rows,
+          // half of the channels at a time, through Q's place in shared memory.
+          auto join = [&] {
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&aux->join);
+            ok = __all_sync(0xffffffffu, wait(&aux->join, joins++ & 1)) && ok;
+          };
+          float* xs = reinterpret_cast<float*>(q_s);  // [copy - 1][channel][row]
+          float* ls = xs + (copies - 1) * share * (D / 2);  // [copy][row] log-sum-exps
+          ls[r] = lse2;
+          join();
+          float m = -INFINITY, w = 0.f;
+          for (int e = 0; e < copies; ++e) m = fmaxf(m, ls[e * share + row_i]);
+          for (int e = 0; e < copies; ++e) w += m == -INFINITY ? 0.f : exp2f(ls[e * share + row_i] - m);
+          f = seen_any ? f * exp2f(lse2 - m) / w : 0.f;
+          lse2 = w > 0.f || isnan(w) ? m + log2f(w) : -INFINITY;
+#pragma unroll 1
+          for (int half = 0; half < 2; ++half) {
+            if (copy > 0) {
+#pragma unroll 1
+              for (int col = 0; col < D / 2; col += 32) {
+                float x[32];
+                sums(half * (D / 2) + col, x);
+#pragma unroll
+                for (int e = 0; e < 32; ++e) xs[((copy - 1) * (D / 2) + col + e) * share + row_i] = x[e];
+              }
+            }
+            join();
+            if (copy == 0) {
+#pragma unroll 1
+              for (int col = 0; col < D / 2; col += 32) {
+                float x[32];
+                sums(half * (D / 2) + col, x);
+                for (int e = 1; e < copies; ++e)
+#pragma unroll
+                  for (int ch = 0; ch < 32; ++ch) x[ch] += xs[((e - 1) * (D / 2) + col + ch) * share + row_i];
+                if (mine) put(half * (D / 2) + col, x);
+              }
+            }
+            join();
+          }
+          if (!ok) break;
         }
+        if (mine && copy == 0) {
+          if (g.slot >= 0) P.part_lse[prow] = lse2;
+          else if (p.lse != nullptr) p.lse[row] = lse2 * 0.6931471805599453f;
+        }
+        tc_fence_before();  // the accumulators are read before the next segment's products
       }
     } else if (warp < kSoftWarps + kDqWarps) {
       // -------------------------------------------------- dequantisation
+      if (D <= 128) setmaxnreg_dec<NT == 2 ? 72 : 64>();
       const int me = (warp - kSoftWarps) >> 2;  // this warpgroup takes units me, me + kDq, ...
       int u = 0, did = 0;
       bool ok = true;
@@ -562,6 +655,7 @@ __global__ void __launch_bounds__(threads_of(D, NT), 1) chunk_kernel(const Param
         }
       }
     } else {
+      if (D <= 128) setmaxnreg_dec<NT == 2 ? 72 : 64>();
       if (warp == kMisc) {
         // ---------------------------------------------------------- copies
         int u = 0;
@@ -620,14 +714,14 @@ __global__ void __launch_bounds__(threads_of(D, NT), 1) chunk_kernel(const Param
                                         make_desc_sw128_lo(q_a + (i * kChunks + part * kSlotCh) * 16384, 0),
                                         make_desc_sw128_lo(ring_a + (n + part) % kSlots * kSlot, 0), idesc_s, part > 0);
         };
-        auto values = [&](int i, int buf, int n, bool add) {
+        auto values = [&](int i, int pcol, int n, bool add) {  // pcol: column of the probabilities
 #pragma unroll 1
           for (int part = 0; part < kParts; ++part)  // V rows are channels: 64 tokens to a chunk of kN rows
-            rows::issue_values(tmem + 256 + i * D + part * 128, tmem + 128 * buf,
+            rows::issue_values(tmem + 256 + i * D + part * 128, tmem + pcol,
                                make_desc_sw128_lo(ring_a + (n + part) % kSlots * kSlot, 0), 2, kN * 8, idesc_o, add);
         };
         int n = 0;  // slots taken so far
-        int use0 = 0, use1 = 0;  // score tiles per buffer (two row tiles) or in all (one)
+        uint32_t p_phase = 0, free_phase = 0;  // next phases of p[], of s_free
         bool ok = true;
         auto take = [&]() {
           const int at = n;
@@ -637,40 +731,57 @@ __global__ void __launch_bounds__(threads_of(D, NT), 1) chunk_kernel(const Param
         auto release = [&](int at) {
           for (int part = 0; part < kParts; ++part) tc_commit(&aux->empty[(at + part) % kSlots]);
         };
+        auto probabilities = [&](int buf) {  // written
+          ok = wait(&aux->p[buf], p_phase >> buf & 1);
+          p_phase ^= 1u << buf;
+          tc_fence_after();
+          return ok;
+        };
         Segment g;
         for (int k = 0; ok && next_segment(k, g); ++k) {
           if (lane == 0) {
             const int ntok = min(tok_cta, g.n - g.tile * tok_cta);
             const int act = NT == 2 && ntok > tok_tile ? 2 : 1;
+            const bool split = copies_of(ntok * p.gq) > 1;  // one buffer of scores, probabilities apart
             ok = wait(&aux->q, k & 1);
             tc_fence_after();
-            int issued = 0;
-#pragma unroll 1
-            for (int j = 0; j < kAhead && j < g.tiles && ok; ++j) {
+            auto first_scores = [&](int j) {  // tile j's, for every row tile
               const int ks = take();
-              if (!ok) break;
+              if (!ok) return;
 #pragma unroll 1
               for (int i = 0; i < act; ++i) {
-                const int buf = NT == 2 ? i : (use0 + j) & 1;
+                const int buf = NT == 2 ? i : j;
                 scores(i, buf, ks);
                 tc_commit(&aux->s[buf]);
               }
               release(ks);
-              ++issued;
-            }
+            };
+            for (int j = 0; j < (split ? 1 : kAhead) && j < g.tiles && ok; ++j) first_scores(j);
 #pragma unroll 1
             for (int j = 0; j < g.tiles && ok; ++j) {
+              if (NT == 1 && split) {
+                // S of tile j + 1 as soon as tile j's scores are read
+                if (j + 1 < g.tiles) {
+                  ok = wait(&aux->s_free, free_phase & 1);
+                  tc_fence_after();
+                  if (ok) first_scores(0);
+                }
+                ++free_phase;
+                const int vs = ok ? take() : 0;
+                if (!ok || !probabilities(j & 1)) break;
+                values(0, kPCol + 64 * (j & 1), vs, j > 0);
+                tc_commit(&aux->sums);
+                release(vs);
+                continue;
+              }
               const int vs = take();
               const bool more = j + kAhead < g.tiles;
               int ks = 0;
 #pragma unroll 1
               for (int i = 0; i < act && ok; ++i) {
-                const int use = NT == 2 && i == 1 ? use1 : use0;
-                const int buf = NT == 2 ? i : use & 1;
-                ok = wait(&aux->p[buf], (NT == 2 ? use : use >> 1) & 1);
-                if (!ok) break;
-                tc_fence_after();
-                values(i, buf, vs, j > 0);
+                const int buf = NT == 2 ? i : j & 1;
+                if (!probabilities(buf)) break;
+                values(i, 128 * buf, vs, j > 0);
                 if (NT == 1) tc_commit(&aux->sums);
                 if (i == act - 1) release(vs);
                 if (more) {
@@ -679,8 +790,6 @@ __global__ void __launch_bounds__(threads_of(D, NT), 1) chunk_kernel(const Param
                   scores(i, buf, ks);
                   tc_commit(&aux->s[buf]);
                 }
-                if (NT == 2 && i == 1) ++use1;
-                else ++use0;
               }
               if (ok && more) release(ks);
             }
