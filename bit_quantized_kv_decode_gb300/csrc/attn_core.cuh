@@ -33,7 +33,7 @@ __device__ __forceinline__ bool bounded_wait(uint64_t* bar, uint32_t parity, vol
     }
   return true;
 }
-constexpr int kTries = 1 << 21, kTestTries = 1 << 12;  // under the stall flag: a test's patience
+constexpr int kTries = 1 << 19, kTestTries = 1 << 12;  // under the stall flag: a test's patience
 
 // fp32 pairs in one register pair: the FMA pipe takes both at once.
 __device__ __forceinline__ uint64_t pair(float a, float b) {
@@ -225,16 +225,19 @@ __device__ __forceinline__ void softmax_tile_rolled(uint32_t t_s, uint32_t t_p, 
       }
     }
     if (b + 32 == col1) scores_read();
+    // neighbouring columns lie in register pairs, as the packed arithmetic wants
+    // them; the operand's order is made as they are rounded
+    float e[32];
 #pragma unroll
     for (int i = 0; i < 16; ++i) {
-      float x, y;
-      unpair(fma2(pair(__uint_as_float(s[perm(2 * i)]), __uint_as_float(s[perm(2 * i + 1)])), c2, off2), x, y);
-      x = ex2(x);
-      y = ex2(y);
-      if (i & 1) sum1 = add2(sum1, pair(x, y));
-      else sum0 = add2(sum0, pair(x, y));
-      p[i] = round2<FP16>(x, y);
+      unpair(fma2(pair(__uint_as_float(s[2 * i]), __uint_as_float(s[2 * i + 1])), c2, off2), e[2 * i], e[2 * i + 1]);
+      e[2 * i] = ex2(e[2 * i]);
+      e[2 * i + 1] = ex2(e[2 * i + 1]);
+      if (i & 1) sum1 = add2(sum1, pair(e[2 * i], e[2 * i + 1]));
+      else sum0 = add2(sum0, pair(e[2 * i], e[2 * i + 1]));
     }
+#pragma unroll
+    for (int i = 0; i < 16; ++i) p[i] = round2<FP16>(e[perm(2 * i)], e[perm(2 * i + 1)]);
     tmem_st_32x32b_x16(t_p + (b >> 1), p);
   }
   float x, y;

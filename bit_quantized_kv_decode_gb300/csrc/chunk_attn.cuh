@@ -241,61 +241,91 @@ __device__ __forceinline__ void prepare_table(const uint16_t* s, const uint16_t*
   }
 }
 
-// One slot (part) of a K or V block: codes -> fp16 operand tile of NROWS rows
-// x kCols columns, 128-byte swizzled, 64 columns to a chunk.  128 threads.
+__device__ __forceinline__ uint4 lds128(uint32_t addr) {
+  uint4 v;
+  asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr));
+  return v;
+}
+__device__ __forceinline__ uint32_t lds32(uint32_t addr) {
+  uint32_t v;
+  asm volatile("ld.shared.b32 %0, [%1];" : "=r"(v) : "r"(addr));
+  return v;
+}
+__device__ __forceinline__ void sts128(uint32_t addr, uint32_t x, uint32_t y, uint32_t z, uint32_t w) {
+  asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(x), "r"(y), "r"(z), "r"(w) : "memory");
+}
+
+// One slot (part) of a K or V block: codes -> fp16 operand tile of kNR rows
+// x kCols columns, 128-byte swizzled, 64 columns to a chunk.  128 threads, a
+// 16-byte piece of codes (32 or 64 columns of a row) at a time; every thread
+// keeps its row (64 rows: two threads to a row), so that only constants are
+// added to its addresses (shared-memory addresses, 32 bits).
 template <int BITS, int D, bool VALUE, bool BYCOL>
-__device__ __forceinline__ void dequant_part(const unsigned char* codes, const unsigned char* table, int nsz, int part,
-                                             int gshift, unsigned char* slot) {
-  constexpr int kRowsAll = VALUE ? D : kTile;            // rows of the packed block
-  constexpr int kNR = VALUE ? (D < 128 ? D : 128) : kTile;  // rows of the part
+__device__ __forceinline__ void dequant_part(uint32_t codes, uint32_t table, int nsz, int part, int gshift,
+                                             uint32_t slot) {
+  constexpr int kRowsAll = VALUE ? D : kTile;                 // rows of the packed block
+  constexpr int kNR = VALUE ? (D < 128 ? D : 128) : kTile;    // rows of the part
   constexpr int kCols = VALUE ? kTile : (D < 128 ? D : 128);  // columns of the part
-  constexpr int kPer = 128 / BITS;                       // codes of a 16-byte piece
+  constexpr int kPer = 128 / BITS;                            // codes of a piece
   constexpr int kChunks = kCols / kPer;
-  constexpr int kWord = 32 / BITS;                       // codes of a word
-  const int t = threadIdx.x & 127;
+  constexpr int kStep = 128 / kNR;                            // pieces of a row that the threads take at once
+  constexpr int kWord = 32 / BITS;                            // codes of a word
+  const int t = threadIdx.x & 127, row = t & (kNR - 1), chunk0 = t / kNR;
+  const int grow = row + (VALUE ? part * 128 : 0);            // row of the block
+  const int gchunk0 = chunk0 + (VALUE ? 0 : part * kChunks);  // piece of the row
+  uint32_t src = codes + (uint32_t)(gchunk0 * kRowsAll + grow) * 16;
+  // 16-byte unit u of the row's 128 bytes of a chunk lies at (u ^ (row & 7)) * 16
+  const uint32_t at_row = slot + row * 128, sw = (uint32_t)(row & 7) << 4;
+  // by column: scales of the row's group, then offsets nsz entries on; by row:
+  // entry (row, column group), a column group every 2^gshift columns
+  uint32_t ts = table, step;
+  if (BYCOL) {
+    ts += (uint32_t)((grow >> gshift) * (VALUE ? kTile : D) + gchunk0 * kPer) * 2;
+    step = kStep * kPer * 2;
+  } else {
+    ts += (uint32_t)(VALUE ? grow : grow * (D >> gshift)) * 4;
+    step = 0;
+  }
 #pragma unroll 1
-  for (int i = 0; i < kNR * kChunks / 128; ++i) {
-    const int piece = t + 128 * i, row = piece % kNR, chunk = piece / kNR;
-    const int grow = row + (VALUE ? part * 128 : 0);
-    const int gchunk = chunk + (VALUE ? 0 : part * kChunks);
-    const uint4 v = *reinterpret_cast<const uint4*>(codes + ((size_t)gchunk * kRowsAll + grow) * 16);
+  for (int i = 0; i < kChunks; i += kStep, src += kStep * kRowsAll * 16, ts += step) {
+    const int chunk = i + chunk0;
+    const uint4 v = lds128(src);
     const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-    unsigned char* dst = slot + (chunk * kPer / 64) * (kNR * 128) + row * 128;
-    const int c16 = (chunk * kPer % 64) / 8, sw = row & 7;
+    const uint32_t dst = at_row + (uint32_t)(chunk * kPer / 64) * (kNR * 128);
+    const uint32_t u0 = (uint32_t)(chunk * kPer % 64) / 8 * 16 ^ sw;
     uint32_t sz = 0;
 #pragma unroll
     for (int q = 0; q < 4; ++q) {
-      const int col = gchunk * kPer + q * kWord;  // first column of the word
+      uint4 s4[kWord / 8], z4[kWord / 8];
+      if (BYCOL) {
+#pragma unroll
+        for (int hf = 0; hf < kWord / 8; ++hf) {
+          s4[hf] = lds128(ts + (q * kWord + 8 * hf) * 2);
+          z4[hf] = lds128(ts + nsz * 2 + (q * kWord + 8 * hf) * 2);
+        }
+      } else if (q == 0 || (BITS == 2 && q == 2)) {  // a group is at least 32 columns
+        const int g = ((gchunk0 + i) * kPer + q * kWord) >> gshift;
+        sz = lds32(ts + (VALUE ? g * D : g) * 4);
+      }
       __half2 c[kWord / 2];
       unpack_word<BITS>(w[q], c);
       uint32_t x[kWord / 2];
       if (BYCOL) {
-        // K: table row = token group of `row`; V: channel group of `row`
-        const int g = grow >> gshift, base = g * (VALUE ? kTile : D) + col;
-        const uint16_t* ts = reinterpret_cast<const uint16_t*>(table) + base;
 #pragma unroll
         for (int hf = 0; hf < kWord / 8; ++hf) {
-          const uint4 s4 = *reinterpret_cast<const uint4*>(ts + 8 * hf);
-          const uint4 z4 = *reinterpret_cast<const uint4*>(ts + nsz + 8 * hf);
-          x[4 * hf] = as_u32(__hfma2(c[4 * hf], as_h2(s4.x), as_h2(z4.x)));
-          x[4 * hf + 1] = as_u32(__hfma2(c[4 * hf + 1], as_h2(s4.y), as_h2(z4.y)));
-          x[4 * hf + 2] = as_u32(__hfma2(c[4 * hf + 2], as_h2(s4.z), as_h2(z4.z)));
-          x[4 * hf + 3] = as_u32(__hfma2(c[4 * hf + 3], as_h2(s4.w), as_h2(z4.w)));
+          x[4 * hf] = as_u32(__hfma2(c[4 * hf], as_h2(s4[hf].x), as_h2(z4[hf].x)));
+          x[4 * hf + 1] = as_u32(__hfma2(c[4 * hf + 1], as_h2(s4[hf].y), as_h2(z4[hf].y)));
+          x[4 * hf + 2] = as_u32(__hfma2(c[4 * hf + 2], as_h2(s4[hf].z), as_h2(z4[hf].z)));
+          x[4 * hf + 3] = as_u32(__hfma2(c[4 * hf + 3], as_h2(s4[hf].w), as_h2(z4[hf].w)));
         }
       } else {
-        if (q == 0 || (BITS == 2 && q == 2)) {  // a group is at least 32 columns
-          const int g = col >> gshift;
-          const int e = VALUE ? g * D + grow : grow * (D >> gshift) + g;
-          sz = reinterpret_cast<const uint32_t*>(table)[e];
-        }
         const __half2 s2 = as_h2(__byte_perm(sz, 0, 0x1010)), z2 = as_h2(__byte_perm(sz, 0, 0x3232));
 #pragma unroll
         for (int k = 0; k < kWord / 2; ++k) x[k] = as_u32(__hfma2(c[k], s2, z2));
       }
 #pragma unroll
       for (int hf = 0; hf < kWord / 8; ++hf)
-        *reinterpret_cast<uint4*>(dst + (((c16 + q * (kWord / 8) + hf) ^ sw) << 4)) =
-            make_uint4(x[4 * hf], x[4 * hf + 1], x[4 * hf + 2], x[4 * hf + 3]);
+        sts128(dst + (u0 ^ (q * (kWord / 8) + hf) * 16), x[4 * hf], x[4 * hf + 1], x[4 * hf + 2], x[4 * hf + 3]);
     }
   }
 }
@@ -629,13 +659,13 @@ __global__ void __launch_bounds__(threads_of(D, NT), 1) chunk_kernel(const Param
             const int n = u * kParts + part, sl = n % kSlots, round = n / kSlots;
             if (round > 0) ok = __all_sync(0xffffffffu, wait(&aux->empty[sl], (round - 1) & 1));
             if (!ok) break;
-            unsigned char* dst = ring + sl * kSlot;
+            const uint32_t dst = smem_u32(ring) + sl * kSlot;
             if (value) {
-              if (by_column) dequant_part<BITS, D, true, true>(src, table, nsz, part, P.gshift, dst);
-              else dequant_part<BITS, D, true, false>(src, table, nsz, part, P.gshift, dst);
+              if (by_column) dequant_part<BITS, D, true, true>(smem_u32(src), smem_u32(table), nsz, part, P.gshift, dst);
+              else dequant_part<BITS, D, true, false>(smem_u32(src), smem_u32(table), nsz, part, P.gshift, dst);
             } else {
-              if (by_column) dequant_part<BITS, D, false, true>(src, table, nsz, part, P.gshift, dst);
-              else dequant_part<BITS, D, false, false>(src, table, nsz, part, P.gshift, dst);
+              if (by_column) dequant_part<BITS, D, false, true>(smem_u32(src), smem_u32(table), nsz, part, P.gshift, dst);
+              else dequant_part<BITS, D, false, false>(smem_u32(src), smem_u32(table), nsz, part, P.gshift, dst);
             }
             fence_proxy_async_smem();
             __syncwarp();
