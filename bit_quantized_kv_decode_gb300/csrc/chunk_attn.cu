@@ -69,12 +69,40 @@ __global__ void __launch_bounds__(kMergeThreads) merge_kernel(const Params P, in
 }  // namespace
 }  // namespace chunk
 
-ChunkPlan chunk_plan(int head_dim, int batch, int total, int num_q_heads, int num_kv_heads) {
+namespace chunk {
+namespace {
+
+struct Memory {
+  int table_bytes, unit_bytes, units;
+  size_t total;
+};
+// What an instance's shared memory is divided into: units = 0 where the
+// ring of packed blocks would not hold one for each team.
+Memory memory_of(int head_dim, int group, int bits, int nt) {
+  Memory m;
+  const int nsz = kBlockTokens * head_dim / group, teams = teams_of(head_dim);
+  m.table_bytes = 4 * nsz;
+  m.unit_bytes = kBlockTokens * head_dim * bits / 8 + 4 * nsz;
+  const int fixed = fixed_bytes(head_dim, nt) + teams * 2 * m.table_bytes;
+  m.units = (kSmem - fixed) / m.unit_bytes;
+  if (m.units > kMaxUnits) m.units = kMaxUnits;
+  m.units -= m.units % teams;  // a unit's place in the ring belongs to one dequantising team
+  m.total = (size_t)fixed + (size_t)m.units * m.unit_bytes;
+  return m;
+}
+
+}  // namespace
+}  // namespace chunk
+
+ChunkPlan chunk_plan(int head_dim, int group, int bits, int batch, int total, int num_q_heads, int num_kv_heads) {
   ChunkPlan c;
   // two row tiles where the sequences have more rows than one on average
-  // (head dim 256: one, its accumulators fill tensor memory)
+  // (head dim 256: one, its accumulators fill tensor memory; nor where shared
+  // memory is too small for two, as with 4-bit codes in groups of 32 at 128)
   const long long rows = (long long)total * (num_q_heads / num_kv_heads);
-  c.nt = head_dim <= 128 && rows > (long long)batch * chunk::kTile ? 2 : 1;
+  c.nt = head_dim <= 128 && rows > (long long)batch * chunk::kTile && chunk::memory_of(head_dim, group, bits, 2).units > 0
+             ? 2
+             : 1;
   c.grid = chunk::kGrid;
   const size_t slots = (size_t)2 * c.grid * c.nt * chunk::kTile;
   c.part_lse = slots * head_dim * sizeof(float);
@@ -88,19 +116,14 @@ cudaError_t launch_chunk_attn(const RowAttnParams& p, const ChunkPlan& plan, voi
   P.r = p;
   P.part_o = static_cast<float*>(workspace);
   P.part_lse = reinterpret_cast<float*>(static_cast<unsigned char*>(workspace) + plan.part_lse);
-  const int nsz = kBlockTokens * p.head_dim / p.group;
   P.gshift = p.group == 32 ? 5 : p.group == 64 ? 6 : 7;
-  P.table_bytes = 4 * nsz;
-  P.unit_bytes = kBlockTokens * p.head_dim * p.bits / 8 + 4 * nsz;
-  const int groups = dequant_groups(p.head_dim, plan.nt);
-  const int fixed = fixed_bytes(p.head_dim, plan.nt) + groups * 2 * P.table_bytes;
-  P.units = (kSmem - fixed) / P.unit_bytes;
-  if (P.units > kMaxUnits) P.units = kMaxUnits;
-  P.units -= P.units % groups;  // a unit's place in the ring belongs to one dequantising warpgroup
-  if (P.units < groups) return cudaErrorInvalidValue;
-  const size_t smem = (size_t)fixed + (size_t)P.units * P.unit_bytes;
-  cudaError_t e = p.bits == 2 ? launch_i2(p.head_dim, plan.nt, P, plan.grid, smem, stream)
-                              : launch_i4(p.head_dim, plan.nt, P, plan.grid, smem, stream);
+  const Memory m = memory_of(p.head_dim, p.group, p.bits, plan.nt);
+  P.table_bytes = m.table_bytes;
+  P.unit_bytes = m.unit_bytes;
+  P.units = m.units;
+  if (m.units < 1) return cudaErrorInvalidValue;
+  cudaError_t e = p.bits == 2 ? launch_i2(p.head_dim, plan.nt, P, plan.grid, m.total, stream)
+                              : launch_i4(p.head_dim, plan.nt, P, plan.grid, m.total, stream);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(plan.grid - 1), (unsigned)(plan.nt * kTile / kMergeRows));

@@ -151,7 +151,6 @@ struct Aux {
   uint64_t raw_full[kMaxUnits], raw_empty[kMaxUnits];
   uint64_t full[4], empty[4];
   uint64_t seg_full[4], seg_empty[4];
-  uint64_t prep[4];
   uint64_t s[2], p[2], q, sums, done, s_free, join;
   uint32_t tmem;
   int fail;
@@ -209,9 +208,9 @@ __host__ __device__ constexpr int element_at(int i) {
 // columns, in operand order: col_major: [group][column] u16 scales, then
 // offsets; else [entry] (scale | offset << 16).
 template <int BITS>
-__device__ __forceinline__ void prepare_table(const uint16_t* s, const uint16_t* z, int nsz, bool by_column, bool value,
-                                              int D, int gshift, bool bad, unsigned char* table, uint32_t* dev_status) {
-  const int t = threadIdx.x & 127;
+__device__ __forceinline__ void prepare_table(int t, const uint16_t* s, const uint16_t* z, int nsz, bool by_column,
+                                              bool value, int D, int gshift, bool bad, unsigned char* table,
+                                              uint32_t* dev_status) {
   const float most = (float)((1 << BITS) - 1);
   uint16_t* ts = reinterpret_cast<uint16_t*>(table);
   uint16_t* tz = ts + nsz;
@@ -232,7 +231,7 @@ __device__ __forceinline__ void prepare_table(const uint16_t* s, const uint16_t*
       if (!value) {  // K, channel-wise: entry group * D + channel
         at = (e & ~15) + position_of<BITS>(e & 15);
       } else {       // V, token-wise: entry token * (D / G) + group
-        const int gpt = D >> gshift, tok = e / gpt, g = e - tok * gpt;
+        const int gpt = D >> gshift, tok = e >> (31 - __clz(gpt)), g = e & (gpt - 1);
         at = g * kTile + position_of<BITS>(tok);
       }
       ts[at] = __half_as_ushort(sh);
@@ -261,7 +260,7 @@ __device__ __forceinline__ void sts128(uint32_t addr, uint32_t x, uint32_t y, ui
 // keeps its row (64 rows: two threads to a row), so that only constants are
 // added to its addresses (shared-memory addresses, 32 bits).
 template <int BITS, int D, bool VALUE, bool BYCOL>
-__device__ __forceinline__ void dequant_part(uint32_t codes, uint32_t table, int nsz, int part, int gshift,
+__device__ __forceinline__ void dequant_part(int t, uint32_t codes, uint32_t table, int nsz, int part, int gshift,
                                              uint32_t slot) {
   constexpr int kRowsAll = VALUE ? D : kTile;                 // rows of the packed block
   constexpr int kNR = VALUE ? (D < 128 ? D : 128) : kTile;    // rows of the part
@@ -270,7 +269,7 @@ __device__ __forceinline__ void dequant_part(uint32_t codes, uint32_t table, int
   constexpr int kChunks = kCols / kPer;
   constexpr int kStep = 128 / kNR;                            // pieces of a row that the threads take at once
   constexpr int kWord = 32 / BITS;                            // codes of a word
-  const int t = threadIdx.x & 127, row = t & (kNR - 1), chunk0 = t / kNR;
+  const int row = t & (kNR - 1), chunk0 = t / kNR;
   const int grow = row + (VALUE ? part * 128 : 0);            // row of the block
   const int gchunk0 = chunk0 + (VALUE ? 0 : part * kChunks);  // piece of the row
   uint32_t src = codes + (uint32_t)(gchunk0 * kRowsAll + grow) * 16;
@@ -339,10 +338,14 @@ __global__ void __launch_bounds__(threads_of(D, NT), 1) chunk_kernel(const Param
   constexpr int kParts = D > 128 ? D / 128 : 1;       // slots of a K or V tile
   constexpr int kSlotCh = kChunks / kParts;
   constexpr int kSlot = slot_bytes(D), kSlots = slots_of(D, NT);
-  constexpr int kThreads = threads_of(D, NT), kDq = dequant_groups(D, NT);
+  constexpr int kThreads = threads_of(D, NT), kDq = teams_of(D);
   constexpr int kSoftWarps = 4 * NT, kDqWarps = 4 * kDq;
-  constexpr int kMisc = kSoftWarps + kDqWarps;        // first warp of the last warpgroup: copies, products, segments
-  // A warpgroup waits for a slot's release by the parity of its round, so the
+  // (warps by role: chunk_attn.h)
+  enum { kCopies, kProducts, kSegments };
+  const int other = ((int)threadIdx.x >> 5) - kSoftWarps;
+  const int role = other >= 0 && (other & 3) == 3 ? other >> 2 : -1;
+  const int dq = other >= 0 && (other & 3) != 3 ? (other >> 2) * 3 + (other & 3) : -1;  // dequantising warp
+  // A team waits for a slot's release by the parity of its round, so the
   // round before last must be known to be over: it has waited for slot
   // (u - kDq + 1) kParts - 1 - kSlots before (its last unit), which must not
   // be older than u kParts - 2 kSlots.
@@ -361,7 +364,7 @@ __global__ void __launch_bounds__(threads_of(D, NT), 1) chunk_kernel(const Param
   const int nsz = kBlockTokens * D >> P.gshift;
 
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // the merge may be launched; it waits for this grid
-  if (warp == kMisc + 3 && lane == 0) {
+  if (role == kCopies && lane == 0) {
     for (int i = 0; i < P.units; ++i) {
       mbar_init(&aux->raw_full[i], 1);
       mbar_init(&aux->raw_empty[i], 4);
@@ -372,7 +375,6 @@ __global__ void __launch_bounds__(threads_of(D, NT), 1) chunk_kernel(const Param
       mbar_init(&aux->seg_full[i], 1);
       mbar_init(&aux->seg_empty[i], kSoftWarps + kDqWarps + 2);
     }
-    for (int i = 0; i < kDq; ++i) mbar_init(&aux->prep[i], 4);
     for (int i = 0; i < 2; ++i) {
       mbar_init(&aux->s[i], 1);
       mbar_init(&aux->p[i], 4);
@@ -386,7 +388,7 @@ __global__ void __launch_bounds__(threads_of(D, NT), 1) chunk_kernel(const Param
     fence_barrier_init();
   }
   __syncwarp();
-  if (warp == kMisc + 2) {
+  if (role == kSegments) {
     tmem_alloc(&aux->tmem, 512);
     tmem_relinquish();
   }
@@ -421,7 +423,7 @@ __global__ void __launch_bounds__(threads_of(D, NT), 1) chunk_kernel(const Param
 
     if (warp < kSoftWarps) {
       // ------------------------------------------------------------ softmax
-      // (registers at launch: 5 warpgroups x 96 of two row tiles, 6 x 80 of one;
+      // (registers at launch: 6 warpgroups x 80 of two row tiles, 5 x 96 of one;
       // head dim 256: 4 x 128, enough as they are)
       if (D <= 128) setmaxnreg_inc<NT == 2 ? 128 : 144>();
       const int i = warp >> 2, r = tid & 127;
@@ -634,59 +636,77 @@ __global__ void __launch_bounds__(threads_of(D, NT), 1) chunk_kernel(const Param
         }
         tc_fence_before();  // the accumulators are read before the next segment's products
       }
-    } else if (warp < kSoftWarps + kDqWarps) {
+    } else if (dq >= 0) {
       // -------------------------------------------------- dequantisation
-      if (D <= 128) setmaxnreg_dec<NT == 2 ? 72 : 64>();
-      const int me = (warp - kSoftWarps) >> 2;  // this warpgroup takes units me, me + kDq, ...
-      int u = 0, did = 0;
-      bool ok = true;
-      auto unit = [&](bool value) {  // the next K or V block
-        if (ok && u % kDq == me) {
-          const int slot_r = u % P.units;
-          unsigned char* src = raw + slot_r * P.unit_bytes;
-          unsigned char* table = tables + (me * 2 + (did & 1)) * P.table_bytes;
-          ok = __all_sync(0xffffffffu, wait(&aux->raw_full[slot_r], (u / P.units) & 1));
-          const bool by_column = value ? p.v_scheme == KVQ_TOKENWISE : p.k_scheme == KVQ_CHANNELWISE;
-          if (ok) {
-            const uint16_t* s = reinterpret_cast<const uint16_t*>(src + kBlockTokens * D * BITS / 8);
-            prepare_table<BITS>(s, s + nsz, nsz, by_column, value, D, P.gshift, aux->raw_bad[slot_r] != 0, table,
-                                p.dev_status);
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&aux->prep[me]);
-            ok = __all_sync(0xffffffffu, wait(&aux->prep[me], did & 1));
-          }
-          for (int part = 0; part < kParts && ok; ++part) {
-            const int n = u * kParts + part, sl = n % kSlots, round = n / kSlots;
-            if (round > 0) ok = __all_sync(0xffffffffu, wait(&aux->empty[sl], (round - 1) & 1));
-            if (!ok) break;
-            const uint32_t dst = smem_u32(ring) + sl * kSlot;
-            if (value) {
-              if (by_column) dequant_part<BITS, D, true, true>(smem_u32(src), smem_u32(table), nsz, part, P.gshift, dst);
-              else dequant_part<BITS, D, true, false>(smem_u32(src), smem_u32(table), nsz, part, P.gshift, dst);
-            } else {
-              if (by_column) dequant_part<BITS, D, false, true>(smem_u32(src), smem_u32(table), nsz, part, P.gshift, dst);
-              else dequant_part<BITS, D, false, false>(smem_u32(src), smem_u32(table), nsz, part, P.gshift, dst);
+      if (D <= 128) setmaxnreg_dec<NT == 2 ? 56 : 80>();
+      const int me = dq >> 2, t = (dq & 3) * 32 + lane;  // this team takes units me, me + kDq, ...
+      if (me < kDq) {
+        const bool k_col = p.k_scheme == KVQ_CHANNELWISE, v_col = p.v_scheme == KVQ_TOKENWISE;
+        // The team's own barrier, with a vote.  Every warp of it comes here after
+        // each segment is read and after each unit's table is written, whatever
+        // its waits returned, so that all of them go on or leave together.
+        auto together = [&](bool ok) -> bool {
+          uint32_t all;
+          asm volatile(
+              "{\n\t.reg .pred q, r;\n\tsetp.ne.u32 q, %1, 0;\n\tbarrier.cta.red.and.pred r, %2, 128, q;\n\t"
+              "selp.u32 %0, 1, 0, r;\n\t}"
+              : "=r"(all)
+              : "r"((uint32_t)ok), "r"(me + 1)
+              : "memory");
+          return all != 0;
+        };
+        // Units of a segment of n key tiles: K_0 V_0 K_1 V_1 ... with one score
+        // tile ahead, else K_0 K_1 V_0 K_2 V_1 ... K_n-1 V_n-2 V_n-1.
+        auto is_value = [](int i, int n) { return kAhead == 1 ? (i & 1) != 0 : (i >= 2 && !(i & 1)) || i == 2 * n - 1; };
+        int u = me, first = 0, did = 0;  // next unit, units of the segments before, units done
+        int slot_r = me, round_r = 0;    // its place in the ring of packed blocks
+        Segment g;
+        for (int k = 0; together(next_segment(k, g)); ++k) {
+          const int end = first + 2 * g.tiles;
+          bool ok = true;
+          for (; u < end; u += kDq) {
+            unsigned char* src = raw + slot_r * P.unit_bytes;
+            unsigned char* table = tables + (me * 2 + (did & 1)) * P.table_bytes;
+            const bool value = is_value(u - first, g.tiles), by_column = value ? v_col : k_col;
+            ok = ok && __all_sync(0xffffffffu, wait(&aux->raw_full[slot_r], round_r & 1));
+            if (ok) {
+              const uint16_t* s = reinterpret_cast<const uint16_t*>(src + kBlockTokens * D * BITS / 8);
+              prepare_table<BITS>(t, s, s + nsz, nsz, by_column, value, D, P.gshift, aux->raw_bad[slot_r] != 0, table,
+                                  p.dev_status);
             }
-            fence_proxy_async_smem();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&aux->full[sl]);
-          }
-          if (ok && lane == 0) mbar_arrive(&aux->raw_empty[slot_r]);
-          ++did;
-        }
-        ++u;
-      };
-      Segment g;
-      for (int k = 0; ok && next_segment(k, g); ++k) {
-        for (int j = -kAhead; j < g.tiles && ok; ++j) {
+            ok = together(ok);
+            if (!ok) break;
 #pragma unroll 1
-          for (int v = 1; v >= 0; --v)
-            if (v ? j >= 0 : j + kAhead < g.tiles) unit(v != 0);
+            for (int part = 0; part < kParts && ok; ++part) {
+              const int n = u * kParts + part, sl = n % kSlots, round = n / kSlots;
+              if (round > 0) ok = __all_sync(0xffffffffu, wait(&aux->empty[sl], (round - 1) & 1));
+              if (!ok) break;
+              const uint32_t dst = smem_u32(ring) + sl * kSlot;
+              if (value) {
+                if (by_column) dequant_part<BITS, D, true, true>(t, smem_u32(src), smem_u32(table), nsz, part, P.gshift, dst);
+                else dequant_part<BITS, D, true, false>(t, smem_u32(src), smem_u32(table), nsz, part, P.gshift, dst);
+              } else {
+                if (by_column) dequant_part<BITS, D, false, true>(t, smem_u32(src), smem_u32(table), nsz, part, P.gshift, dst);
+                else dequant_part<BITS, D, false, false>(t, smem_u32(src), smem_u32(table), nsz, part, P.gshift, dst);
+              }
+              fence_proxy_async_smem();
+              __syncwarp();
+              if (lane == 0) mbar_arrive(&aux->full[sl]);
+            }
+            if (ok && lane == 0) mbar_arrive(&aux->raw_empty[slot_r]);
+            ++did;
+            slot_r += kDq;
+            if (slot_r >= P.units) {
+              slot_r = me;
+              ++round_r;
+            }
+          }
+          first = end;
         }
       }
     } else {
-      if (D <= 128) setmaxnreg_dec<NT == 2 ? 72 : 64>();
-      if (warp == kMisc) {
+      if (D <= 128) setmaxnreg_dec<NT == 2 ? 56 : 80>();
+      if (role == kCopies) {
         // ---------------------------------------------------------- copies
         int u = 0;
         bool ok = true;
@@ -731,7 +751,7 @@ __global__ void __launch_bounds__(threads_of(D, NT), 1) chunk_kernel(const Param
           if ((p.flags & KVQ_FLAG_TEST_STALL) && s0 == 0 && n == 0) continue;
           drain(&aux->raw_full[n % P.units], (n / P.units) & 1);
         }
-      } else if (warp == kMisc + 1) {
+      } else if (role == kProducts) {
         // -------------------------------------------------------- products
         constexpr uint32_t idesc_s = make_idesc(0, 0, 0, 0, 128, 128);
         constexpr int kN = D < 128 ? D : 128;
@@ -829,7 +849,7 @@ __global__ void __launch_bounds__(threads_of(D, NT), 1) chunk_kernel(const Param
           ok = __shfl_sync(0xffffffffu, (int)ok, 0) != 0;
         }
         __syncwarp();
-      } else if (warp == kMisc + 2 && lane == 0) {
+      } else if (role == kSegments && lane == 0) {
         // ---------------------------------------------------------- segments
         Place at = aux->start;
         uint32_t bad = 0;
@@ -870,7 +890,7 @@ __global__ void __launch_bounds__(threads_of(D, NT), 1) chunk_kernel(const Param
   __syncwarp();
   tc_fence_before();
   __syncthreads();
-  if (warp == kMisc + 2) tmem_dealloc(tmem, 512);
+  if (role == kSegments) tmem_dealloc(tmem, 512);
   if (tid == 0 && aux->fail) report(p.dev_status, KVQ_DEV_TIMEOUT);
 }
 

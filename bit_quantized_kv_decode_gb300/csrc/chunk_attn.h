@@ -21,10 +21,15 @@ struct Params {
 __host__ __device__ constexpr int slot_bytes(int D) { return 128 * (D < 128 ? D : 128) * 2; }
 __host__ __device__ constexpr int q_bytes(int D, int nt) { return nt * 128 * D * 2; }
 __host__ __device__ constexpr int slots_of(int D, int nt) { return D > 128 ? 3 : 4; }
-// Dequantising warpgroups: they take K and V blocks in turn.  (Their code is a
-// chain of shared-memory loads and stores, so it takes several to fill the SM.)
-__host__ __device__ constexpr int dequant_groups(int D, int nt) { return nt == 2 || D > 128 ? 2 : 4; }
-__host__ __device__ constexpr int threads_of(int D, int nt) { return 128 * (nt + dequant_groups(D, nt) + 1); }
+// Warps.  The first nt warpgroups are the softmax's, a warp on each quarter of
+// the SM.  Of the others, every fourth warp (the last quarter's) has a role of
+// its own -- copies, products, segments -- and the rest dequantise, four warps
+// to a team: 12 of them, 8 with head dim 256, whose operand slots are few.  So
+// the warp that issues the products shares its quarter, and with it the
+// instruction buffer, with softmax warps only.
+__host__ __device__ constexpr int teams_of(int D) { return D > 128 ? 2 : 3; }
+__host__ __device__ constexpr int other_groups(int D) { return D > 128 ? 3 : 4; }
+__host__ __device__ constexpr int threads_of(int D, int nt) { return 128 * (nt + other_groups(D)); }
 __host__ __device__ constexpr int fixed_bytes(int D, int nt) { return q_bytes(D, nt) + slots_of(D, nt) * slot_bytes(D) + kAuxBytes; }
 
 cudaError_t launch_i2(int head_dim, int nt, const Params& p, int grid, size_t smem, cudaStream_t stream);
@@ -37,7 +42,7 @@ struct ChunkPlan {
   int nt, grid;
   size_t part_lse, total;  // workspace: partial outputs first
 };
-ChunkPlan chunk_plan(int head_dim, int batch, int total, int num_q_heads, int num_kv_heads);
+ChunkPlan chunk_plan(int head_dim, int group, int bits, int batch, int total, int num_q_heads, int num_kv_heads);
 cudaError_t launch_chunk_attn(const RowAttnParams& p, const ChunkPlan& plan, void* workspace, cudaStream_t stream);
 
 }  // namespace kvq

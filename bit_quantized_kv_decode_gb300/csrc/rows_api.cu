@@ -131,7 +131,7 @@ KVQ_API kvq_status kvq_chunk_workspace_size(const kvq_chunk_desc* d, size_t* byt
   kvq_status s = check_chunk(d);
   if (s != KVQ_OK) return s;
   if (bytes == nullptr) return KVQ_ERR_INVALID_ARG;
-  *bytes = chunk_plan(d->cache.head_dim, d->batch, d->total_tokens, d->num_q_heads, d->cache.num_kv_heads).total;
+  *bytes = chunk_plan(d->cache.head_dim, group_of(&d->cache), d->cache.bits, d->batch, d->total_tokens, d->num_q_heads, d->cache.num_kv_heads).total;
   return KVQ_OK;
 }
 
@@ -152,7 +152,7 @@ KVQ_API kvq_status kvq_chunk_attn(const kvq_chunk_desc* d, const kvq_rows* q, co
     if (!aligned4(ptr)) return KVQ_ERR_INVALID_ARG;
   if (page_table == nullptr && (long long)d->batch * d->max_blocks > d->cache.num_pages) return KVQ_ERR_INVALID_ARG;
   const ChunkPlan plan =
-      chunk_plan(d->cache.head_dim, d->batch, d->total_tokens, d->num_q_heads, d->cache.num_kv_heads);
+      chunk_plan(d->cache.head_dim, group_of(&d->cache), d->cache.bits, d->batch, d->total_tokens, d->num_q_heads, d->cache.num_kv_heads);
   if (workspace == nullptr || (reinterpret_cast<uintptr_t>(workspace) & 255u) != 0 || workspace_bytes < plan.total)
     return KVQ_ERR_WORKSPACE;
   s = check_device(nullptr);
