@@ -9,6 +9,11 @@
 // probabilities back as the A operand of the second product.  Warp 8 copies Q,
 // K and V by TMA into a ring of slots; warp 9 issues the MMAs:
 //   S_i = Q_i K^T (both from shared memory), O_i += P_i V (P from tensor memory).
+// Only a few MMAs queue up in the tensor core, so whatever the issuing thread
+// does in between that takes longer leaves it idle.  Warp 10 therefore does its
+// waiting for copies: it arrives at the probabilities' barriers too, once the
+// tile's V (and, two row tiles, the next K, which is copied with it) is there,
+// and the issuing thread waits for that barrier alone.
 // With two tiles (head dims 64 and 128) the tensor cores work on one tile's
 // products while the other's softmax runs; with one (head dim 256: two
 // accumulators would not fit tensor memory) the scores are double-buffered
@@ -57,14 +62,17 @@ struct Shape {
   static constexpr int kParts = kChunks / kSlotCh;       // slots of a K or V tile
   static constexpr int kSlotBytes = kSlotCh * 16384;
   static constexpr int kQBytes = kNT * kChunks * 16384;
-  static constexpr int kSlots = D == 64 ? 8 : 5;
+  // Two row tiles: K of the first key tile in slot 0, then pairs (V of tile j,
+  // K of tile j + 1), copied and given up together.  One: single slots.
+  static constexpr int kPairs = D == 64 ? 3 : 2;
+  static constexpr int kSlots = kNT == 2 ? 1 + 2 * kPairs : 5;
   static constexpr int kThreads = 384;  // three warpgroups: softmax, softmax, copies and products
   static constexpr int kSmem = kQBytes + kSlots * kSlotBytes + 512 + 4 * D;
   static_assert(kSmem <= 227 * 1024, "shared memory");
 };
 
 struct Aux {  // after the ring
-  uint64_t full[8], empty[8], q, fixed[2], s[2], p[2], sums, done;
+  uint64_t full[8], empty[8], first, q, fixed[2], s[2], p[2], sums, done;
   uint32_t tmem;
   int fail, any_bad;
   int seq_first, seq_n, tile;  // this CTA's sequence (rows [first, first + n)) and tile; tile < 0: none
@@ -232,17 +240,18 @@ prompt_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__
       tma_prefetch_map(&map_q);
       tma_prefetch_map(&map_k);
       tma_prefetch_map(&map_v);
-      for (int i = 0; i < Sh::kSlots; ++i) {
+      for (int i = 0; i < 8; ++i) {
         mbar_init(&aux->full[i], 1);
         mbar_init(&aux->empty[i], 1);
       }
       mbar_init(&aux->q, 1);
+      mbar_init(&aux->first, 1);
       mbar_init(&aux->sums, 1);
       mbar_init(&aux->done, 1);
       for (int i = 0; i < 2; ++i) {
         mbar_init(&aux->fixed[i], 1);
         mbar_init(&aux->s[i], 1);
-        mbar_init(&aux->p[i], 4);
+        mbar_init(&aux->p[i], 5);  // the row tile's warps and the one that waits for copies
       }
       aux->fail = 0;
       aux->any_bad = 0;
@@ -308,33 +317,65 @@ prompt_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__
             tma_load_3d(q_s + (i * Sh::kChunks + c) * 16384, &map_q, c * 64, kvh * p.gq, first + tok0 + i * tok_tile,
                         &aux->q);
       }
-      const bool stall = (p.flags & KVQ_FLAG_TEST_STALL) && blockIdx.x == 0;
-      for (int i = 0; i < Sh::kAhead && i < tiles; ++i)
-        for (int part = 0; part < Sh::kParts; ++part) load(map_k, last - i, part);
-      for (int i = 0; i < tiles && ok; ++i) {
-        if (stall) break;  // test hook: the V tiles of the first CTA are withheld
-        const int vslot = slot, vround = round;
-        for (int part = 0; part < Sh::kParts; ++part) load(map_v, last - i, part);
-        if (i + Sh::kAhead < tiles)
-          for (int part = 0; part < Sh::kParts; ++part) load(map_k, last - i - Sh::kAhead, part);
-        if (i < mend && ok) {
-          int s = vslot, r = vround;
-          for (int part = 0; part < Sh::kParts && ok; ++part) {
-            ok = __all_sync(0xffffffffu, wait(&aux->full[s], r & 1));
-            if (ok)
-              mend_values<FP16>(ring + s * Sh::kSlotBytes, Sh::kSlotCh, part * Sh::kSlotCh * 64,
-                                (last - i - clean) * kTile, min(kTile, n - (last - i) * kTile), bad, &aux->any_bad);
-            if (++s == Sh::kSlots) { s = 0; ++r; }
+      const bool stall = (p.flags & KVQ_FLAG_TEST_STALL) && blockIdx.x == 0;  // test hook: V of the first CTA is withheld
+      auto mend_tile = [&](int j, int sl, int rd, uint64_t* loaded, uint32_t parity) {
+        // V of the walk's tile j, in the slots from sl on
+        for (int part = 0; part < Sh::kParts && ok; ++part) {
+          ok = __all_sync(0xffffffffu, wait(NT == 2 ? loaded : &aux->full[sl], NT == 2 ? parity : rd & 1));
+          if (ok)
+            mend_values<FP16>(ring + sl * Sh::kSlotBytes, Sh::kSlotCh, part * Sh::kSlotCh * 64, (last - j - clean) * kTile,
+                              min(kTile, n - (last - j) * kTile), bad, &aux->any_bad);
+          if (++sl == Sh::kSlots) { sl = 0; ++rd; }
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&aux->fixed[j]);
+      };
+      if (NT == 2) {
+        auto copy = [&](const CUtensorMap& map, int j, int sl, uint64_t* bar) {
+#pragma unroll
+          for (int c = 0; c < Sh::kSlotCh; ++c)
+            tma_load_3d(ring + sl * Sh::kSlotBytes + c * 16384, &map, c * 64, kvh, first + j * kTile, bar);
+        };
+        if (lane == 0) {
+          mbar_arrive_expect_tx(&aux->first, Sh::kSlotBytes);
+          copy(map_k, last, 0, &aux->first);
+        }
+        auto mend_pair = [&](int j) {
+          const int m = j % Sh::kPairs;
+          mend_tile(j, 1 + 2 * m, 0, &aux->full[m], j / Sh::kPairs & 1);
+        };
+        for (int j = 0; j < tiles && ok && !stall; ++j) {
+          const int m = j % Sh::kPairs;
+          if (j >= Sh::kPairs) ok = __all_sync(0xffffffffu, wait(&aux->empty[m], (j / Sh::kPairs - 1) & 1));
+          if (!ok) break;
+          if (lane == 0) {
+            const bool more = j + 1 < tiles;
+            mbar_arrive_expect_tx(&aux->full[m], (more ? 2 : 1) * Sh::kSlotBytes);
+            copy(map_v, last - j, 1 + 2 * m, &aux->full[m]);
+            if (more) copy(map_k, last - j - 1, 2 + 2 * m, &aux->full[m]);
           }
-          fence_proxy_async_smem();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&aux->fixed[i]);
+          ++issued;
+          // the tile before, with this one's copies on their way
+          if (j > 0 && j - 1 < mend) mend_pair(j - 1);
+        }
+        if (ok && !stall && tiles - 1 < mend) mend_pair(tiles - 1);
+      } else {
+        for (int i = 0; i < Sh::kAhead && i < tiles; ++i)
+          for (int part = 0; part < Sh::kParts; ++part) load(map_k, last - i, part);
+        for (int i = 0; i < tiles && ok && !stall; ++i) {
+          const int vslot = slot, vround = round;
+          for (int part = 0; part < Sh::kParts; ++part) load(map_v, last - i, part);
+          if (i + Sh::kAhead < tiles)
+            for (int part = 0; part < Sh::kParts; ++part) load(map_k, last - i - Sh::kAhead, part);
+          if (i < mend && ok) mend_tile(i, vslot, vround, nullptr, 0);
         }
       }
       // copies in flight land before this CTA's shared memory is given up
-      const int from = issued > Sh::kSlots ? issued - Sh::kSlots : 0;
-      for (int k = from; k < issued; ++k)
-        drain(&aux->full[k % Sh::kSlots], (k / Sh::kSlots) & 1);
+      constexpr int kRing = NT == 2 ? Sh::kPairs : Sh::kSlots;
+      for (int k = issued > kRing ? issued - kRing : 0; k < issued; ++k)
+        drain(&aux->full[k % kRing], (k / kRing) & 1);
+      if (NT == 2) drain(&aux->first, 0);
       drain(&aux->q, 0);
     } else if (warp == 9) {
       // ------------------------------------------------------------ products
@@ -344,7 +385,6 @@ prompt_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__
         constexpr int kN = D < 128 ? D : 128;
         constexpr uint32_t idesc_o = make_idesc(fmt, fmt, 0, 1, 128, kN);
         const uint32_t q_a = smem_u32(q_s), ring_a = smem_u32(ring);
-        int slot = 0, round = 0;  // next slot to consume
         bool ok = wait(&aux->q, 0);
         // S of row tile i <- Q_i K^T with K in the slots from `sl`
         auto scores = [&](int i, int buf, int sl) {
@@ -364,58 +404,108 @@ prompt_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__
             if (++sl == Sh::kSlots) sl = 0;
           }
         };
-        auto take = [&](int& sl) {  // the next tile's slots, loaded
-          sl = slot;
-          for (int part = 0; part < Sh::kParts && ok; ++part) {
-            ok = wait(&aux->full[slot], round & 1);
-            if (++slot == Sh::kSlots) { slot = 0; ++round; }
-          }
-        };
-        auto release = [&](int sl) {
-          for (int part = 0; part < Sh::kParts; ++part) {
-            tc_commit(&aux->empty[sl]);
-            if (++sl == Sh::kSlots) sl = 0;
-          }
-        };
-        int ks;
+        if (NT == 2) {
+          ok = ok && wait(&aux->first, 0);
+          int m = 0;  // the pair of tile j
 #pragma unroll 1
-        for (int j = 0; j < Sh::kAhead && j < tiles && ok; ++j) {
-          take(ks);
-          if (!ok) break;
+          for (int j = -1; j < tiles && ok; ++j) {
+            const bool more = j + 1 < tiles;
 #pragma unroll 1
-          for (int i = 0; i < act; ++i) {
-            scores(i, NT == 2 ? i : j, ks);
-            tc_commit(&aux->s[NT == 2 ? i : j]);
-          }
-          release(ks);
-        }
-#pragma unroll 1
-        for (int j = 0; j < tiles && ok; ++j) {
-          int vs;
-          take(vs);
-          if (ok && j < mend) ok = wait(&aux->fixed[j], 0);
-          const bool more = j + Sh::kAhead < tiles;
-          if (ok && more) take(ks);
-#pragma unroll 1
-          for (int i = 0; i < act && ok; ++i) {
-            const int buf = NT == 2 ? i : j & 1;
-            ok = wait(&aux->p[buf], (NT == 2 ? j : j >> 1) & 1);
-            if (!ok) break;
-            tc_fence_after();
-            values(i, buf, vs, j > 0);
-            if (NT == 1) tc_commit(&aux->sums);
-            if (i == act - 1) release(vs);
-            if (more) {
-              scores(i, buf, ks);
-              tc_commit(&aux->s[buf]);
+            for (int i = 0; i < act; ++i) {
+              if (j >= 0) {
+                if (!(ok = wait(&aux->p[i], j & 1))) break;  // the probabilities, and the pair's copies
+                tc_fence_after();
+                values(i, i, 1 + 2 * m, j > 0);
+              }
+              if (more) {
+                scores(i, i, j < 0 ? 0 : 2 + 2 * m);
+                tc_commit(&aux->s[i]);
+              }
+            }
+            if (j >= 0) {
+              tc_commit(&aux->empty[m]);
+              if (++m == Sh::kPairs) m = 0;
             }
           }
-          if (ok && more) release(ks);
+        } else {
+          int slot = 0, round = 0;  // next slot to consume
+          auto pass = [&](int& sl) {  // the next tile's slots
+            sl = slot;
+            for (int part = 0; part < Sh::kParts; ++part)
+              if (++slot == Sh::kSlots) { slot = 0; ++round; }
+          };
+          auto take = [&](int& sl) {  // ... loaded
+            const int r0 = round;
+            pass(sl);
+            for (int part = 0, at = sl, r = r0; part < Sh::kParts && ok; ++part) {
+              ok = wait(&aux->full[at], r & 1);
+              if (++at == Sh::kSlots) { at = 0; ++r; }
+            }
+          };
+          auto release = [&](int sl) {
+            for (int part = 0; part < Sh::kParts; ++part) {
+              tc_commit(&aux->empty[sl]);
+              if (++sl == Sh::kSlots) sl = 0;
+            }
+          };
+          int ks, vs;
+#pragma unroll 1
+          for (int j = -Sh::kAhead; j < tiles && ok; ++j) {
+            const int buf = j & 1;
+            if (j >= 0) {
+              pass(vs);
+              if (!(ok = wait(&aux->p[buf], j >> 1 & 1))) break;  // the probabilities, and V's copies
+              tc_fence_after();
+              values(0, buf, vs, j > 0);
+              tc_commit(&aux->sums);
+              release(vs);
+            }
+            if (j + Sh::kAhead < tiles) {
+              take(ks);
+              if (!ok) break;
+              scores(0, buf, ks);
+              tc_commit(&aux->s[buf]);
+              release(ks);
+            }
+          }
         }
         tc_commit(&aux->done);
         drain(&aux->done, 0);  // nothing in flight when tensor memory is freed
       }
       __syncwarp();
+    } else if (warp == 10 && lane == 0) {
+      // ------------------------------------------------------------ copies' arrival, for the products
+      bool ok = true;
+      int slot = 0, round = 0;  // one row tile: every slot in turn, so that each wait is for the round after the last
+      auto next_tile = [&] {
+        for (int part = 0; part < Sh::kParts && ok; ++part) {
+          ok = wait(&aux->full[slot], round & 1);
+          if (++slot == Sh::kSlots) { slot = 0; ++round; }
+        }
+      };
+      if (NT == 1)
+        for (int i = 0; i < Sh::kAhead && i < tiles; ++i) next_tile();  // K
+#pragma unroll 1
+      for (int j = 0; j < tiles && ok; ++j) {
+        if (NT == 2) {
+          ok = wait(&aux->full[j % Sh::kPairs], j / Sh::kPairs & 1);
+        } else {
+          if (j > 0 && j - 1 + Sh::kAhead < tiles) next_tile();  // the K tile copied before this V
+          next_tile();
+        }
+        if (ok && j < mend) ok = wait(&aux->fixed[j], 0);
+        if (!ok) break;
+        // (an arrival counts for the barrier's present phase: the one before must be over)
+        if (NT == 2) {
+          for (int i = 0; i < act && ok; ++i) {
+            if (j > 0) ok = wait(&aux->p[i], (j - 1) & 1);
+            mbar_arrive(&aux->p[i]);
+          }
+        } else {
+          if (j > 1) ok = wait(&aux->p[j & 1], (j >> 1 & 1) ^ 1);
+          mbar_arrive(&aux->p[j & 1]);
+        }
+      }
     }
     } else {
       // ------------------------------------------------------------ softmax
