@@ -17,6 +17,7 @@ __global__ void __launch_bounds__(kMergeThreads) merge_kernel(const Params P, in
   asm volatile("griddepcontrol.wait;" ::: "memory");
   __shared__ long long scan[kMergeThreads / 32], range[3];
   __shared__ Place at;
+  __shared__ int list[kGrid], parts;
   const RowAttnParams& p = P.r;
   const int cta = blockIdx.x + 1, tid = threadIdx.x, lane = tid & 31;
   const int tok_tile = kTile / p.gq, tok_cta = tok_tile * nt;
@@ -29,36 +30,48 @@ __global__ void __launch_bounds__(kMergeThreads) merge_kernel(const Params P, in
   const Seq s = load_seq(p, at.b, &bad);
   const long long end = tile0 + tile_steps(s, at.t, tok_cta, p.causal);
   const int slot0 = 2 * (cta - 1) + (before == tile0 ? 0 : 1);
+  // The parts: CTA cta - 1's, then one of every CTA that begins before the end
+  // and has steps (all have, where there are as many steps as CTAs).
+  if (tid == 0) {
+    int n = 0;
+    for (int c = cta; c < grid && total * c / grid < end; ++c)
+      if (total >= grid || total * (c + 1) / grid > total * c / grid) list[n++] = 2 * c;
+    parts = n;
+  }
+  __syncthreads();
+  const size_t pitch = (size_t)nt * kTile;
   for (int i = tid >> 5; i < kMergeRows; i += kMergeThreads / 32) {
     const int prow = blockIdx.y * kMergeRows + i, r = prow & (kTile - 1);
     const int tile_tok = at.t * tok_cta + (prow / kTile) * tok_tile, tok = tile_tok + r / p.gq;
     if (r >= tok_tile * p.gq || tok >= s.n) continue;
-    const size_t pitch = (size_t)nt * kTile;
-    auto part = [&](int c) { return (size_t)(c < cta ? slot0 : 2 * c) * pitch + prow; };
+    auto part = [&](int k) { return (size_t)(k == 0 ? slot0 : list[k - 1]) * pitch + prow; };
     float m = -INFINITY;
-    for (int c = cta - 1 + lane; c < grid && total * c / grid < end; c += 32)
-      if (c < cta || total * (c + 1) / grid > total * c / grid) m = fmaxf(m, P.part_lse[part(c)]);
+    for (int k = lane; k <= parts; k += 32) m = fmaxf(m, P.part_lse[part(k)]);
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-    float acc[D / 32], sum = 0.f;
+    constexpr int kPer = D / 32;  // channels of a lane
+    float acc[kPer], sum = 0.f;
 #pragma unroll
-    for (int c = 0; c < D / 32; ++c) acc[c] = 0.f;
-    for (int c = cta - 1; c < grid && total * c / grid < end; ++c) {
-      if (c >= cta && total * (c + 1) / grid <= total * c / grid) continue;
-      const size_t at_part = part(c);
+    for (int c = 0; c < kPer; ++c) acc[c] = 0.f;
+#pragma unroll 2
+    for (int k = 0; k <= parts; ++k) {
+      const size_t at_part = part(k);
       const float l = P.part_lse[at_part];
-      if (l == -INFINITY) continue;  // nothing seen in this part
-      const float w = exp2f(l - m);
+      const float w = m == -INFINITY ? 0.f : exp2f(l - m);  // 0: nothing seen in this part
       sum += w;
-      const float* o = P.part_o + at_part * D + lane * (D / 32);
+      const float2* o = reinterpret_cast<const float2*>(P.part_o + at_part * D + lane * kPer);
 #pragma unroll
-      for (int e = 0; e < D / 32; ++e) acc[e] = fmaf(w, o[e], acc[e]);
+      for (int e = 0; e < kPer / 2; ++e) {
+        const float2 v = o[e];
+        acc[2 * e] = fmaf(w, v.x, acc[2 * e]);
+        acc[2 * e + 1] = fmaf(w, v.y, acc[2 * e + 1]);
+      }
     }
     const float inv = sum > 0.f || isnan(sum) ? 1.f / sum : 0.f;
     const long long row = (long long)(s.first + tok) * p.num_q_heads + at.h * p.gq + r % p.gq;
-    uint32_t* dst = reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(p.out) + row * D + lane * (D / 32));
+    uint32_t* dst = reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(p.out) + row * D + lane * kPer);
 #pragma unroll
-    for (int e = 0; e < D / 64; ++e)
+    for (int e = 0; e < kPer / 2; ++e)
       dst[e] = p.fp16 ? rows::round2<true>(acc[2 * e] * inv, acc[2 * e + 1] * inv)
                       : rows::round2<false>(acc[2 * e] * inv, acc[2 * e + 1] * inv);
     if (lane == 0 && p.lse != nullptr)

@@ -450,7 +450,7 @@ __global__ void __launch_bounds__(threads_of(D, NT), 1) chunk_kernel(const Param
           float mul = 1.f;
           if (mine && !p.fp16) {
             uint32_t most = 0;
-#pragma unroll 8
+#pragma unroll 16
             for (int e = 0; e < D / 8; ++e) {
               const uint4 v = src[e];
               most = __vmaxu2(most, __vmaxu2(__vmaxu2(v.x & 0x7fff7fffu, v.y & 0x7fff7fffu),
@@ -464,7 +464,7 @@ __global__ void __launch_bounds__(threads_of(D, NT), 1) chunk_kernel(const Param
             }
           }
           if (any) {
-#pragma unroll 2
+#pragma unroll 4
             for (int e = 0; e < D / 16; ++e) {
               float f[16];
 #pragma unroll
