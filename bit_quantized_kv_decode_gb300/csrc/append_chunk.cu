@@ -37,7 +37,10 @@
 namespace kvq {
 namespace {
 
-constexpr int kThreads = 256, kWarps = 8, kWarpTok = kBlockTokens / kWarps;  // tokens of a warp
+// Warps of a block.  Edges: twice as many, each with half the tokens (8 of a
+// thread): their loads and stores depend on one another, so what counts is how
+// many warps wait at a time.
+constexpr int kBlockWarps = 8, kEdgeWarps = 16;
 
 __device__ __forceinline__ float min_nan(float a, float b) {
   float r;
@@ -173,61 +176,63 @@ __device__ __forceinline__ int part_blocks(const Chunk& c) {
   return PART == kWhole ? whole_blocks(c) : PART == kEdges ? touched_blocks(c) - whole_blocks(c) : touched_blocks(c);
 }
 
-// The sequence and block of the rank-th block that the kernel takes, by one
-// warp: found[0] = sequence (-1: none), found[1] = block, counted from the
+// The i-th block of a sequence that the kernel takes, counted from the
 // sequence's first touched one.
 template <Part PART>
-__device__ __forceinline__ void find_block(const AppendParams& p, int rank, bool report_bad, int* found) {
+__device__ __forceinline__ int block_of(const Chunk& c, int i) {
+  const int lead = c.len % kBlockTokens != 0 ? 1 : 0;  // an edge before the whole ones?
+  return PART == kWhole ? lead + i : PART == kEdges && i >= lead ? i + whole_blocks(c) : i;
+}
+
+// The sequence and block of a CTA, by one warp: found[0] = sequence (-1:
+// none), found[1] = block.  With SKIP blocks of every sequence left out, the
+// rank-th of the rest.
+template <Part PART, int SKIP>
+__device__ __forceinline__ void find_block(const AppendParams& p, int rank, int* found) {
   const int lane = threadIdx.x & 31;
   if (lane == 0) found[0] = -1;
   __syncwarp();
   constexpr int kAt = 4;  // sequences of a lane at a time: their loads overlap
-  for (int b0 = 0; b0 < p.batch; b0 += 32 * kAt) {
+  for (int b0 = 0; b0 < p.batch && rank >= 0; b0 += 32 * kAt) {
     Chunk c[kAt];
 #pragma unroll
     for (int k = 0; k < kAt; ++k) {
       const int b = b0 + 32 * k + lane;
       c[k] = Chunk{{0, 0, false}, 0, true};
-      if (b < p.batch) {
-        c[k] = load_chunk(p, b);
-        if (c[k].bad && report_bad) report(p.dev_status, KVQ_DEV_BAD_SEQ_LEN);
-      }
+      if (b < p.batch) c[k] = load_chunk(p, b);
     }
-    int left = rank;
 #pragma unroll
     for (int k = 0; k < kAt; ++k) {
       if (b0 + 32 * k >= p.batch) break;
-      const int blocks = part_blocks<PART>(c[k]);
+      const int blocks = max(0, part_blocks<PART>(c[k]) - SKIP);
       int incl = blocks;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
         const int v = __shfl_up_sync(0xffffffffu, incl, o);
         if (lane >= o) incl += v;
       }
-      const int i = left - (incl - blocks);
+      const int i = rank - (incl - blocks);
       if (i >= 0 && i < blocks) {
         found[0] = b0 + 32 * k + lane;
-        const int whole = whole_blocks(c[k]), lead = c[k].len % kBlockTokens != 0 ? 1 : 0;  // an edge before the whole ones?
-        found[1] = PART == kWhole ? lead + i : PART == kEdges && i >= lead ? i + whole : i;
+        found[1] = block_of<PART>(c[k], i + SKIP);
       }
-      left -= __shfl_sync(0xffffffffu, incl, 31);
+      rank -= __shfl_sync(0xffffffffu, incl, 31);
     }
-    if (left < 0 && !report_bad) break;  // (the reporting CTA looks at every sequence)
-    rank = left;
   }
 }
 
 // Channel-wise groups of a tile, by the whole block: the warps' ranges in
 // `ranges` ([low, high][warp][channel]) become scales and offsets ([s,
 // z][token group][channel]); their 16-bit forms go to s_out, z_out.
-template <int BITS, int W>
-__device__ __forceinline__ void channel_groups(float (*ranges)[kWarps][W], int groups, int gw, uint16_t* s_out,
+template <int BITS, int W, int NW>
+__device__ __forceinline__ void channel_groups(float (*ranges)[NW][W], int groups, int gw, uint16_t* s_out,
                                                uint16_t* z_out, uint32_t* dev_status) {
+  constexpr int kThreads = 32 * NW, kEach = 512 / kThreads;  // groups * W <= 512
   const int tid = threadIdx.x;
-  Group mine[2];  // groups * W / 256 <= 2 of a thread
+  Group mine[kEach];
   __syncthreads();
 #pragma unroll
-  for (int k = 0; k < 2; ++k) {
+  for (int k = 0; k < kEach; ++k) {
     const int e = tid + k * kThreads;
     if (e < groups * W) {
       const int g = e / W, c = e % W;
@@ -244,7 +249,7 @@ __device__ __forceinline__ void channel_groups(float (*ranges)[kWarps][W], int g
   }
   __syncthreads();
 #pragma unroll
-  for (int k = 0; k < 2; ++k) {
+  for (int k = 0; k < kEach; ++k) {
     const int e = tid + k * kThreads;
     if (e < groups * W) {
       ranges[0][e / W][e % W] = mine[k].s;
@@ -256,8 +261,9 @@ __device__ __forceinline__ void channel_groups(float (*ranges)[kWarps][W], int g
 
 template <typename T, int BITS, int W, Part PART>  // W: channels of the slab
 __device__ __forceinline__ void append_edge(const AppendParams& p) {
+  constexpr int kWarps = kEdgeWarps, kThreads = 32 * kWarps, kWarpTok = kBlockTokens / kWarps;  // tokens of a warp
   constexpr int kLanes = W / 4;                 // lanes that share a token
-  constexpr int kTok = kWarpTok * kLanes / 32;  // tokens of a thread (16 or 8)
+  constexpr int kTok = kWarpTok * kLanes / 32;  // tokens of a thread (8 or 4)
   constexpr int kPer = 128 / BITS;              // codes of a 16-byte piece
   constexpr int kPieces = W * BITS;             // 16-byte pieces of the slab's block: 128 W BITS / 128
   constexpr float kMax = (float)((1 << BITS) - 1);
@@ -272,7 +278,17 @@ __device__ __forceinline__ void append_edge(const AppendParams& p) {
   const int h = blockIdx.y, which = blockIdx.z & 1, slab = blockIdx.z >> 1;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const bool lead = h == 0 && blockIdx.z == 0;
-  if (warp == 0) find_block<PART>(p, blockIdx.x, lead && blockIdx.x == 0, found);
+  // the first `batch` CTAs take the first block of a sequence each, the others what more there is
+  if (blockIdx.x < p.batch) {
+    if (tid == 0) {
+      const Chunk c = load_chunk(p, blockIdx.x);
+      if (c.bad && lead) report(p.dev_status, KVQ_DEV_BAD_SEQ_LEN);
+      found[0] = part_blocks<PART>(c) > 0 ? (int)blockIdx.x : -1;
+      found[1] = block_of<PART>(c, 0);
+    }
+  } else if (warp == 0) {
+    find_block<PART, 1>(p, blockIdx.x - p.batch, found);
+  }
   __syncthreads();
   const int b = found[0], nth = found[1];
   if (b < 0) return;
@@ -474,7 +490,7 @@ __device__ __forceinline__ void append_edge(const AppendParams& p) {
     *reinterpret_cast<float4*>(&lo_s[warp][ch]) = make_float4(mn[0], mn[1], mn[2], mn[3]);
     *reinterpret_cast<float4*>(&hi_s[warp][ch]) = make_float4(mx[0], mx[1], mx[2], mx[3]);
     const int gw = G / kWarpTok, groups = kBlockTokens / G;  // warps of a token group, token groups
-    channel_groups<BITS, W>(ranges, groups, gw, s_out, z_out, p.dev_status);
+    channel_groups<BITS, W, kWarps>(ranges, groups, gw, s_out, z_out, p.dev_status);
     const int g = warp * kWarpTok / G;
     const float4 s4 = *reinterpret_cast<const float4*>(&lo_s[g][ch]);
     const float4 z4 = *reinterpret_cast<const float4*>(&hi_s[g][ch]);
@@ -570,7 +586,7 @@ __device__ __forceinline__ void append_edge(const AppendParams& p) {
 }
 
 template <typename T, int BITS, int W, Part PART>
-__global__ void __launch_bounds__(kThreads, 2) append_edges_kernel(const AppendParams p) {
+__global__ void __launch_bounds__(32 * kEdgeWarps, sizeof(Raw<T>) == 8 ? 2 : 1) append_edges_kernel(const AppendParams p) {
   append_edge<T, BITS, W, PART>(p);
   // launched beside append_blocks_kernel: what follows in the stream waits for
   // this grid, which is not done before that one is
@@ -620,7 +636,8 @@ __device__ __forceinline__ void reduce_group2(uint32_t (&v)[N], int lg) {
 }
 
 template <typename T, int BITS, int W>
-__global__ void __launch_bounds__(kThreads, 3) append_blocks_kernel(const AppendParams p) {
+__global__ void __launch_bounds__(32 * kBlockWarps, 3) append_blocks_kernel(const AppendParams p) {
+  constexpr int kWarps = kBlockWarps, kThreads = 32 * kWarps, kWarpTok = kBlockTokens / kWarps;  // tokens of a warp
   constexpr int kLanes = W / 4, kTok = kWarpTok * kLanes / 32, kPer = 128 / BITS;
   constexpr int kPieces = W * BITS;
   constexpr float kMax = (float)((1 << BITS) - 1);
@@ -638,7 +655,7 @@ __global__ void __launch_bounds__(kThreads, 3) append_blocks_kernel(const Append
   const int D = p.head_dim;
   const int h = blockIdx.y, which = blockIdx.z & 1, slab = blockIdx.z >> 1;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  if (warp == 0) find_block<kWhole>(p, blockIdx.x, false, found);
+  if (warp == 0) find_block<kWhole, 0>(p, blockIdx.x, found);
   __syncthreads();
   const int b = found[0];
   if (b < 0) return;
@@ -751,7 +768,7 @@ __global__ void __launch_bounds__(kThreads, 3) append_blocks_kernel(const Append
     a = wide<T>(hi.x);
     c = wide<T>(hi.y);
     *reinterpret_cast<float4*>(&ranges[1][warp][ch]) = make_float4(a.x, a.y, c.x, c.y);
-    channel_groups<BITS, W>(ranges, kBlockTokens / G, G / kWarpTok, s_out, z_out, p.dev_status);
+    channel_groups<BITS, W, kWarps>(ranges, kBlockTokens / G, G / kWarpTok, s_out, z_out, p.dev_status);
     const int g = warp * kWarpTok / G;
     const float4 s4 = *reinterpret_cast<const float4*>(&ranges[0][g][ch]);
     const float4 z4 = *reinterpret_cast<const float4*>(&ranges[1][g][ch]);
@@ -811,7 +828,7 @@ cudaError_t launch_w(const AppendParams& p, cudaStream_t stream) {
   const bool whole = kHalf && p.total >= kBlockTokens;  // there may be blocks of new tokens alone
   if constexpr (kHalf) {
     if (whole) {
-      append_blocks_kernel<T, BITS, W><<<dim3((unsigned)(p.total / kBlockTokens), heads, planes), kThreads, 0, stream>>>(p);
+      append_blocks_kernel<T, BITS, W><<<dim3((unsigned)(p.total / kBlockTokens), heads, planes), 32 * kBlockWarps, 0, stream>>>(p);
       const cudaError_t e = cudaGetLastError();
       if (e != cudaSuccess) return e;
     }
@@ -822,7 +839,7 @@ cudaError_t launch_w(const AppendParams& p, cudaStream_t stream) {
   const long long blocks = p.batch + two + (kHalf ? 0 : (p.total - 2 * two) / kBlockTokens);
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)blocks, heads, planes);
-  cfg.blockDim = dim3(kThreads);
+  cfg.blockDim = dim3(32 * kEdgeWarps);
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
