@@ -278,25 +278,29 @@ __device__ __forceinline__ void append_edge(const AppendParams& p) {
   const int h = blockIdx.y, which = blockIdx.z & 1, slab = blockIdx.z >> 1;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const bool lead = h == 0 && blockIdx.z == 0;
-  // the first `batch` CTAs take the first block of a sequence each, the others what more there is
-  if (blockIdx.x < p.batch) {
-    if (tid == 0) {
-      const Chunk c = load_chunk(p, blockIdx.x);
-      if (c.bad && lead) report(p.dev_status, KVQ_DEV_BAD_SEQ_LEN);
-      found[0] = part_blocks<PART>(c) > 0 ? (int)blockIdx.x : -1;
-      found[1] = block_of<PART>(c, 0);
-    }
-  } else if (warp == 0) {
-    find_block<PART, 1>(p, blockIdx.x - p.batch, found);
+  // the first `batch` CTAs take the first block of a sequence each (every thread
+  // looks for itself), the others what more there is
+  int b = blockIdx.x, nth = 0;
+  if (blockIdx.x >= p.batch) {
+    if (warp == 0) find_block<PART, 1>(p, blockIdx.x - p.batch, found);
+    __syncthreads();
+    b = found[0];
+    nth = found[1];
+    if (b < 0) return;
   }
-  __syncthreads();
-  const int b = found[0], nth = found[1];
-  if (b < 0) return;
-  const SeqRows s = seq_rows(p.cu, b, p.total);
-  const int len = p.seq_lens[b], end = len + s.n;
+  const Chunk chunk = load_chunk(p, b);
+  if (blockIdx.x < p.batch) {
+    if (chunk.bad && lead && tid == 0) report(p.dev_status, KVQ_DEV_BAD_SEQ_LEN);
+    if (part_blocks<PART>(chunk) <= 0) return;
+    nth = block_of<PART>(chunk, 0);
+  }
+  const SeqRows s = chunk.rows;
+  const int len = chunk.len, end = len + s.n;
   const int j = len / kBlockTokens + nth, t0 = j * kBlockTokens;
   const int nv = min(kBlockTokens, end - t0);  // rows of this block
   const int from = min(max(len - t0, 0), nv);  // ... that were there before
+  // (asked for now, needed at the end; an empty chunk may be at the end of its table)
+  const int page = s.n == 0 ? -1 : p.page_table ? p.page_table[(size_t)b * p.max_blocks + j] : b * p.max_blocks + j;
   const bool tokenwise = p.scheme[which] == KVQ_TOKENWISE;
   const size_t win_at = ((size_t)b * p.num_kv_heads + h) * kBlockTokens * D + slab * W;
   const float* win = p.window[which] ? p.window[which] + win_at : nullptr;
@@ -370,7 +374,6 @@ __device__ __forceinline__ void append_edge(const AppendParams& p) {
     }
   }
   if (s.n == 0) return;
-  const int page = p.page_table ? p.page_table[(size_t)b * p.max_blocks + j] : b * p.max_blocks + j;
   if (page < 0 || page >= p.num_pages) {
     if (lead && tid == 0) report(p.dev_status, KVQ_DEV_BAD_PAGE);
     return;
@@ -404,7 +407,25 @@ __device__ __forceinline__ void append_edge(const AppendParams& p) {
       else *at = (unsigned char)acc[0][c];
     }
   };
-  if (tokenwise) {
+  const bool past = warp * kWarpTok >= nv;  // none of this warp's tokens is there: codes 0
+  auto put_none = [&] {
+    if (which == 0) {
+      const uint32_t none[4] = {0u, 0u, 0u, 0u};
+#pragma unroll
+      for (int i = 0; i < kTok; ++i) put_k(tok + i, none);
+    } else {
+      uint32_t none[kWords][4];
+#pragma unroll
+      for (int i = 0; i < kWords * 4; ++i) none[i / 4][i % 4] = kWordMagic;
+      put_v(none);
+    }
+  };
+  if (tokenwise && (warp + 1) * kWarpTok <= from) {
+    // tokens that stay, all of this warp's: nothing of theirs is written
+  } else if (tokenwise && past) {
+    for (int e = warp * kWarpTok * gps + lane; e < (warp + 1) * kWarpTok * gps; e += 32) s_out[e] = z_out[e] = 0;
+    put_none();
+  } else if (tokenwise) {
     // ranges of the thread's tokens over its 4 channels, then over the group's lanes
     const int lg = G / 4, gl = lane & (lg - 1);  // lanes of a group, place in it
     float mn[kTok], mx[kTok];
@@ -469,7 +490,7 @@ __device__ __forceinline__ void append_edge(const AppendParams& p) {
           mn[c] = min_nan(mn[c], x[i][c]);
           mx[c] = max_nan(mx[c], x[i][c]);
         }
-    } else {
+    } else if (!past) {
 #pragma unroll
       for (int i = 0; i < kTok; ++i)
         if (tok + i < nv) {
@@ -491,49 +512,53 @@ __device__ __forceinline__ void append_edge(const AppendParams& p) {
     *reinterpret_cast<float4*>(&hi_s[warp][ch]) = make_float4(mx[0], mx[1], mx[2], mx[3]);
     const int gw = G / kWarpTok, groups = kBlockTokens / G;  // warps of a token group, token groups
     channel_groups<BITS, W, kWarps>(ranges, groups, gw, s_out, z_out, p.dev_status);
-    const int g = warp * kWarpTok / G;
-    const float4 s4 = *reinterpret_cast<const float4*>(&lo_s[g][ch]);
-    const float4 z4 = *reinterpret_cast<const float4*>(&hi_s[g][ch]);
-    float sc[4] = {s4.x, s4.y, s4.z, s4.w}, rc[4];
-    const float zc[4] = {z4.x, z4.y, z4.z, z4.w};
+    if (past) {
+      put_none();
+    } else {
+      const int g = warp * kWarpTok / G;
+      const float4 s4 = *reinterpret_cast<const float4*>(&lo_s[g][ch]);
+      const float4 z4 = *reinterpret_cast<const float4*>(&hi_s[g][ch]);
+      float sc[4] = {s4.x, s4.y, s4.z, s4.w}, rc[4];
+      const float zc[4] = {z4.x, z4.y, z4.z, z4.w};
 #pragma unroll
-    for (int c = 0; c < 4; ++c) {
-      if (isnan(sc[c])) {
-        sc[c] = 0.f;
+      for (int c = 0; c < 4; ++c) {
+        if (isnan(sc[c])) {
+          sc[c] = 0.f;
 #pragma unroll
-        for (int i = 0; i < kTok; ++i) x[i][c] = 0.f;
-      }
-      rc[c] = reciprocal(sc[c]);
-    }
-    uint64_t sn[2], zn[2], r2[2];
-#pragma unroll
-    for (int c = 0; c < 2; ++c) {
-      sn[c] = rows::pair(-sc[2 * c], -sc[2 * c + 1]);
-      zn[c] = rows::pair(-zc[2 * c], -zc[2 * c + 1]);
-      r2[c] = rows::pair(rc[2 * c], rc[2 * c + 1]);
-    }
-    if (nv < kBlockTokens) {  // tokens past the end have code 0
-#pragma unroll
-      for (int i = 0; i < kTok; ++i)
-        if (tok + i >= nv) {
-#pragma unroll
-          for (int c = 0; c < 4; ++c) x[i][c] = zc[c];
+          for (int i = 0; i < kTok; ++i) x[i][c] = 0.f;
         }
-    }
-    uint32_t acc[kWords][4] = {};
-#pragma unroll
-    for (int i = 0; i < kTok; ++i) {
-      uint32_t y[4];
-#pragma unroll
-      for (int c = 0; c < 4; c += 2) code_pair(x[i][c], x[i][c + 1], sn[c / 2], zn[c / 2], r2[c / 2], y[c], y[c + 1]);
-      if (which == 0) {
-        put_k(tok + i, y);
-      } else {
-#pragma unroll
-        for (int c = 0; c < 4; ++c) acc[i / kWordTok][c] += y[c] << (i % kWordTok * BITS);
+        rc[c] = reciprocal(sc[c]);
       }
+      uint64_t sn[2], zn[2], r2[2];
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        sn[c] = rows::pair(-sc[2 * c], -sc[2 * c + 1]);
+        zn[c] = rows::pair(-zc[2 * c], -zc[2 * c + 1]);
+        r2[c] = rows::pair(rc[2 * c], rc[2 * c + 1]);
+      }
+      if (nv < kBlockTokens) {  // tokens past the end have code 0
+#pragma unroll
+        for (int i = 0; i < kTok; ++i)
+          if (tok + i >= nv) {
+#pragma unroll
+            for (int c = 0; c < 4; ++c) x[i][c] = zc[c];
+          }
+      }
+      uint32_t acc[kWords][4] = {};
+#pragma unroll
+      for (int i = 0; i < kTok; ++i) {
+        uint32_t y[4];
+#pragma unroll
+        for (int c = 0; c < 4; c += 2) code_pair(x[i][c], x[i][c + 1], sn[c / 2], zn[c / 2], r2[c / 2], y[c], y[c + 1]);
+        if (which == 0) {
+          put_k(tok + i, y);
+        } else {
+#pragma unroll
+          for (int c = 0; c < 4; ++c) acc[i / kWordTok][c] += y[c] << (i % kWordTok * BITS);
+        }
+      }
+      if (which == 1) put_v(acc);
     }
-    if (which == 1) put_v(acc);
   }
   __syncthreads();
 
