@@ -28,7 +28,9 @@ __global__ void __launch_bounds__(kMergeThreads) merge_kernel(const Params P, in
   if (before > tile0) return;  // an earlier border cut this tile
   uint32_t bad = 0;
   const Seq s = load_seq(p, at.b, &bad);
-  const long long end = tile0 + tile_steps(s, at.t, tok_cta, p.causal);
+  const int work = work_steps(key_tiles(s, at.t, tok_cta, p.causal));
+  if (at.x >= work) return;  // the border lies behind the tile's work
+  const long long end = tile0 + work;
   const int slot0 = 2 * (cta - 1) + (before == tile0 ? 0 : 1);
   // The parts: CTA cta - 1's, then one of every CTA that begins before the end
   // and has steps (all have, where there are as many steps as CTAs).

@@ -1,7 +1,8 @@
 // Attention of chunks of new tokens over the packed cache, on tcgen05.
 //
 // Work: a row tile is up to NT x 128 (token, head) rows of one sequence and KV
-// head, and costs one step per key tile of 128 tokens (a cache block).  All
+// head, and takes one step per key tile of 128 tokens (a cache block); a few
+// more are counted for what it costs besides (tile_cost).  All
 // steps of all tiles, in a fixed order, are cut into as many equal ranges as
 // there are CTAs; a CTA walks its range tile by tile (a segment each).  A tile
 // that a range border cuts leaves partial results (normalised outputs and
@@ -18,10 +19,10 @@
 // zero, with a maximum and a sum of its own, so that its accumulator rows are
 // the attention over its share of the tokens.  The copies are joined like the
 // parts of a cut tile, at the end of the segment, in shared memory.  The extra
-// MMA rows are free.  (64 ragged paged sequences, 8 tokens at most: @REP@.)
+// MMA rows are free.
 //
 // A step: the block's packed codes, scales and offsets come in by bulk copies
-// (warp `copy`); a dequantising warpgroup turns them into fp16 operands in
+// (warp `copy`); a team of dequantising warps turns them into fp16 operands in
 // shared memory (x_hat = s code + z, one rounding); S = Q K^T and O += P V run
 // on the tensor cores with fp32 accumulators in tensor memory; a thread per
 // row does the softmax in between (attn_core.cuh).  K and V operands are both
@@ -61,16 +62,23 @@ __device__ __forceinline__ int key_tiles(const Seq& s, int t, int tok, int causa
   const int top = causal ? s.len - s.n + end : s.len;
   return top > 0 ? (top + kTile - 1) / kTile : 0;
 }
-// Steps of tile t: a tile that sees nothing still has its rows written.
-__device__ __forceinline__ int tile_steps(const Seq& s, int t, int tok, int causal) {
-  return max(1, key_tiles(s, t, tok, causal));
+// Steps of a tile that sees n key tiles: one at least, since a tile that sees
+// nothing still has its rows written, and tile_cost more for what a segment
+// costs beside its steps (Q, the epilogue, filling the pipeline), so that a CTA
+// with many short tiles is not the last.  (32 sequences at head dim 256: 156 us
+// without, 132 with 3, 137 with 6; head dim 128, 64 ragged sequences: 1063,
+// 1026 with 10; four drafted tokens: 55.6, 52 with 6 or 10, 56 with 16.)
+__device__ __forceinline__ int tile_cost(int head_dim) { return head_dim > 128 ? 3 : 8; }
+__device__ __forceinline__ int work_steps(int n) { return max(1, n); }
+__device__ __forceinline__ int tile_steps(const RowAttnParams& p, const Seq& s, int t, int tok) {
+  return work_steps(key_tiles(s, t, tok, p.causal)) + tile_cost(p.head_dim);
 }
-__device__ __forceinline__ long long seq_steps(const Seq& s, int tok, int causal) {
+__device__ __forceinline__ long long seq_steps(const RowAttnParams& p, const Seq& s, int tok) {
   const int nt = (s.n + tok - 1) / tok;
   if (nt == 0) return 0;
-  if (!causal) return (long long)nt * tile_steps(s, 0, tok, 0);
+  if (!p.causal) return (long long)nt * tile_steps(p, s, 0, tok);
   long long n = 0;
-  for (int t = 0; t < nt; ++t) n += tile_steps(s, t, tok, 1);
+  for (int t = 0; t < nt; ++t) n += tile_steps(p, s, t, tok);
   return n;
 }
 
@@ -91,7 +99,7 @@ __device__ __forceinline__ void find_place(const RowAttnParams& p, int tok, int 
   const int per = (p.batch + NT - 1) / NT, b0 = min(p.batch, tid * per), b1 = min(p.batch, b0 + per);
   uint32_t bad = 0;
   long long mine = 0;
-  for (int b = b0; b < b1; ++b) mine += seq_steps(load_seq(p, b, &bad), tok, p.causal);
+  for (int b = b0; b < b1; ++b) mine += seq_steps(p, load_seq(p, b, &bad), tok);
   if (report_bad && bad) report(p.dev_status, bad);
   long long incl = mine;
 #pragma unroll
@@ -120,14 +128,14 @@ __device__ __forceinline__ void find_place(const RowAttnParams& p, int tok, int 
     if (at >= 0 && at < mine) {
       for (int b = b0; b < b1; ++b) {
         const Seq s = load_seq(p, b, &bad);
-        const long long n = seq_steps(s, tok, p.causal);
+        const long long n = seq_steps(p, s, tok);
         if (at >= n) {
           at -= n;
           continue;
         }
         int t = 0;
         for (;; ++t) {
-          const int w = tile_steps(s, t, tok, p.causal);
+          const int w = tile_steps(p, s, t, tok);
           if (at < w) break;
           at -= w;
         }
@@ -205,7 +213,7 @@ __host__ __device__ constexpr int element_at(int i) {
 // The block's scales and offsets into the table that the dequantising threads
 // read: checked (a group whose values would not fit fp16 has its scale
 // lowered to fit, one that is not finite is zeroed) and, where they belong to
-// columns, in operand order: col_major: [group][column] u16 scales, then
+// columns, in operand order: by_column: [group][column] u16 scales, then
 // offsets; else [entry] (scale | offset << 16).
 template <int BITS>
 __device__ __forceinline__ void prepare_table(int t, const uint16_t* s, const uint16_t* z, int nsz, bool by_column,
@@ -856,24 +864,29 @@ __global__ void __launch_bounds__(threads_of(D, NT), 1) chunk_kernel(const Param
         Seq s = load_seq(p, at.b, &bad);
         long long left = s1 - s0;
         bool first = true, ok = true;
-        for (int k = 0; ok; ++k) {
-          if (k >= 4) ok = wait(&aux->seg_empty[k & 3], ((k >> 2) - 1) & 1);
-          if (!ok) break;
+        for (int k = 0; ok;) {
           Segment g;
           g.tiles = -1;
+          bool some = true;  // else: none of the tile's work, only steps that stand for its cost
           if (left > 0) {
-            const int w = key_tiles(s, at.t, tok_cta, p.causal), steps = max(1, w);
-            const int take = (int)min(left, (long long)(steps - at.x));
+            const int w = key_tiles(s, at.t, tok_cta, p.causal), work = work_steps(w);
+            const int take = (int)min(left, (long long)(work + tile_cost(D) - at.x));
+            some = at.x < work;
             g.kvh = at.h; g.first = s.first; g.n = s.n; g.len = s.len; g.tile = at.t; g.b = at.b;
             g.top = w - 1 - at.x;
-            g.tiles = min(take, w);  // 0: nothing to see
-            g.slot = at.x == 0 && take == steps ? -1 : 2 * (int)blockIdx.x + (first ? 0 : 1);
+            g.tiles = min(take, w - at.x);  // 0: nothing to see
+            g.slot = at.x == 0 && take >= work ? -1 : 2 * (int)blockIdx.x + (first ? 0 : 1);
             left -= take;
             first = false;
           }
-          aux->seg[k & 3] = g;
-          mbar_arrive(&aux->seg_full[k & 3]);
-          if (g.tiles < 0) break;
+          if (some) {
+            if (k >= 4) ok = wait(&aux->seg_empty[k & 3], ((k >> 2) - 1) & 1);
+            if (!ok) break;
+            aux->seg[k & 3] = g;
+            mbar_arrive(&aux->seg_full[k & 3]);
+            if (g.tiles < 0) break;
+            ++k;
+          }
           if (left > 0) {  // the next tile with rows
             at.x = 0;
             ++at.t;
