@@ -169,16 +169,16 @@ __device__ void find_tile(const RowAttnParams& p, int rank, int per_tile, bool l
 // sequence's rows, or none) become zeros, and values that are not finite are
 // zeroed and noted in `bad`, so that a zero probability keeps them out of the
 // rows before them; the epilogue adds them to the rows from there on.  token0:
-// the tile's first token as `bad` counts them.  One warp.
-template <bool FP16>
-__device__ void mend_values(unsigned char* slot, int chunks, int channel0, int token0, int valid, uint32_t* bad,
-                            int* any_bad) {
-  const int lane = threadIdx.x & 31;
+// the tile's first token as `bad` counts them.  By THREADS threads, in their
+// own time: this one is number `me`.
+template <bool FP16, int THREADS>
+__device__ __forceinline__ void mend_values(int me, unsigned char* slot, int chunks, int channel0, int token0, int valid,
+                                            uint32_t* bad, int* any_bad) {
   const uint32_t inf = FP16 ? 0x7c00u : 0x7f80u;
   uint32_t acc = 0;
   const int n = chunks * kTile * 8;
 #pragma unroll 4
-  for (int i = lane; i < n; i += 32) {  // 16 bytes each; rows of 8
+  for (int i = me; i < n; i += THREADS) {  // 16 bytes each; rows of 8
     const int t = (i >> 3) & (kTile - 1);
     uint4* at = reinterpret_cast<uint4*>(slot) + i;
     if (t >= valid) {
@@ -194,9 +194,9 @@ __device__ void mend_values(unsigned char* slot, int chunks, int channel0, int t
     }
   }
   if (!__any_sync(0xffffffffu, acc != 0)) return;
-  if (lane == 0) *any_bad = 1;
+  if ((me & 31) == 0) *any_bad = 1;
 #pragma unroll 1
-  for (int i = lane; i < n; i += 32) {
+  for (int i = me; i < n; i += THREADS) {
     const int t = (i >> 3) & (kTile - 1), chunk = (i >> 3) / kTile, c16 = (i & 7) ^ (t & 7);
     if (t >= valid) continue;
     uint16_t* at = reinterpret_cast<uint16_t*>(slot) + i * 8;
@@ -249,7 +249,7 @@ prompt_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__
       mbar_init(&aux->sums, 1);
       mbar_init(&aux->done, 1);
       for (int i = 0; i < 2; ++i) {
-        mbar_init(&aux->fixed[i], 1);
+        mbar_init(&aux->fixed[i], 8);
         mbar_init(&aux->s[i], 1);
         mbar_init(&aux->p[i], 5);  // the row tile's warps and the one that waits for copies
       }
@@ -286,6 +286,28 @@ prompt_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__
       for (int i = 0; i < tries && !mbar_try_wait_sleep(bar, parity, 20000u); ++i) {}
     };
 
+    // V of the walk's tile j (one of the first two), a share of this thread.
+    // Warps 0-7 do it, the softmax's between the probabilities and their
+    // arrival: a single warp beside them took longer than that (packed prompts
+    // 203 -> 188 us, head dim 256 203 -> 177 us).
+    auto mend_tile = [&](int j) -> bool {
+      bool ok = true;
+      // the tile's first slot, counted from the walk's start.  One row tile: this
+      // slot's round before held K of tile j or less, whose scores are there.
+      const int at = NT == 2 ? 1 + 2 * j : Sh::kParts * (min(Sh::kAhead, tiles) + j + (j > 0 && tiles > Sh::kAhead));
+      for (int part = 0; part < Sh::kParts && ok; ++part) {
+        const int sl = NT == 2 ? at : (at + part) % Sh::kSlots;
+        ok = __all_sync(0xffffffffu, NT == 2 ? wait(&aux->full[j], 0) : wait(&aux->full[sl], (at + part) / Sh::kSlots & 1));
+        if (ok)
+          mend_values<FP16, 256>(tid, ring + sl * Sh::kSlotBytes, Sh::kSlotCh, part * Sh::kSlotCh * 64,
+                                      (last - j - clean) * kTile, min(kTile, n - (last - j) * kTile), bad, &aux->any_bad);
+      }
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&aux->fixed[j]);
+      return ok;
+    };
+
     // Registers: 384 threads x 168 at launch; the softmax warpgroups take 208
     // each (a row's 128 scores stay in registers), the third keeps 88.
     if (warp >= (NT == 2 ? 8 : 4)) {
@@ -318,19 +340,6 @@ prompt_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__
                         &aux->q);
       }
       const bool stall = (p.flags & KVQ_FLAG_TEST_STALL) && blockIdx.x == 0;  // test hook: V of the first CTA is withheld
-      auto mend_tile = [&](int j, int sl, int rd, uint64_t* loaded, uint32_t parity) {
-        // V of the walk's tile j, in the slots from sl on
-        for (int part = 0; part < Sh::kParts && ok; ++part) {
-          ok = __all_sync(0xffffffffu, wait(NT == 2 ? loaded : &aux->full[sl], NT == 2 ? parity : rd & 1));
-          if (ok)
-            mend_values<FP16>(ring + sl * Sh::kSlotBytes, Sh::kSlotCh, part * Sh::kSlotCh * 64, (last - j - clean) * kTile,
-                              min(kTile, n - (last - j) * kTile), bad, &aux->any_bad);
-          if (++sl == Sh::kSlots) { sl = 0; ++rd; }
-        }
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&aux->fixed[j]);
-      };
       if (NT == 2) {
         auto copy = [&](const CUtensorMap& map, int j, int sl, uint64_t* bar) {
 #pragma unroll
@@ -341,10 +350,6 @@ prompt_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__
           mbar_arrive_expect_tx(&aux->first, Sh::kSlotBytes);
           copy(map_k, last, 0, &aux->first);
         }
-        auto mend_pair = [&](int j) {
-          const int m = j % Sh::kPairs;
-          mend_tile(j, 1 + 2 * m, 0, &aux->full[m], j / Sh::kPairs & 1);
-        };
         for (int j = 0; j < tiles && ok && !stall; ++j) {
           const int m = j % Sh::kPairs;
           if (j >= Sh::kPairs) ok = __all_sync(0xffffffffu, wait(&aux->empty[m], (j / Sh::kPairs - 1) & 1));
@@ -356,19 +361,14 @@ prompt_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__
             if (more) copy(map_k, last - j - 1, 2 + 2 * m, &aux->full[m]);
           }
           ++issued;
-          // the tile before, with this one's copies on their way
-          if (j > 0 && j - 1 < mend) mend_pair(j - 1);
         }
-        if (ok && !stall && tiles - 1 < mend) mend_pair(tiles - 1);
       } else {
         for (int i = 0; i < Sh::kAhead && i < tiles; ++i)
           for (int part = 0; part < Sh::kParts; ++part) load(map_k, last - i, part);
         for (int i = 0; i < tiles && ok && !stall; ++i) {
-          const int vslot = slot, vround = round;
           for (int part = 0; part < Sh::kParts; ++part) load(map_v, last - i, part);
           if (i + Sh::kAhead < tiles)
             for (int part = 0; part < Sh::kParts; ++part) load(map_k, last - i - Sh::kAhead, part);
-          if (i < mend && ok) mend_tile(i, vslot, vround, nullptr, 0);
         }
       }
       // copies in flight land before this CTA's shared memory is given up
@@ -473,6 +473,8 @@ prompt_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__
         drain(&aux->done, 0);  // nothing in flight when tensor memory is freed
       }
       __syncwarp();
+    } else if (warp < 8) {  // (head dim 256: warps 4-7)
+      for (int j = 0; j < mend && __all_sync(0xffffffffu, wait(&aux->s[j], 0)) && mend_tile(j); ++j) {}
     } else if (warp == 10 && lane == 0) {
       // ------------------------------------------------------------ copies' arrival, for the products
       bool ok = true;
@@ -514,7 +516,9 @@ prompt_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__
       const int r = tid & 127;  // row of the tile = lane of tensor memory
       const uint32_t lanes = (uint32_t)(warp & 3) << 21;
       const int rows = min(tok_tile, ntok - i * tok_tile) * p.gq;
-      if (i < act) {
+      if (i >= act) {
+        for (int j = 0; j < mend && mend_tile(j); ++j) {}
+      } else {
         const bool mine = r < rows, any = (warp & 3) * 32 < rows;
         const int tok = tok0 + i * tok_tile + r / p.gq;
         const uint32_t t_o = tmem + lanes + 256 + i * D;
@@ -539,6 +543,7 @@ prompt_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__
                                     }
                                   });
           }
+          if (__builtin_expect(j < mend, 0)) ok = mend_tile(j);
           tc_fence_before();
           __syncwarp();
           if (lane == 0) mbar_arrive(&aux->p[buf]);
