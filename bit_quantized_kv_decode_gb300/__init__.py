@@ -359,14 +359,14 @@ def _cache_ptrs(desc: CacheDesc, name: str, cache, device: int):
 def _outputs(q: torch.Tensor, T: int, Hq: int, D: int, out, lse, return_lse: bool, device: int):
     """(out, lse, their addresses); what is not given is made."""
     if out is None:
-        out = torch.empty((T, Hq, D), dtype=q.dtype, device=q.device)
+        out = q.new_empty(T, Hq, D)
         po = out.data_ptr()
     else:
         po = _ptr(out, "out", (q.dtype,), T * Hq * D, device)
     if lse is None:
         if not return_lse:
             return out, None, po, None
-        lse = torch.empty((T, Hq), dtype=torch.float32, device=q.device)
+        lse = q.new_empty(T, Hq, dtype=torch.float32)
         return out, lse, po, lse.data_ptr()
     return out, lse, po, _ptr(lse, "lse", (torch.float32,), T * Hq, device)
 

@@ -560,22 +560,17 @@ __global__ void __launch_bounds__(threads_of(D, NT), 1) chunk_kernel(const Param
         float lse2 = seen_any ? st.m * c + log2f(st.l) - rows::shift_log2<true>() : -INFINITY;
         const long long row = (long long)(g.first + tok) * p.num_q_heads + head;
         const size_t prow = (size_t)max(g.slot, 0) * (NT * kTile) + i * kTile + row_i;
-        auto put = [&](int col, const float (&x)[32]) {  // 32 channels of this thread's row
+        auto put = [&](int col, const float* x) {  // 8 channels of this thread's row
           if (g.slot >= 0) {
             float4* dst = reinterpret_cast<float4*>(P.part_o + prow * D + col);
 #pragma unroll
-            for (int e = 0; e < 8; ++e) dst[e] = make_float4(x[4 * e], x[4 * e + 1], x[4 * e + 2], x[4 * e + 3]);
+            for (int e = 0; e < 2; ++e) dst[e] = make_float4(x[4 * e], x[4 * e + 1], x[4 * e + 2], x[4 * e + 3]);
           } else {
-            uint4* dst = reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.out) + row * D + col);
+            uint32_t w[4];
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              uint32_t w[4];
-#pragma unroll
-              for (int j = 0; j < 4; ++j)
-                w[j] = p.fp16 ? rows::round2<true>(x[8 * e + 2 * j], x[8 * e + 2 * j + 1])
-                              : rows::round2<false>(x[8 * e + 2 * j], x[8 * e + 2 * j + 1]);
-              dst[e] = make_uint4(w[0], w[1], w[2], w[3]);
-            }
+            for (int j = 0; j < 4; ++j)
+              w[j] = p.fp16 ? rows::round2<true>(x[2 * j], x[2 * j + 1]) : rows::round2<false>(x[2 * j], x[2 * j + 1]);
+            *reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.out) + row * D + col) = make_uint4(w[0], w[1], w[2], w[3]);
           }
         };
         auto sums = [&](int col, float (&x)[32]) {
@@ -591,48 +586,53 @@ __global__ void __launch_bounds__(threads_of(D, NT), 1) chunk_kernel(const Param
             for (int col = 0; col < D; col += 32) {
               float x[32];
               sums(col, x);
-              if (mine) put(col, x);
+              if (mine) {
+#pragma unroll
+                for (int e = 0; e < 32; e += 8) put(col + e, x + e);
+              }
             }
           }
         } else {
-          // Joined over the copies: the first one's warps add the others' rows,
-          // half of the channels at a time, through Q's place in shared memory.
+          // Joined over the copies through Q's place in shared memory, half of
+          // the channels at a time; every copy's warps add up a share of them.
           auto join = [&] {
             __syncwarp();
             if (lane == 0) mbar_arrive(&aux->join);
             ok = __all_sync(0xffffffffu, wait(&aux->join, joins++ & 1)) && ok;
           };
-          float* xs = reinterpret_cast<float*>(q_s);  // [copy - 1][channel][row]
-          float* ls = xs + (copies - 1) * share * (D / 2);  // [copy][row] log-sum-exps
-          ls[r] = lse2;
+          float* xs = reinterpret_cast<float*>(q_s);  // [copy, row] log-sum-exps, then [channel][copy, row]
+          xs[r] = lse2;
           join();
           float m = -INFINITY, w = 0.f;
-          for (int e = 0; e < copies; ++e) m = fmaxf(m, ls[e * share + row_i]);
-          for (int e = 0; e < copies; ++e) w += m == -INFINITY ? 0.f : exp2f(ls[e * share + row_i] - m);
+          for (int e = 0; e < copies; ++e) m = fmaxf(m, xs[e * share + row_i]);
+          for (int e = 0; e < copies; ++e) w += m == -INFINITY ? 0.f : exp2f(xs[e * share + row_i] - m);
           f = seen_any ? f * exp2f(lse2 - m) / w : 0.f;
           lse2 = w > 0.f || isnan(w) ? m + log2f(w) : -INFINITY;
+          join();
+          constexpr int kHalf = D / 2;
+          const int each = kHalf / copies;
 #pragma unroll 1
           for (int half = 0; half < 2; ++half) {
-            if (copy > 0) {
 #pragma unroll 1
-              for (int col = 0; col < D / 2; col += 32) {
-                float x[32];
-                sums(half * (D / 2) + col, x);
+            for (int col = 0; col < kHalf; col += 32) {
+              float x[32];
+              sums(half * kHalf + col, x);
 #pragma unroll
-                for (int e = 0; e < 32; ++e) xs[((copy - 1) * (D / 2) + col + e) * share + row_i] = x[e];
-              }
+              for (int e = 0; e < 32; ++e) xs[(col + e) * kTile + r] = x[e];
             }
             join();
-            if (copy == 0) {
 #pragma unroll 1
-              for (int col = 0; col < D / 2; col += 32) {
-                float x[32];
-                sums(half * (D / 2) + col, x);
-                for (int e = 1; e < copies; ++e)
+            for (int col = copy * each; col < (copy + 1) * each; col += 8) {
+              const float* at = xs + col * kTile + row_i;
+              float x[8];
 #pragma unroll
-                  for (int ch = 0; ch < 32; ++ch) x[ch] += xs[((e - 1) * (D / 2) + col + ch) * share + row_i];
-                if (mine) put(half * (D / 2) + col, x);
+              for (int e = 0; e < 8; ++e) x[e] = at[e * kTile];
+              for (int c = 1; c < copies; ++c) {
+                at += share;
+#pragma unroll
+                for (int e = 0; e < 8; ++e) x[e] += at[e * kTile];
               }
+              if (mine) put(half * kHalf + col, x);
             }
             join();
           }
