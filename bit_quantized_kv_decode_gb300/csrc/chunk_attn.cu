@@ -7,21 +7,24 @@ namespace {
 
 constexpr int kGrid = 152;  // one CTA per SM; they do not wait on one another, so fewer SMs only take longer
 constexpr int kSmem = 227 * 1024;
-constexpr int kMergeThreads = 256, kMergeRows = 32;
+constexpr int kMergeThreads = 256, kMergeRows = 32, kMergeLanes = kMergeThreads / kMergeRows;  // lanes of a row
 
 // Joins the parts of the tile that the border between CTAs blockIdx.x and
 // blockIdx.x + 1 is the first to cut, rows blockIdx.y * 32 on:
-// lse = log2 sum 2^lse_i, out = sum 2^(lse_i - lse) o_i.  A warp per row.
+// lse = log2 sum 2^lse_i, out = sum 2^(lse_i - lse) o_i.  Eight lanes to a row,
+// so that a CTA's rows are all read at once: what it takes is latency.
 template <int D>
 __global__ void __launch_bounds__(kMergeThreads) merge_kernel(const Params P, int nt, int grid) {
-  asm volatile("griddepcontrol.wait;" ::: "memory");
   __shared__ long long scan[kMergeThreads / 32], range[3];
   __shared__ Place at;
   __shared__ int list[kGrid], parts;
   const RowAttnParams& p = P.r;
-  const int cta = blockIdx.x + 1, tid = threadIdx.x, lane = tid & 31;
+  const int cta = blockIdx.x + 1, tid = threadIdx.x;
   const int tok_tile = kTile / p.gq, tok_cta = tok_tile * nt;
   find_place<kMergeThreads>(p, tok_cta, cta, grid, scan, &at, range, false);
+  // every CTA waits, those that have nothing to join too: what follows in the
+  // stream waits for this grid, which must not be done before that one is
+  asm volatile("griddepcontrol.wait;" ::: "memory");
   const long long total = range[2];
   if (range[0] >= total || at.x == 0) return;  // past the last step (`at` is unset), or between two tiles
   const long long tile0 = at.tile0, before = total * (cta - 1) / grid;
@@ -42,43 +45,48 @@ __global__ void __launch_bounds__(kMergeThreads) merge_kernel(const Params P, in
   }
   __syncthreads();
   const size_t pitch = (size_t)nt * kTile;
-  for (int i = tid >> 5; i < kMergeRows; i += kMergeThreads / 32) {
-    const int prow = blockIdx.y * kMergeRows + i, r = prow & (kTile - 1);
-    const int tile_tok = at.t * tok_cta + (prow / kTile) * tok_tile, tok = tile_tok + r / p.gq;
-    if (r >= tok_tile * p.gq || tok >= s.n) continue;
-    auto part = [&](int k) { return (size_t)(k == 0 ? slot0 : list[k - 1]) * pitch + prow; };
-    float m = -INFINITY;
-    for (int k = lane; k <= parts; k += 32) m = fmaxf(m, P.part_lse[part(k)]);
+  const int prow = blockIdx.y * kMergeRows + tid / kMergeLanes, r = prow & (kTile - 1), sub = tid % kMergeLanes;
+  const int tile_tok = at.t * tok_cta + (prow / kTile) * tok_tile, tok = tile_tok + r / p.gq;
+  const bool mine = r < tok_tile * p.gq && tok < s.n;
+  auto part = [&](int k) { return (size_t)(k == 0 ? slot0 : list[k - 1]) * pitch + prow; };
+  float m = -INFINITY;
+  if (mine)
+    for (int k = sub; k <= parts; k += kMergeLanes) m = fmaxf(m, P.part_lse[part(k)]);
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-    constexpr int kPer = D / 32;  // channels of a lane
-    float acc[kPer], sum = 0.f;
+  for (int o = kMergeLanes / 2; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+  if (!mine) return;
+  constexpr int kPer = D / 4 / kMergeLanes;  // of four channels, kMergeLanes apart
+  float4 acc[kPer];
+  float sum = 0.f;
 #pragma unroll
-    for (int c = 0; c < kPer; ++c) acc[c] = 0.f;
+  for (int c = 0; c < kPer; ++c) acc[c] = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 2
-    for (int k = 0; k <= parts; ++k) {
-      const size_t at_part = part(k);
-      const float l = P.part_lse[at_part];
-      const float w = m == -INFINITY ? 0.f : exp2f(l - m);  // 0: nothing seen in this part
-      sum += w;
-      const float2* o = reinterpret_cast<const float2*>(P.part_o + at_part * D + lane * kPer);
+  for (int k = 0; k <= parts; ++k) {
+    const size_t at_part = part(k);
+    const float l = P.part_lse[at_part];
+    const float w = m == -INFINITY ? 0.f : exp2f(l - m);  // 0: nothing seen in this part
+    sum += w;
+    const float4* o = reinterpret_cast<const float4*>(P.part_o + at_part * D) + sub;
 #pragma unroll
-      for (int e = 0; e < kPer / 2; ++e) {
-        const float2 v = o[e];
-        acc[2 * e] = fmaf(w, v.x, acc[2 * e]);
-        acc[2 * e + 1] = fmaf(w, v.y, acc[2 * e + 1]);
-      }
+    for (int e = 0; e < kPer; ++e) {
+      const float4 v = o[e * kMergeLanes];
+      acc[e].x = fmaf(w, v.x, acc[e].x);
+      acc[e].y = fmaf(w, v.y, acc[e].y);
+      acc[e].z = fmaf(w, v.z, acc[e].z);
+      acc[e].w = fmaf(w, v.w, acc[e].w);
     }
-    const float inv = sum > 0.f || isnan(sum) ? 1.f / sum : 0.f;
-    const long long row = (long long)(s.first + tok) * p.num_q_heads + at.h * p.gq + r % p.gq;
-    uint32_t* dst = reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(p.out) + row * D + lane * kPer);
-#pragma unroll
-    for (int e = 0; e < kPer / 2; ++e)
-      dst[e] = p.fp16 ? rows::round2<true>(acc[2 * e] * inv, acc[2 * e + 1] * inv)
-                      : rows::round2<false>(acc[2 * e] * inv, acc[2 * e + 1] * inv);
-    if (lane == 0 && p.lse != nullptr)
-      p.lse[row] = sum > 0.f || isnan(sum) ? (m + log2f(sum)) * 0.6931471805599453f : -INFINITY;
   }
+  const float inv = sum > 0.f || isnan(sum) ? 1.f / sum : 0.f;
+  const long long row = (long long)(s.first + tok) * p.num_q_heads + at.h * p.gq + r % p.gq;
+  uint2* dst = reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.out) + row * D) + sub;
+#pragma unroll
+  for (int e = 0; e < kPer; ++e) {
+    const float4 v = make_float4(acc[e].x * inv, acc[e].y * inv, acc[e].z * inv, acc[e].w * inv);
+    dst[e * kMergeLanes] = p.fp16 ? make_uint2(rows::round2<true>(v.x, v.y), rows::round2<true>(v.z, v.w))
+                                  : make_uint2(rows::round2<false>(v.x, v.y), rows::round2<false>(v.z, v.w));
+  }
+  if (sub == 0 && p.lse != nullptr)
+    p.lse[row] = sum > 0.f || isnan(sum) ? (m + log2f(sum)) * 0.6931471805599453f : -INFINITY;
 }
 
 }  // namespace
