@@ -356,19 +356,30 @@ def _cache_ptrs(desc: CacheDesc, name: str, cache, device: int):
             _ptr(scale, name + " scale", _SCALES, n, device), _ptr(zero, name + " zero", _SCALES, n, device))
 
 
-def _outputs(q: torch.Tensor, T: int, Hq: int, D: int, out, lse, return_lse: bool, device: int):
+def _apart(t: torch.Tensor, name: str, rows, tokens: int, heads, dim: int) -> None:
+    """Refuses an output over the memory of rows that other CTAs may still read."""
+    at, end = t.data_ptr(), t.data_ptr() + t.numel() * t.element_size()
+    for r, h in zip(rows, heads):
+        if tokens and r.data and r.data < end and at < r.data + ((tokens - 1) * r.stride_token + (h - 1) * r.stride_head + dim) * 2:
+            raise ValueError(f"{name} overlaps the rows that are read")
+
+
+def _outputs(q: torch.Tensor, T: int, Hq: int, D: int, out, lse, return_lse: bool, device: int, rows, heads):
     """(out, lse, their addresses); what is not given is made."""
     if out is None:
         out = q.new_empty(T, Hq, D)
         po = out.data_ptr()
     else:
         po = _ptr(out, "out", (q.dtype,), T * Hq * D, device)
+        _apart(out, "out", rows, T, heads, D)
     if lse is None:
         if not return_lse:
             return out, None, po, None
         lse = q.new_empty(T, Hq, dtype=torch.float32)
         return out, lse, po, lse.data_ptr()
-    return out, lse, po, _ptr(lse, "lse", (torch.float32,), T * Hq, device)
+    pl = _ptr(lse, "lse", (torch.float32,), T * Hq, device)
+    _apart(lse, "lse", rows, T, heads, D)
+    return out, lse, po, pl
 
 
 def _launch(device: int, what: str, fn, *args):
@@ -400,7 +411,7 @@ def prompt_attn(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu_seqlens: t
     if k.get_device() != dev or v.get_device() != dev:
         raise ValueError(f"q, k and v are on {q.device}, {k.device} and {v.device}")
     B, pcu = _starts(cu_seqlens, dev)
-    out, lse, po, pl = _outputs(q, T, Hq, D, out, lse, return_lse, dev)
+    out, lse, po, pl = _outputs(q, T, Hq, D, out, lse, return_lse, dev, (qr, kr, vr), (Hq, Hkv, Hkv))
     d = PromptDesc(_DTYPES[q.dtype], D, Hq, Hkv, B, T, 1 if causal else 0, sm_scale, flags)
     _launch(dev, "kvq_prompt_attn", library().kvq_prompt_attn, ctypes.byref(d), ctypes.byref(qr), ctypes.byref(kr),
             ctypes.byref(vr), pcu, po, pl, _ptr(dev_status, "dev_status", _STATUS, 1, dev))
@@ -442,6 +453,8 @@ def append_chunk(desc: CacheDesc, k_new: torch.Tensor, v_new: torch.Tensor, cu_s
         pw = _ptr(w, name, (torch.float32,), size, dev)
         windows += [pw, pw if o is None else _ptr(o, name + "_out", (torch.float32,), size, dev)]
     kw, kwo, vw, vwo = windows
+    if kwo is not None and kwo in (vw, vwo) or vwo is not None and vwo == kw:
+        raise ValueError("k_window and v_window are the same memory")
     _launch(dev, "kvq_append_chunk", library().kvq_append_chunk, ctypes.byref(desc), _DTYPES[k_new.dtype],
             ctypes.byref(kr), ctypes.byref(vr), B, T, pcu, _ptr(seq_lens, "seq_lens", (torch.int32,), B, dev), pt, mb,
             kw, vw, kwo, vwo, *_cache_ptrs(desc, "k_cache", k_cache, dev), *_cache_ptrs(desc, "v_cache", v_cache, dev),
@@ -476,7 +489,7 @@ def chunk_attn(desc: CacheDesc, q: torch.Tensor, k_cache, v_cache, cu_seqlens: t
     if seq_lens is None:
         raise ValueError("seq_lens must be int32 [batch]")
     pk, pv = _cache_ptrs(desc, "k_cache", k_cache, dev), _cache_ptrs(desc, "v_cache", v_cache, dev)
-    out, lse, po, pl = _outputs(q, T, Hq, D, out, lse, return_lse, dev)
+    out, lse, po, pl = _outputs(q, T, Hq, D, out, lse, return_lse, dev, (qr,), (Hq,))
     d = ChunkDesc(desc, _DTYPES[q.dtype], B, T, Hq, mb, 1 if causal else 0, sm_scale, flags)
     if workspace is None:
         n = ctypes.c_size_t()

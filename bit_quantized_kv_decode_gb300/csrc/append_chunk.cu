@@ -1,14 +1,14 @@
 // Quantise and append a chunk of new tokens to the packed K and V caches.
 //
-// One CTA per (block touched, KV head, 128-channel slab, K or V); sequence b
-// touches blocks seq_lens[b] / 128 to (seq_lens[b] + n - 1) / 128.  The tile
-// (128 tokens x 64 or 128 channels) is read once into registers: a thread has 4
-// neighbouring channels of 16 (or, 64 channels wide, 8) consecutive tokens, so
-// rows are read as 8-byte (fp32: 16-byte) pieces of full lines, a channel-wise
-// group is reduced in registers and across warps, a token-wise one across the
-// lanes that share the token, and V's codes, packed along tokens, come out of
-// one thread's registers as whole words.  The packed block is put together in
-// shared memory and written in 16-byte pieces.
+// One CTA per (block touched, KV head, 64- or 128-channel slab, K or V);
+// sequence b touches blocks seq_lens[b] / 128 to (seq_lens[b] + n - 1) / 128.
+// The tile (128 tokens x 64 or 128 channels) is read once into registers: a
+// thread has 4 neighbouring channels of 4 to 16 consecutive tokens, so rows are
+// read as 8-byte (fp32: 16-byte) pieces of full lines, a channel-wise group is
+// reduced in registers and across warps, a token-wise one across the lanes that
+// share the token, and V's codes, packed along tokens, come out of one thread's
+// registers as whole words.  The packed block is put together in shared memory
+// and written in 16-byte pieces.
 //
 // Two kernels.  append_blocks_kernel takes the blocks that consist of new
 // 16-bit tokens alone: the tile stays in its 16-bit form (half the registers,
@@ -17,19 +17,25 @@
 // chunk, with the window's rows and the tokens that stay, and every block of
 // fp32 rows.  They write disjoint places and run side by side.
 //
-// The work is one pass over the rows: it is bound by memory where the
-// arithmetic per value stays below about ten instructions.  The code of a value
-// is clamp(rint(fl(fl(x - z) / s))) in IEEE fp32.  With d = fl(x - z) and
-// r = fl(1 / s) once per group, the quotient is corrected once after
-// Markstein ("Computation of elementary functions on the IBM RISC System/6000
-// processor", 1990): q = fl(d r), q' = fma(fma(-q, s, d), r, q) is fl(d / s),
-// since s, an fp16 number, has no all-ones fp32 significand (checked for every
-// s and the 13 fp32 numbers nearest to each half of a code); adding 1.5 x 2^23
-// then rounds it to the nearest even integer.  No clamp is needed: q' >= 0,
-// because z was rounded down, and at most 2^b - 1 up to rounding, because s
-// was rounded up.  (Deciding by d r alone and dividing where it lies near a
-// half was slower: coarse 16-bit values meet exact halves 0.07% of the time,
-// in three warps of four.)
+// The work is one pass over the rows, and memory would bound it below about ten
+// instructions a value; it takes 16 with everything, so whole blocks are bound
+// by instructions and barriers (65,536 tokens x 8 heads of 128, bf16 to 4 bits,
+// K channel-wise, V token-wise: 87 us, 3.9 TB/s, 59% of the issue slots), edges
+// by the latency of one block (128 sequences of a token, windows re-quantised:
+// 49 us, 2.8 TB/s).  Slower when tried: 16 warps to a whole block (140 -> 164
+// us); K and V of a block in one CTA, V's loads under K's stores, gained 2%.
+//
+// The code of a value is clamp(rint(fl(fl(x - z) / s))) in IEEE fp32.  With
+// d = fl(x - z) and r = fl(1 / s) once per group, the quotient is corrected once
+// after Markstein ("Computation of elementary functions on the IBM RISC
+// System/6000 processor", 1990): q = fl(d r), q' = fma(fma(-q, s, d), r, q) is
+// fl(d / s), since s, an fp16 number, has no all-ones fp32 significand (checked
+// for every s and the 13 fp32 numbers nearest to each half of a code); adding
+// 1.5 x 2^23 then rounds it to the nearest even integer.  No clamp is needed:
+// q' >= 0, because z was rounded down, and at most 2^b - 1 up to rounding,
+// because s was rounded up.  (Deciding by d r alone and dividing where it lies
+// near a half was slower: coarse 16-bit values meet exact halves 0.07% of the
+// time, in three warps of four.)
 #include <cuda_fp16.h>
 
 #include "attn_core.cuh"
@@ -39,7 +45,7 @@ namespace {
 
 // Warps of a block.  Edges: twice as many, each with half the tokens (8 of a
 // thread): their loads and stores depend on one another, so what counts is how
-// many warps wait at a time.
+// many warps wait at a time (128 sequences of a token: 67 -> 54 us).
 constexpr int kBlockWarps = 8, kEdgeWarps = 16;
 
 __device__ __forceinline__ float min_nan(float a, float b) {

@@ -30,6 +30,23 @@
 // neighbouring codes are split off two at a time (the halves of a 32-bit word),
 // which leaves the contraction index in a permuted order within 8 (4-bit) or
 // 16 (2-bit) elements; Q's channels and P's tokens are put in the same order.
+//
+// Roundings: x_hat, q (bf16 rows, 8 bits: none) and the probabilities are fp16,
+// 2^-11 each; e4m3 codes with the scales folded into the other operand, as
+// decode has them for its 4 to 16 rows, would need three-part splits of 128 rows.
+//
+// What bounds it: the chain of a step, scores - softmax - probabilities -
+// products, more than any unit.  Few rows: 1.2 us a step, of which one thread
+// spends 0.75 us issuing 16 MMAs at the tensor cores' pace and the rest waiting
+// its turn; without dequantisation it would still be 1.1 us, without softmax
+// 1.1 us (64 ragged paged sequences up to 128K, 2 bits, 8 tokens at most:
+// 955 us, 1.1 TB/s; four drafted tokens of 8 sequences of 4K: 44 us).  Many rows:
+// the tensor cores run half of the time (512 tokens behind 32K cached ones,
+// 4 bits, 32 heads of 128: 283 us, 0.98 PFLOP/s).  The roles' code together has to stay
+// within the instruction cache: two pieces side by side in the dequantising
+// loop took 1.4 times as long, a straight-line softmax 1.2 times.  Slower too:
+// a second issuing warp (308 -> 355 us), a warp that waits for operands on the
+// issuing one's behalf (304 -> 320 us), a fourth dequantising team (1063 -> 1165).
 #pragma once
 #include "attn_core.cuh"
 #include "chunk_attn.h"

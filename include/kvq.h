@@ -18,6 +18,10 @@
  * out[b, h, :] = softmax(S) V_hat[b, h/G_q],  S_l = sm_scale * q[b,h] . K_hat[b, h/G_q, l],
  * lse[b, h] = ln sum_l exp(S_l), with x_hat = s * code + z and code unsigned.
  *
+ * Before and between decode steps: attention over whole prompts
+ * (kvq_prompt_attn), their rows quantised into the cache (kvq_append_chunk),
+ * and attention of a chunk of new tokens over it (kvq_chunk_attn).
+ *
  * Cache format (this library's; the pages leave it open)
  * -------------------------------------------------------
  * head_dim D (64, 128 or 256); a block (= page) holds 128 consecutive tokens
@@ -351,8 +355,9 @@ KVQ_API kvq_status kvq_merge(const float* o_parts, const float* lse_parts, int32
  * second product (their sum is not), the output once at the end.
  *   cu_seqlens int32 [batch + 1], cu_seqlens[0] >= 0, not decreasing, at most
  *              total_tokens; sequences may be empty
- *   out        16-bit [total_tokens][num_q_heads][head_dim], contiguous; rows
- *              outside every sequence are left as they were
+ *   out        16-bit [total_tokens][num_q_heads][head_dim], contiguous, not
+ *              over the rows that are read; rows outside every sequence are
+ *              left as they were
  *   lse        fp32 [total_tokens][num_q_heads], or NULL
  * Device errors: KVQ_DEV_BAD_SEQ_LEN (a decreasing or out-of-range
  * cu_seqlens entry: that sequence is skipped), KVQ_DEV_TIMEOUT.
@@ -418,8 +423,9 @@ KVQ_API kvq_status kvq_chunk_workspace_size(const kvq_chunk_desc* desc, size_t* 
  *   cu_seqlens int32 [batch + 1] as for kvq_prompt_attn
  *   seq_lens   int32 [batch], each in [0, max_blocks * 128]
  *   page_table int32 [batch][max_blocks] or NULL (contiguous)
- *   out        16-bit [total_tokens][num_q_heads][head_dim], contiguous; rows
- *              outside every sequence are left as they were
+ *   out        16-bit [total_tokens][num_q_heads][head_dim], contiguous, not
+ *              over the rows that are read; rows outside every sequence are
+ *              left as they were
  *   lse        fp32 [total_tokens][num_q_heads], or NULL
  *   workspace  >= kvq_chunk_workspace_size bytes, 256-byte aligned; needs no
  *              initialisation; concurrent calls need separate workspaces

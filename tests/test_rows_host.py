@@ -175,3 +175,29 @@ def test_wrappers_refuse_bad_tensors():
         kvq.prompt_attn(q.clone().requires_grad_(), k, k, cu)
     empty = kvq.prompt_attn(q[:0], k[:0], k[:0], torch.zeros(2, dtype=torch.int32, device="cuda"))
     assert empty.shape == (0, 8, D)
+
+
+@pytest.mark.gpu
+def test_wrappers_refuse_outputs_over_their_inputs():
+    T, D = 6, 128
+    qkv = torch.zeros(T, 12, D, dtype=torch.bfloat16, device="cuda")
+    q, k, v = qkv[:, :8], qkv[:, 8:10], qkv[:, 10:]
+    cu = torch.tensor([0, T], dtype=torch.int32, device="cuda")
+    lens = torch.tensor([T], dtype=torch.int32, device="cuda")
+    desc = kvq.cache_desc(4, 1, 1, 2, 1)
+    caches = [kvq.alloc_cache(desc) for _ in "kv"]
+    window, other = (torch.zeros(1, 2, 128, D, device="cuda") for _ in "kv")
+    inside = qkv.view(-1)[-T * 8 * D:].view(T, 8, D)
+    own = q.contiguous()
+    bad = [lambda: kvq.prompt_attn(q, k, v, cu, out=inside), lambda: kvq.prompt_attn(own, k, v, cu, out=own),
+           lambda: kvq.prompt_attn(q, k, v, cu, lse=qkv.view(torch.float32).view(-1)[:T * 8].view(T, 8)),
+           lambda: kvq.chunk_attn(desc, own, *caches, cu, lens, max_blocks=1, out=own),
+           lambda: kvq.append_chunk(desc, k, v, cu, lens, *caches, window, window, max_blocks=1),
+           lambda: kvq.append_chunk(desc, k, v, cu, lens, *caches, window, other, max_blocks=1, k_window_out=other)]
+    for i, call in enumerate(bad):
+        with pytest.raises(ValueError, match="overlaps|same memory"):
+            call()
+            pytest.fail(f"call {i} was not refused")
+    out = torch.full((T + 1, 8, D), 7.0, dtype=torch.bfloat16, device="cuda")
+    assert kvq.prompt_attn(own, k, v, cu, out=out[:T]).abs().max().item() == 0.0
+    assert (out[T:] == 7.0).all()
