@@ -23,9 +23,9 @@
 // them and the softmax (16,384 tokens, 32 heads of 128, bf16, causal: 1.65 ms,
 // 1.34 PFLOP/s, 69% of a large library product's rate; a step of two tiles
 // takes 1.9 us of which 1.1 us are MMAs).  With short ones it is what a CTA
-// takes besides its steps, about 7 us (first copies, the diagonal's V, output):
-// 24 prompts of 12,289 tokens in all take 188 us where their products would
-// take 52.  Slower when tried: a second issuing warp (1.66 -> 1.99 ms), the
+// takes besides its steps, about 6 us (its tile found, first copies, the
+// diagonal's V, the last product, output): 24 prompts of 12,289 tokens in all
+// take 172 us where their products would take 52.  Slower when tried: a second issuing warp (1.66 -> 1.99 ms), the
 // probabilities handed over in halves (1.66 -> 1.81 ms).
 //
 // Tensor memory (512 columns): S_0, S_1 (128 each; P_i over S_i), O_0, O_1.
@@ -109,6 +109,7 @@ __device__ void find_tile(const RowAttnParams& p, int rank, int per_tile, bool l
     for (int i = 0; i < 8; ++i) {
       const int b = lane + 32 * i;
       nt[i] = 0;
+      if (32 * i >= p.batch) continue;
       if (b < p.batch) {
         const SeqRows s = seq_rows(p.cu, b, p.total);
         if (s.bad && lead) report(p.dev_status, KVQ_DEV_BAD_SEQ_LEN);
@@ -120,7 +121,8 @@ __device__ void find_tile(const RowAttnParams& p, int rank, int per_tile, bool l
     auto cum = [&](int t) {
       int n = 0;
 #pragma unroll
-      for (int i = 0; i < 8; ++i) n += max(0, nt[i] - t);
+      for (int i = 0; i < 8; ++i)
+        if (32 * i < p.batch) n += max(0, nt[i] - t);
       return __reduce_add_sync(0xffffffffu, n);
     };
     if (rank < cum(0)) {
@@ -134,11 +136,12 @@ __device__ void find_tile(const RowAttnParams& p, int rank, int per_tile, bool l
       int k = rank - cum(lo + 1);  // the k-th sequence with more than `tile` tiles
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
+        if (seq >= 0 || 32 * i >= p.batch) continue;
         const uint32_t has = __ballot_sync(0xffffffffu, nt[i] > tile);
-        if (seq < 0) {
-          if (k < __popc(has)) seq = 32 * i + __fns(has, 0, k + 1);
-          else k -= __popc(has);
-        }
+        const int before = __popc(has & ((1u << lane) - 1));
+        const uint32_t kth = __ballot_sync(0xffffffffu, nt[i] > tile && before == k);
+        if (kth != 0) seq = 32 * i + __ffs(kth) - 1;
+        else k -= __popc(has);
       }
     }
   } else {
@@ -560,34 +563,46 @@ prompt_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__
         ok = ok && __all_sync(0xffffffffu, wait(&aux->done, 0));
         if (ok && any) {
           tc_fence_after();
-          const long long row = (long long)(first + tok) * p.num_q_heads + kvh * p.gq + r % p.gq;
+          const int row = (first + tok) * p.num_q_heads + kvh * p.gq + r % p.gq;  // (at most 2^30 of them)
           const float inv = st.l > 0.f || isnan(st.l) ? 1.f / st.l : 0.f;
-          uint4* dst = reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.out) + row * D);
           const bool spoiled = aux->any_bad != 0;
+          // The warp's rows go out through Q's place in shared memory (16-byte units
+          // at unit ^ (row & 7)), so that neighbouring lanes write neighbouring units:
+          // written by its thread alone, a row is D / 8 stores of half sectors (2.7 us
+          // of a CTA's time; packed prompts 188 -> 172 us, head dim 256 178 -> 172 us).
+          unsigned char* stage = q_s + warp * (32 * D * 2);
 #pragma unroll
           for (int c = 0; c < D / 32; ++c) {
             uint32_t o[32];
             tmem_ld_32x32b_x32(t_o + 32 * c, o);
             tc_wait_ld();
-            if (mine) {
-              float x[32];
+            float x[32];
 #pragma unroll
-              for (int k = 0; k < 32; ++k) x[k] = __uint_as_float(o[k]) * inv;
-              if (spoiled) {
+            for (int k = 0; k < 32; ++k) x[k] = __uint_as_float(o[k]) * inv;
+            if (spoiled) {
 #pragma unroll
-                for (int k = 0; k < 32; ++k) {
-                  const uint32_t w = bad[32 * c + k], at = (uint32_t)(tok - clean * kTile);
-                  if ((w & kNone) != kNone && at >= (w & kNone)) x[k] = NAN;
-                  if ((w >> 10 & kNone) != kNone && at >= (w >> 10 & kNone)) x[k] += INFINITY;
-                  if ((w >> 20) != kNone && at >= (w >> 20)) x[k] -= INFINITY;
-                }
+              for (int k = 0; k < 32; ++k) {
+                const uint32_t w = bad[32 * c + k], at = (uint32_t)(tok - clean * kTile);
+                if ((w & kNone) != kNone && at >= (w & kNone)) x[k] = NAN;
+                if ((w >> 10 & kNone) != kNone && at >= (w >> 10 & kNone)) x[k] += INFINITY;
+                if ((w >> 20) != kNone && at >= (w >> 20)) x[k] -= INFINITY;
               }
-#pragma unroll
-              for (int k = 0; k < 4; ++k)
-                dst[4 * c + k] = make_uint4(round2<FP16>(x[8 * k], x[8 * k + 1]), round2<FP16>(x[8 * k + 2], x[8 * k + 3]),
-                                            round2<FP16>(x[8 * k + 4], x[8 * k + 5]),
-                                            round2<FP16>(x[8 * k + 6], x[8 * k + 7]));
             }
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+              *reinterpret_cast<uint4*>(stage + lane * (D * 2) + ((4 * c + k) ^ (lane & 7)) * 16) =
+                  make_uint4(round2<FP16>(x[8 * k], x[8 * k + 1]), round2<FP16>(x[8 * k + 2], x[8 * k + 3]),
+                             round2<FP16>(x[8 * k + 4], x[8 * k + 5]), round2<FP16>(x[8 * k + 6], x[8 * k + 7]));
+          }
+          __syncwarp();
+          constexpr int kUnits = D / 8, kAtOnce = 32 / kUnits;  // units of a row, rows of a store
+          const int rows_w = min(32, rows - (warp & 3) * 32), u = lane % kUnits;
+#pragma unroll 4
+          for (int i0 = 0; i0 < 32; i0 += kAtOnce) {
+            const int rr = i0 + lane / kUnits, to = __shfl_sync(0xffffffffu, row, rr);
+            if (rr < rows_w)
+              reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.out) + (long long)to * D)[u] =
+                  *reinterpret_cast<const uint4*>(stage + rr * (D * 2) + (u ^ (rr & 7)) * 16);
           }
           if (mine && p.lse != nullptr) p.lse[row] = row_lse<FP16>(st, p.scale_log2);
         }
