@@ -42,8 +42,8 @@
 // 1.1 us (64 ragged paged sequences up to 128K, 2 bits, 8 tokens at most:
 // 955 us, 1.1 TB/s; four drafted tokens of 8 sequences of 4K: 44 us).  Many rows:
 // the tensor cores run half of the time (512 tokens behind 32K cached ones,
-// 4 bits, 32 heads of 128: 283 us, 0.98 PFLOP/s).  The roles' code together has to stay
-// within the instruction cache: two pieces side by side in the dequantising
+// 4 bits, 32 heads of 128: 276 us, 1.0 PFLOP/s).  The roles' code together has
+// to stay within the instruction cache: two pieces side by side in the dequantising
 // loop took 1.4 times as long, a straight-line softmax 1.2 times.  Slower too:
 // a second issuing warp (308 -> 355 us), a warp that waits for operands on the
 // issuing one's behalf (304 -> 320 us), a fourth dequantising team (1063 -> 1165).
@@ -354,6 +354,77 @@ __device__ __forceinline__ void dequant_part(int t, uint32_t codes, uint32_t tab
   }
 }
 
+// ------------------------------------------------------------------ Q rows
+
+// 16-byte unit u of row rr of this warp's 32 in a row tile's Q operand.
+__device__ __forceinline__ uint4* unit_of(unsigned char* q_s, int rr, int u) {
+  const int at = (threadIdx.x & 96) + rr;
+  return reinterpret_cast<uint4*>(q_s + u / 8 * 16384 + at * 128 + ((u % 8) ^ (at & 7)) * 16);
+}
+
+// This warp's 32 Q rows -> fp16 operand rows, channels in operand order; this
+// thread's is at data + off, if `mine`.  A lane has 16 channels of every kR-th
+// row, so that lines are read whole.  bf16 rows are scaled by a power of two
+// that brings the largest magnitude to [2^13, 2^14): eight significant bits down
+// to 2^-30 of it, nothing overflows.  Returns what undoes it in this thread's row.
+template <int BITS, int D>
+__device__ __forceinline__ float stage_rows(const uint16_t* data, long long off, bool mine, bool fp16, unsigned char* q_s) {
+  constexpr int kL = D / 16, kR = 32 / kL, kIts = 32 / kR, kB = 4;  // lanes of a row, rows at once; kB in flight
+  const int lane = threadIdx.x & 31, u2 = lane % kL;
+  const uint32_t there = __ballot_sync(0xffffffffu, mine);
+  int my_ex = 0;
+  auto up_of = [](int ex) { return ex > 0 && ex < 255 ? min(13 + 127 - ex, 100) : 0; };
+#pragma unroll 1
+  for (int b = 0; b < kIts; b += kB) {
+    uint4 v[kB][2];
+#pragma unroll
+    for (int k = 0; k < kB; ++k) {
+      const int rr = (b + k) * kR + lane / kL;
+      const uint4* src = reinterpret_cast<const uint4*>(data + __shfl_sync(0xffffffffu, off, rr)) + 2 * u2;
+#pragma unroll
+      for (int hf = 0; hf < 2; ++hf) v[k][hf] = there >> rr & 1 ? src[hf] : make_uint4(0u, 0u, 0u, 0u);
+    }
+#pragma unroll
+    for (int k = 0; k < kB; ++k) {
+      const int rr = (b + k) * kR + lane / kL;
+      const uint32_t w[8] = {v[k][0].x, v[k][0].y, v[k][0].z, v[k][0].w, v[k][1].x, v[k][1].y, v[k][1].z, v[k][1].w};
+      float mul = 1.f;
+      if (!fp16) {
+        uint32_t most = 0;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) most = __vmaxu2(most, w[j] & 0x7fff7fffu);
+        int ex = (int)(max(most & 0xffffu, most >> 16) >> 7);  // biased exponent
+#pragma unroll
+        for (int o = kL / 2; o > 0; o >>= 1) ex = max(ex, __shfl_xor_sync(0xffffffffu, ex, o));
+        mul = __uint_as_float((uint32_t)(up_of(ex) + 127) << 23);
+        const int got = __shfl_sync(0xffffffffu, ex, lane % kR * kL);
+        if (lane / kR == b + k) my_ex = got;  // this thread's own row
+      }
+      float f[16];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        if (fp16) {
+          const float2 h = __half22float2(as_h2(w[j]));
+          f[2 * j] = h.x;
+          f[2 * j + 1] = h.y;
+        } else {
+          f[2 * j] = __uint_as_float(w[j] << 16) * mul;
+          f[2 * j + 1] = __uint_as_float(w[j] & 0xffff0000u) * mul;
+        }
+      }
+#pragma unroll
+      for (int hf = 0; hf < 2; ++hf) {
+        uint32_t o[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          o[j] = rows::round2<true>(f[element_at<BITS>(8 * hf + 2 * j)], f[element_at<BITS>(8 * hf + 2 * j + 1)]);
+        *unit_of(q_s, rr, 2 * u2 + hf) = make_uint4(o[0], o[1], o[2], o[3]);
+      }
+    }
+  }
+  return __uint_as_float((uint32_t)(127 - up_of(my_ex)) << 23);
+}
+
 // ------------------------------------------------------------- the kernel
 
 template <int BITS, int D, int NT>
@@ -465,57 +536,66 @@ __global__ void __launch_bounds__(threads_of(D, NT), 1) chunk_kernel(const Param
         const bool mine = row_i < rows_i, any = ((warp & 3) * 32 & (share - 1)) < rows_i;
         const int tok = tok0 + i * tok_tile + row_i / p.gq, head = g.kvh * p.gq + row_i % p.gq;
         const int pos = g.len - g.n + tok;
-        // Q row -> fp16, channels in operand order.  bf16 rows are scaled by a
-        // power of two that brings the largest magnitude to [2^13, 2^14): eight
-        // significant bits down to 2^-30 of it, nothing overflows.
+        auto unit_at = [&](int rr, int u) { return unit_of(q_s + i * kChunks * 16384, rr, u); };
+        // Q rows -> fp16 (stage_rows).  With two row tiles by whole warps; with one, the
+        // thread's own row, by less code, is the better of the two (four chunks of
+        // 2,048 tokens 1212 -> 1176 us with the output's below, but 64 ragged
+        // sequences of a few tokens 956 -> 988 us).
         float c = p.scale_log2;
         if (g.tiles > 0) {
-          const uint4* src = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p.q.data) +
-                                                            (long long)(g.first + tok) * p.q.st + head * p.q.sh);
-          float mul = 1.f;
-          if (mine && !p.fp16) {
-            uint32_t most = 0;
+          if constexpr (NT == 2) {
+            if (any)
+              c *= stage_rows<BITS, D>(static_cast<const uint16_t*>(p.q.data),
+                                       (long long)(g.first + tok) * p.q.st + (long long)head * p.q.sh, mine, p.fp16 != 0,
+                                       q_s + i * kChunks * 16384);
+          } else {
+            const uint4* src = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p.q.data) +
+                                                              (long long)(g.first + tok) * p.q.st + head * p.q.sh);
+            float mul = 1.f;
+            if (mine && !p.fp16) {
+              uint32_t most = 0;
 #pragma unroll 16
-            for (int e = 0; e < D / 8; ++e) {
-              const uint4 v = src[e];
-              most = __vmaxu2(most, __vmaxu2(__vmaxu2(v.x & 0x7fff7fffu, v.y & 0x7fff7fffu),
-                                             __vmaxu2(v.z & 0x7fff7fffu, v.w & 0x7fff7fffu)));
+              for (int e = 0; e < D / 8; ++e) {
+                const uint4 v = src[e];
+                most = __vmaxu2(most, __vmaxu2(__vmaxu2(v.x & 0x7fff7fffu, v.y & 0x7fff7fffu),
+                                               __vmaxu2(v.z & 0x7fff7fffu, v.w & 0x7fff7fffu)));
+              }
+              const int ex = (int)(max(most & 0xffffu, most >> 16) >> 7);  // biased exponent
+              if (ex > 0 && ex < 255) {
+                const int up = min(13 + 127 - ex, 100);
+                mul = __uint_as_float((uint32_t)(up + 127) << 23);
+                c *= __uint_as_float((uint32_t)(127 - up) << 23);
+              }
             }
-            const int ex = (int)(max(most & 0xffffu, most >> 16) >> 7);  // biased exponent
-            if (ex > 0 && ex < 255) {
-              const int up = min(13 + 127 - ex, 100);
-              mul = __uint_as_float((uint32_t)(up + 127) << 23);
-              c *= __uint_as_float((uint32_t)(127 - up) << 23);
-            }
-          }
-          if (any) {
+            if (any) {
 #pragma unroll 4
-            for (int e = 0; e < D / 16; ++e) {
-              float f[16];
+              for (int e = 0; e < D / 16; ++e) {
+                float f[16];
 #pragma unroll
-              for (int hf = 0; hf < 2; ++hf) {
-                const uint4 v = mine ? src[2 * e + hf] : make_uint4(0u, 0u, 0u, 0u);
-                const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+                for (int hf = 0; hf < 2; ++hf) {
+                  const uint4 v = mine ? src[2 * e + hf] : make_uint4(0u, 0u, 0u, 0u);
+                  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                  if (p.fp16) {
-                    const float2 h = __half22float2(as_h2(w[j]));
-                    f[8 * hf + 2 * j] = h.x;
-                    f[8 * hf + 2 * j + 1] = h.y;
-                  } else {
-                    f[8 * hf + 2 * j] = __uint_as_float(w[j] << 16) * mul;
-                    f[8 * hf + 2 * j + 1] = __uint_as_float(w[j] & 0xffff0000u) * mul;
+                  for (int j = 0; j < 4; ++j) {
+                    if (p.fp16) {
+                      const float2 h = __half22float2(as_h2(w[j]));
+                      f[8 * hf + 2 * j] = h.x;
+                      f[8 * hf + 2 * j + 1] = h.y;
+                    } else {
+                      f[8 * hf + 2 * j] = __uint_as_float(w[j] << 16) * mul;
+                      f[8 * hf + 2 * j + 1] = __uint_as_float(w[j] & 0xffff0000u) * mul;
+                    }
                   }
                 }
-              }
-              unsigned char* dst = q_s + (i * kChunks + e / 4) * 16384 + r * 128;
+                unsigned char* dst = q_s + (i * kChunks + e / 4) * 16384 + r * 128;
 #pragma unroll
-              for (int hf = 0; hf < 2; ++hf) {
-                uint32_t o[4];
+                for (int hf = 0; hf < 2; ++hf) {
+                  uint32_t o[4];
 #pragma unroll
-                for (int j = 0; j < 4; ++j)
-                  o[j] = rows::round2<true>(f[element_at<BITS>(8 * hf + 2 * j)], f[element_at<BITS>(8 * hf + 2 * j + 1)]);
-                *reinterpret_cast<uint4*>(dst + (((e % 4 * 2 + hf) ^ (r & 7)) << 4)) = make_uint4(o[0], o[1], o[2], o[3]);
+                  for (int j = 0; j < 4; ++j)
+                    o[j] = rows::round2<true>(f[element_at<BITS>(8 * hf + 2 * j)], f[element_at<BITS>(8 * hf + 2 * j + 1)]);
+                  *reinterpret_cast<uint4*>(dst + (((e % 4 * 2 + hf) ^ (r & 7)) << 4)) = make_uint4(o[0], o[1], o[2], o[3]);
+                }
               }
             }
           }
@@ -577,17 +657,20 @@ __global__ void __launch_bounds__(threads_of(D, NT), 1) chunk_kernel(const Param
         float lse2 = seen_any ? st.m * c + log2f(st.l) - rows::shift_log2<true>() : -INFINITY;
         const long long row = (long long)(g.first + tok) * p.num_q_heads + head;
         const size_t prow = (size_t)max(g.slot, 0) * (NT * kTile) + i * kTile + row_i;
+        auto rounded = [&](const float* x) {  // 8 channels
+          uint32_t w[4];
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+            w[j] = p.fp16 ? rows::round2<true>(x[2 * j], x[2 * j + 1]) : rows::round2<false>(x[2 * j], x[2 * j + 1]);
+          return make_uint4(w[0], w[1], w[2], w[3]);
+        };
         auto put = [&](int col, const float* x) {  // 8 channels of this thread's row
           if (g.slot >= 0) {
             float4* dst = reinterpret_cast<float4*>(P.part_o + prow * D + col);
 #pragma unroll
             for (int e = 0; e < 2; ++e) dst[e] = make_float4(x[4 * e], x[4 * e + 1], x[4 * e + 2], x[4 * e + 3]);
           } else {
-            uint32_t w[4];
-#pragma unroll
-            for (int j = 0; j < 4; ++j)
-              w[j] = p.fp16 ? rows::round2<true>(x[2 * j], x[2 * j + 1]) : rows::round2<false>(x[2 * j], x[2 * j + 1]);
-            *reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.out) + row * D + col) = make_uint4(w[0], w[1], w[2], w[3]);
+            *reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.out) + row * D + col) = rounded(x);
           }
         };
         auto sums = [&](int col, float (&x)[32]) {
@@ -598,7 +681,43 @@ __global__ void __launch_bounds__(threads_of(D, NT), 1) chunk_kernel(const Param
           for (int e = 0; e < 32; ++e) x[e] = seen_any ? __uint_as_float(o[e]) * f : 0.f;
         };
         if (copies == 1) {
-          if (any) {
+          // Rows go out: with two row tiles through Q's place, so that neighbouring
+          // lanes write neighbouring units (the rows are this warp's own there too,
+          // and the next segment's are put there by it); with one as above.
+          if (NT == 2 && any) {
+            const int passes = g.slot >= 0 ? 2 : 1, chans = D / passes;  // fp32: half of the channels at a time
+            const int rows_w = min(32, rows_i - (warp & 3) * 32);
+            constexpr int kUnits = D / 8, kAtOnce = 32 / kUnits;
+            const unsigned long long own =
+                g.slot >= 0 ? (unsigned long long)(P.part_o + prow * D)
+                            : (unsigned long long)(static_cast<uint16_t*>(p.out) + row * D);
+#pragma unroll 1
+            for (int pass = 0; pass < passes; ++pass) {
+#pragma unroll 1
+              for (int col = 0; col < chans; col += 32) {
+                float x[32];
+                sums(pass * chans + col, x);
+                if (g.slot >= 0) {
+#pragma unroll
+                  for (int e = 0; e < 8; ++e)
+                    *reinterpret_cast<float4*>(unit_at(lane, col / 4 + e)) =
+                        make_float4(x[4 * e], x[4 * e + 1], x[4 * e + 2], x[4 * e + 3]);
+                } else {
+#pragma unroll
+                  for (int e = 0; e < 4; ++e) *unit_at(lane, col / 8 + e) = rounded(x + 8 * e);
+                }
+              }
+              __syncwarp();
+#pragma unroll 4
+              for (int i0 = 0; i0 < 32; i0 += kAtOnce) {
+                const int rr = i0 + lane / kUnits, u = lane % kUnits;
+                uint4* dst = reinterpret_cast<uint4*>(__shfl_sync(0xffffffffu, own, rr)) + pass * kUnits + u;
+                if (rr < rows_w) *dst = *unit_at(rr, u);
+              }
+              __syncwarp();
+            }
+          }
+          if (NT == 1 && any) {
 #pragma unroll 1
             for (int col = 0; col < D; col += 32) {
               float x[32];
