@@ -64,7 +64,7 @@ __global__ void __launch_bounds__(kMergeThreads) merge_kernel(const Params P, in
   for (int k = 0; k <= parts; ++k) {
     const size_t at_part = part(k);
     const float l = P.part_lse[at_part];
-    const float w = m == -INFINITY ? 0.f : exp2f(l - m);  // 0: nothing seen in this part
+    const float w = l == -INFINITY ? 0.f : exp2f(l - m);  // 0: nothing seen in this part (NaN stays, m passes it over)
     sum += w;
     const float4* o = reinterpret_cast<const float4*>(P.part_o + at_part * D) + sub;
 #pragma unroll

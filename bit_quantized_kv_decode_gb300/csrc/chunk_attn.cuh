@@ -741,7 +741,10 @@ __global__ void __launch_bounds__(threads_of(D, NT), 1) chunk_kernel(const Param
           join();
           float m = -INFINITY, w = 0.f;
           for (int e = 0; e < copies; ++e) m = fmaxf(m, xs[e * share + row_i]);
-          for (int e = 0; e < copies; ++e) w += m == -INFINITY ? 0.f : exp2f(xs[e * share + row_i] - m);
+          for (int e = 0; e < copies; ++e) {
+            const float l = xs[e * share + row_i];
+            w += l == -INFINITY ? 0.f : exp2f(l - m);  // (NaN stays, m passes it over)
+          }
           f = seen_any ? f * exp2f(lse2 - m) / w : 0.f;
           lse2 = w > 0.f || isnan(w) ? m + log2f(w) : -INFINITY;
           join();

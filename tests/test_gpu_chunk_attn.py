@@ -121,6 +121,29 @@ def test_query_magnitudes(exponent):
     s.check(sm_scale=2.0 ** -max(0, exponent - 3))
 
 
+@pytest.mark.parametrize("exponent", [-130, -14, 60])
+@pytest.mark.parametrize("dim,n", [(128, 9), (64, 20), (256, 40)])
+def test_query_magnitudes_of_few_rows(exponent, dim, n):
+    s = Setup(4, (1, 0), dim, 64, 1, 3, new=(n,), total=(500,), seed=18)
+    f = torch.exp2(torch.linspace(0, exponent, n, device="cuda").round())
+    s.q = (s.q.float() * f[:, None, None]).to(torch.bfloat16)
+    s.check(sm_scale=2.0 ** -max(0, exponent - 3))
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+@pytest.mark.parametrize("new", [(6, 3), (70, 90)])
+def test_queries_that_are_not_finite_stay_in_their_rows(dtype, new):
+    s = Setup(dtype=DTYPES[dtype], new=new, total=(500, 1400), seed=19)
+    good, good_lse = s.check()
+    s.q[2, 1, 5] = math.nan
+    s.q[4, 0, 7] = math.inf
+    out, lse = s.call()
+    keep = torch.ones(out.shape[:2], dtype=torch.bool, device="cuda")
+    keep[2, 1] = keep[4, 0] = False
+    assert torch.equal(out[keep], good[keep]) and torch.equal(lse[keep], good_lse[keep])
+    assert out[2, 1].isnan().all() and lse[2, 1].isnan()
+
+
 def test_rows_before_the_first_token_are_empty():
     """Chunks longer than what the cache holds: rows at negative positions."""
     s = Setup(new=(10, 200), total=(4, 130), seed=8)
