@@ -180,7 +180,8 @@ __device__ void find_tile(const RowAttnParams& p, int rank, int per_tile, bool l
 // A V tile that some rows see only in part: tokens from `valid` on (another
 // sequence's rows, or none) become zeros, and values that are not finite are
 // zeroed and noted in `bad`, so that a zero probability keeps them out of the
-// rows before them; the epilogue adds them to the rows from there on.  token0:
+// rows before them; the epilogue adds them to the rows from there on (without a
+// causal mask: to all).  token0:
 // the tile's first token as `bad` counts them.  By THREADS threads, in their
 // own time: this one is number `me`.
 template <bool FP16, int THREADS>
@@ -566,6 +567,8 @@ prompt_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__
           const int row = (first + tok) * p.num_q_heads + kvh * p.gq + r % p.gq;  // (at most 2^30 of them)
           const float inv = st.l > 0.f || isnan(st.l) ? 1.f / st.l : 0.f;
           const bool spoiled = aux->any_bad != 0;
+          // this row's token as `bad` counts them; without a mask every row sees all of them
+          const uint32_t at = p.causal ? (uint32_t)(tok - clean * kTile) : kNone;
           // The warp's rows go out through Q's place in shared memory (16-byte units
           // at unit ^ (row & 7)), so that neighbouring lanes write neighbouring units:
           // written by its thread alone, a row is D / 8 stores of half sectors (2.7 us
@@ -582,7 +585,7 @@ prompt_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__
             if (spoiled) {
 #pragma unroll
               for (int k = 0; k < 32; ++k) {
-                const uint32_t w = bad[32 * c + k], at = (uint32_t)(tok - clean * kTile);
+                const uint32_t w = bad[32 * c + k];
                 if ((w & kNone) != kNone && at >= (w & kNone)) x[k] = NAN;
                 if ((w >> 10 & kNone) != kNone && at >= (w >> 10 & kNone)) x[k] += INFINITY;
                 if ((w >> 20) != kNone && at >= (w >> 20)) x[k] -= INFINITY;
