@@ -567,8 +567,8 @@ prompt_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__
           const int row = (first + tok) * p.num_q_heads + kvh * p.gq + r % p.gq;  // (at most 2^30 of them)
           const float inv = st.l > 0.f || isnan(st.l) ? 1.f / st.l : 0.f;
           const bool spoiled = aux->any_bad != 0;
-          // this row's token as `bad` counts them; without a mask every row sees all of them
-          const uint32_t at = p.causal ? (uint32_t)(tok - clean * kTile) : kNone;
+          // this row's token as `bad` counts them (-1: the last one before); without a mask every row sees all of them
+          const int at = p.causal ? tok - clean * kTile : (int)kNone;
           // The warp's rows go out through Q's place in shared memory (16-byte units
           // at unit ^ (row & 7)), so that neighbouring lanes write neighbouring units:
           // written by its thread alone, a row is D / 8 stores of half sectors (2.7 us
@@ -586,9 +586,9 @@ prompt_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__
 #pragma unroll
               for (int k = 0; k < 32; ++k) {
                 const uint32_t w = bad[32 * c + k];
-                if ((w & kNone) != kNone && at >= (w & kNone)) x[k] = NAN;
-                if ((w >> 10 & kNone) != kNone && at >= (w >> 10 & kNone)) x[k] += INFINITY;
-                if ((w >> 20) != kNone && at >= (w >> 20)) x[k] -= INFINITY;
+                if ((w & kNone) != kNone && at >= (int)(w & kNone)) x[k] = NAN;
+                if ((w >> 10 & kNone) != kNone && at >= (int)(w >> 10 & kNone)) x[k] += INFINITY;
+                if ((w >> 20) != kNone && at >= (int)(w >> 20)) x[k] -= INFINITY;
               }
             }
 #pragma unroll
