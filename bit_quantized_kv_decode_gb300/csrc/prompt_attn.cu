@@ -94,13 +94,23 @@ static_assert(sizeof(Aux) <= 512, "Aux");
 constexpr uint32_t kNone = 0x3ff;
 constexpr uint32_t kNoneAll = kNone | kNone << 10 | kNone << 20;
 
+// Reports entries of cu_seqlens that are out of range or go back, wherever they
+// stand.  Run by a warp of the first CTA that has nothing else to do, since
+// find_tile reads no further than the CTA's own sequence.
+__device__ void check_starts(const RowAttnParams& p) {
+  bool bad = false;
+#pragma unroll 8
+  for (int b = threadIdx.x & 31; b < p.batch; b += 32) bad |= seq_rows(p.cu, b, p.total).bad;
+  if (bad) report(p.dev_status, KVQ_DEV_BAD_SEQ_LEN);
+}
+
 // Which sequence and tile the rank-th CTA of a KV head has.  Run by one warp.
 // Causal tiles cost in proportion to their place in the sequence, so they are
 // handed out by falling place over all sequences at once: the rank's place t
 // is found by bisection on cum(t) = sum_b max(0, tiles_b - t), the number of
 // tiles at places >= t.  (Up to 256 sequences, eight to a lane; beyond that,
 // and without a causal mask, in order of the sequences.)
-__device__ void find_tile(const RowAttnParams& p, int rank, int per_tile, bool lead, Aux* aux) {
+__device__ void find_tile(const RowAttnParams& p, int rank, int per_tile, Aux* aux) {
   const int lane = threadIdx.x & 31;
   int seq = -1, tile = -1;
   if (p.causal && p.batch <= 256) {
@@ -110,11 +120,7 @@ __device__ void find_tile(const RowAttnParams& p, int rank, int per_tile, bool l
       const int b = lane + 32 * i;
       nt[i] = 0;
       if (32 * i >= p.batch) continue;
-      if (b < p.batch) {
-        const SeqRows s = seq_rows(p.cu, b, p.total);
-        if (s.bad && lead) report(p.dev_status, KVQ_DEV_BAD_SEQ_LEN);
-        nt[i] = (s.n + per_tile - 1) / per_tile;
-      }
+      if (b < p.batch) nt[i] = (seq_rows(p.cu, b, p.total).n + per_tile - 1) / per_tile;
       most = max(most, nt[i]);
     }
     most = __reduce_max_sync(0xffffffffu, most);
@@ -149,7 +155,6 @@ __device__ void find_tile(const RowAttnParams& p, int rank, int per_tile, bool l
       const int b = b0 + lane;
       SeqRows s{0, 0, false};
       if (b < p.batch) s = seq_rows(p.cu, b, p.total);
-      if (s.bad && lead) report(p.dev_status, KVQ_DEV_BAD_SEQ_LEN);
       const int n = (s.n + per_tile - 1) / per_tile;
       int incl = n;
 #pragma unroll
@@ -181,9 +186,8 @@ __device__ void find_tile(const RowAttnParams& p, int rank, int per_tile, bool l
 // sequence's rows, or none) become zeros, and values that are not finite are
 // zeroed and noted in `bad`, so that a zero probability keeps them out of the
 // rows before them; the epilogue adds them to the rows from there on (without a
-// causal mask: to all).  token0:
-// the tile's first token as `bad` counts them.  By THREADS threads, in their
-// own time: this one is number `me`.
+// causal mask: to all).  token0: the tile's first token as `bad` counts them.
+// By THREADS threads, in their own time: this one is number `me`.
 template <bool FP16, int THREADS>
 __device__ __forceinline__ void mend_values(int me, unsigned char* slot, int chunks, int channel0, int token0, int valid,
                                             uint32_t* bad, int* any_bad) {
@@ -247,7 +251,7 @@ prompt_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__
   const int tok_tile = kTile / p.gq;          // tokens of a row tile
   const int tok_cta = tok_tile * NT;
 
-  if (warp == 0) find_tile(p, rank, tok_cta, blockIdx.x == 0, aux);
+  if (warp == 0) find_tile(p, rank, tok_cta, aux);
   if (warp == 8) {
     if (lane == 0) {
       tma_prefetch_map(&map_q);
@@ -521,6 +525,8 @@ prompt_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__
           mbar_arrive(&aux->p[j & 1]);
         }
       }
+    } else if (warp == 11 && blockIdx.x == 0) {
+      check_starts(p);
     }
     } else {
       // ------------------------------------------------------------ softmax
@@ -611,6 +617,8 @@ prompt_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__
         }
       }
     }
+  } else if (warp == 11 && blockIdx.x == 0) {  // no sequence has rows
+    check_starts(p);
   }
   __syncwarp();
   tc_fence_before();
