@@ -783,77 +783,78 @@ __global__ void __launch_bounds__(threads_of(D, NT), 1) chunk_kernel(const Param
         }
         tc_fence_before();  // the accumulators are read before the next segment's products
       }
-    } else if (dq >= 0) {
-      // -------------------------------------------------- dequantisation
-      if (D <= 128) setmaxnreg_dec<NT == 2 ? 56 : 80>();
-      const int me = dq >> 2, t = (dq & 3) * 32 + lane;  // this team takes units me, me + kDq, ...
-      if (me < kDq) {
-        const bool k_col = p.k_scheme == KVQ_CHANNELWISE, v_col = p.v_scheme == KVQ_TOKENWISE;
-        // The team's own barrier, with a vote.  Every warp of it comes here after
-        // each segment is read and after each unit's table is written, whatever
-        // its waits returned, so that all of them go on or leave together.
-        auto together = [&](bool ok) -> bool {
-          uint32_t all;
-          asm volatile(
-              "{\n\t.reg .pred q, r;\n\tsetp.ne.u32 q, %1, 0;\n\tbarrier.cta.red.and.pred r, %2, 128, q;\n\t"
-              "selp.u32 %0, 1, 0, r;\n\t}"
-              : "=r"(all)
-              : "r"((uint32_t)ok), "r"(me + 1)
-              : "memory");
-          return all != 0;
-        };
-        // Units of a segment of n key tiles: K_0 V_0 K_1 V_1 ... with one score
-        // tile ahead, else K_0 K_1 V_0 K_2 V_1 ... K_n-1 V_n-2 V_n-1.
-        auto is_value = [](int i, int n) { return kAhead == 1 ? (i & 1) != 0 : (i >= 2 && !(i & 1)) || i == 2 * n - 1; };
-        int u = me, first = 0, did = 0;  // next unit, units of the segments before, units done
-        int slot_r = me, round_r = 0;    // its place in the ring of packed blocks
-        Segment g;
-        for (int k = 0; together(next_segment(k, g)); ++k) {
-          const int end = first + 2 * g.tiles;
-          bool ok = true;
-          for (; u < end; u += kDq) {
-            unsigned char* src = raw + slot_r * P.unit_bytes;
-            unsigned char* table = tables + (me * 2 + (did & 1)) * P.table_bytes;
-            const bool value = is_value(u - first, g.tiles), by_column = value ? v_col : k_col;
-            ok = ok && __all_sync(0xffffffffu, wait(&aux->raw_full[slot_r], round_r & 1));
-            if (ok) {
-              const uint16_t* s = reinterpret_cast<const uint16_t*>(src + kBlockTokens * D * BITS / 8);
-              prepare_table<BITS>(t, s, s + nsz, nsz, by_column, value, D, P.gshift, aux->raw_bad[slot_r] != 0, table,
-                                  p.dev_status);
-            }
-            ok = together(ok);
-            if (!ok) break;
-#pragma unroll 1
-            for (int part = 0; part < kParts && ok; ++part) {
-              const int n = u * kParts + part, sl = n % kSlots, round = n / kSlots;
-              if (round > 0) ok = __all_sync(0xffffffffu, wait(&aux->empty[sl], (round - 1) & 1));
-              if (!ok) break;
-              const uint32_t dst = smem_u32(ring) + sl * kSlot;
-              if (value) {
-                if (by_column) dequant_part<BITS, D, true, true>(t, smem_u32(src), smem_u32(table), nsz, part, P.gshift, dst);
-                else dequant_part<BITS, D, true, false>(t, smem_u32(src), smem_u32(table), nsz, part, P.gshift, dst);
-              } else {
-                if (by_column) dequant_part<BITS, D, false, true>(t, smem_u32(src), smem_u32(table), nsz, part, P.gshift, dst);
-                else dequant_part<BITS, D, false, false>(t, smem_u32(src), smem_u32(table), nsz, part, P.gshift, dst);
-              }
-              fence_proxy_async_smem();
-              __syncwarp();
-              if (lane == 0) mbar_arrive(&aux->full[sl]);
-            }
-            if (ok && lane == 0) mbar_arrive(&aux->raw_empty[slot_r]);
-            ++did;
-            slot_r += kDq;
-            if (slot_r >= P.units) {
-              slot_r = me;
-              ++round_r;
-            }
-          }
-          first = end;
-        }
-      }
     } else {
+      // One instruction for all of these warps: a warpgroup's four have to reach
+      // the same one, and three of them dequantise while the last has another role.
       if (D <= 128) setmaxnreg_dec<NT == 2 ? 56 : 80>();
-      if (role == kCopies) {
+      if (dq >= 0) {
+        // ------------------------------------------------ dequantisation
+        const int me = dq >> 2, t = (dq & 3) * 32 + lane;  // this team takes units me, me + kDq, ...
+        if (me < kDq) {
+          const bool k_col = p.k_scheme == KVQ_CHANNELWISE, v_col = p.v_scheme == KVQ_TOKENWISE;
+          // The team's own barrier, with a vote.  Every warp of it comes here after
+          // each segment is read and after each unit's table is written, whatever
+          // its waits returned, so that all of them go on or leave together.
+          auto together = [&](bool ok) -> bool {
+            uint32_t all;
+            asm volatile(
+                "{\n\t.reg .pred q, r;\n\tsetp.ne.u32 q, %1, 0;\n\tbarrier.cta.red.and.pred r, %2, 128, q;\n\t"
+                "selp.u32 %0, 1, 0, r;\n\t}"
+                : "=r"(all)
+                : "r"((uint32_t)ok), "r"(me + 1)
+                : "memory");
+            return all != 0;
+          };
+          // Units of a segment of n key tiles: K_0 V_0 K_1 V_1 ... with one score
+          // tile ahead, else K_0 K_1 V_0 K_2 V_1 ... K_n-1 V_n-2 V_n-1.
+          auto is_value = [](int i, int n) { return kAhead == 1 ? (i & 1) != 0 : (i >= 2 && !(i & 1)) || i == 2 * n - 1; };
+          int u = me, first = 0, did = 0;  // next unit, units of the segments before, units done
+          int slot_r = me, round_r = 0;    // its place in the ring of packed blocks
+          Segment g;
+          for (int k = 0; together(next_segment(k, g)); ++k) {
+            const int end = first + 2 * g.tiles;
+            bool ok = true;
+            for (; u < end; u += kDq) {
+              unsigned char* src = raw + slot_r * P.unit_bytes;
+              unsigned char* table = tables + (me * 2 + (did & 1)) * P.table_bytes;
+              const bool value = is_value(u - first, g.tiles), by_column = value ? v_col : k_col;
+              ok = ok && __all_sync(0xffffffffu, wait(&aux->raw_full[slot_r], round_r & 1));
+              if (ok) {
+                const uint16_t* s = reinterpret_cast<const uint16_t*>(src + kBlockTokens * D * BITS / 8);
+                prepare_table<BITS>(t, s, s + nsz, nsz, by_column, value, D, P.gshift, aux->raw_bad[slot_r] != 0, table,
+                                    p.dev_status);
+              }
+              ok = together(ok);
+              if (!ok) break;
+  #pragma unroll 1
+              for (int part = 0; part < kParts && ok; ++part) {
+                const int n = u * kParts + part, sl = n % kSlots, round = n / kSlots;
+                if (round > 0) ok = __all_sync(0xffffffffu, wait(&aux->empty[sl], (round - 1) & 1));
+                if (!ok) break;
+                const uint32_t dst = smem_u32(ring) + sl * kSlot;
+                if (value) {
+                  if (by_column) dequant_part<BITS, D, true, true>(t, smem_u32(src), smem_u32(table), nsz, part, P.gshift, dst);
+                  else dequant_part<BITS, D, true, false>(t, smem_u32(src), smem_u32(table), nsz, part, P.gshift, dst);
+                } else {
+                  if (by_column) dequant_part<BITS, D, false, true>(t, smem_u32(src), smem_u32(table), nsz, part, P.gshift, dst);
+                  else dequant_part<BITS, D, false, false>(t, smem_u32(src), smem_u32(table), nsz, part, P.gshift, dst);
+                }
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&aux->full[sl]);
+              }
+              if (ok && lane == 0) mbar_arrive(&aux->raw_empty[slot_r]);
+              ++did;
+              slot_r += kDq;
+              if (slot_r >= P.units) {
+                slot_r = me;
+                ++round_r;
+              }
+            }
+            first = end;
+          }
+        }
+      } else if (role == kCopies) {
         // ---------------------------------------------------------- copies
         int u = 0;
         bool ok = true;
