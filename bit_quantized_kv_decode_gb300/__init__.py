@@ -428,8 +428,10 @@ def append_chunk(desc: CacheDesc, k_new: torch.Tensor, v_new: torch.Tensor, cu_s
     (bf16, fp16 or fp32, strided) go to positions seq_lens[b], ... of sequence
     b.  The windows (fp32 [B, Hkv, 128, head_dim]) hold the raw rows of each
     sequence's partial last block, as for append; they are updated in place
-    unless *_window_out is given, and a token-wise cache may do without.  The
-    caller advances seq_lens afterwards.  Returns (k_cache, v_cache)."""
+    unless *_window_out is given.  A token-wise cache may do without, but append
+    must not follow inside a block written so: it quantises the whole block from
+    its window (chunks of one row do not).  The caller advances seq_lens
+    afterwards.  Returns (k_cache, v_cache)."""
     H, D = desc.num_kv_heads, desc.head_dim
     kr = _rows(k_new, "k_new", _DTYPES, None, H, D)
     T = k_new.shape[0]

@@ -220,7 +220,8 @@ KVQ_API kvq_status kvq_pack(const kvq_cache_desc* cache, int32_t which, const fl
  * caller then advances seq_lens[b] by one; when a block fills, the next
  * block's rows overwrite the window from row 0 (no reset needed).  A cache
  * that starts from kvq_pack of a prefix needs the prefix's partial last block
- * copied into the window first.
+ * copied into the window first (kvq_append_chunk keeps the window it is given
+ * up to date).
  *   x_new      fp32 [batch][num_kv_heads][head_dim], 16-byte aligned
  *   seq_lens   int32 [batch], each in [0, max_blocks * 128)
  *   page_table int32 [batch][max_blocks] or NULL (contiguous; then
@@ -381,7 +382,10 @@ KVQ_API kvq_status kvq_prompt_attn(const kvq_prompt_desc* desc, const kvq_rows* 
  * last block is full).  window_out may be the window itself; with another
  * buffer the call can be repeated or undone, as drafted tokens that are
  * rejected need it.  A token-wise cache may do without (both NULL): its
- * earlier codes are kept as they are.
+ * earlier codes are kept as they are.  kvq_append must not follow inside a
+ * block that was appended to without a window: it quantizes the whole block
+ * from a window that does not hold its rows.  Single tokens of such a cache
+ * are appended as chunks of one row.
  *   dtype      KVQ_BF16, KVQ_FP16 or KVQ_FP32: k and v
  *   k, v       rows [total_tokens][num_kv_heads][head_dim]
  *   cu_seqlens int32 [batch + 1] as for kvq_prompt_attn
