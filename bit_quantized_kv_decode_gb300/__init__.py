@@ -465,7 +465,8 @@ def append_chunk(desc: CacheDesc, k_new: torch.Tensor, v_new: torch.Tensor, cu_s
 
 
 def chunk_workspace_size(desc: CacheDesc, batch: int, total_tokens: int, num_q_heads: int, max_blocks: int) -> int:
-    """Workspace bytes of a chunk_attn call with these sizes."""
+    """Workspace bytes of a chunk_attn call with these sizes (the same for every
+    batch, number of tokens and heads of a cache geometry)."""
     d = ChunkDesc(desc, _lib.BF16, batch, total_tokens, num_q_heads, max_blocks, 1, 0.0, 0)
     n = ctypes.c_size_t()
     _lib.check(library().kvq_chunk_workspace_size(ctypes.byref(d), ctypes.byref(n)), "kvq_chunk_workspace_size")

@@ -123,11 +123,12 @@ ChunkPlan chunk_plan(int head_dim, int group, int bits, int batch, int total, in
   // (head dim 256: one, its accumulators fill tensor memory; nor where shared
   // memory is too small for two, as with 4-bit codes in groups of 32 at 128)
   const long long rows = (long long)total * (num_q_heads / num_kv_heads);
-  c.nt = head_dim <= 128 && rows > (long long)batch * chunk::kTile && chunk::memory_of(head_dim, group, bits, 2).units > 0
-             ? 2
-             : 1;
+  const int most = head_dim <= 128 && chunk::memory_of(head_dim, group, bits, 2).units > 0 ? 2 : 1;
+  c.nt = rows > (long long)batch * chunk::kTile ? most : 1;
   c.grid = chunk::kGrid;
-  const size_t slots = (size_t)2 * c.grid * c.nt * chunk::kTile;
+  // the workspace of the larger shape for both: fewer sequences may take two row
+  // tiles where more take one, and a buffer made for the larger call serves both
+  const size_t slots = (size_t)2 * c.grid * most * chunk::kTile;
   c.part_lse = slots * head_dim * sizeof(float);
   c.total = c.part_lse + slots * sizeof(float);
   return c;

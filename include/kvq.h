@@ -405,7 +405,9 @@ KVQ_API kvq_status kvq_append_chunk(const kvq_cache_desc* cache, int32_t dtype, 
                                     uint8_t* v_codes, uint16_t* v_scale, uint16_t* v_zero, uint32_t* dev_status,
                                     void* stream);
 
-/* Workspace bytes kvq_chunk_attn needs for `desc` (host only, no device needed). */
+/* Workspace bytes kvq_chunk_attn needs for `desc` (host only, no device
+ * needed): 20 or 40 MB, set by the cache's geometry alone, so that one buffer
+ * serves calls of any batch, number of tokens and heads. */
 KVQ_API kvq_status kvq_chunk_workspace_size(const kvq_chunk_desc* desc, size_t* bytes);
 
 /*
