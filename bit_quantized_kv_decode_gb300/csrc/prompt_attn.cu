@@ -149,6 +149,7 @@ __device__ void find_tile(const RowAttnParams& p, int rank, int per_tile, Aux* a
         if (kth != 0) seq = 32 * i + __ffs(kth) - 1;
         else k -= __popc(has);
       }
+      if (seq < 0) tile = -1;  // (more tiles than 31 bits, of sequences that share their rows)
     }
   } else {
     for (int b0 = 0; b0 < p.batch && seq < 0; b0 += 32) {

@@ -361,7 +361,10 @@ KVQ_API kvq_status kvq_merge(const float* o_parts, const float* lse_parts, int32
  *              left as they were
  *   lse        fp32 [total_tokens][num_q_heads], or NULL
  * Device errors: KVQ_DEV_BAD_SEQ_LEN (a decreasing or out-of-range
- * cu_seqlens entry: that sequence is skipped), KVQ_DEV_TIMEOUT.
+ * cu_seqlens entry: that sequence is skipped; where sequences behind a
+ * decreasing entry have rows that earlier ones have too, the launch may be too
+ * small for all of them, and rows of any sequence may be left as they were),
+ * KVQ_DEV_TIMEOUT.
  */
 KVQ_API kvq_status kvq_prompt_attn(const kvq_prompt_desc* desc, const kvq_rows* q, const kvq_rows* k,
                                    const kvq_rows* v, const int32_t* cu_seqlens, void* out, float* lse,
@@ -394,8 +397,10 @@ KVQ_API kvq_status kvq_prompt_attn(const kvq_prompt_desc* desc, const kvq_rows* 
  *   windows    fp32 [batch][num_kv_heads][128][head_dim], 16-byte aligned;
  *              window and window_out of a channel-wise scheme must be given
  * Device errors as kvq_append; a sequence with a bad length or a bad page is
- * skipped (that block of it).  Values that are not finite, or whose group
- * overflows fp16, leave their group zero and set KVQ_DEV_NONFINITE.
+ * skipped (that block of it), and where sequences behind a decreasing
+ * cu_seqlens entry share rows, blocks of any sequence may be left as they were.
+ * Values that are not finite, or whose group overflows fp16, leave their group
+ * zero and set KVQ_DEV_NONFINITE.
  */
 KVQ_API kvq_status kvq_append_chunk(const kvq_cache_desc* cache, int32_t dtype, const kvq_rows* k, const kvq_rows* v,
                                     int32_t batch, int32_t total_tokens, const int32_t* cu_seqlens,
@@ -435,8 +440,10 @@ KVQ_API kvq_status kvq_chunk_workspace_size(const kvq_chunk_desc* desc, size_t* 
  *   lse        fp32 [total_tokens][num_q_heads], or NULL
  *   workspace  >= kvq_chunk_workspace_size bytes, 256-byte aligned; needs no
  *              initialisation; concurrent calls need separate workspaces
- * Device errors: KVQ_DEV_BAD_SEQ_LEN (rows of that sequence: out = 0,
- * lse = -inf), KVQ_DEV_BAD_PAGE (that block's values are taken as zeros),
+ * Device errors: KVQ_DEV_BAD_SEQ_LEN (seq_lens: rows of that sequence get out =
+ * 0, lse = -inf; cu_seqlens: that sequence is skipped, and a row that two
+ * sequences have behind a decreasing entry holds either's result),
+ * KVQ_DEV_BAD_PAGE (that block's values are taken as zeros),
  * KVQ_DEV_NONFINITE, KVQ_DEV_TIMEOUT.
  */
 KVQ_API kvq_status kvq_chunk_attn(const kvq_chunk_desc* desc, const kvq_rows* q, const uint8_t* k_codes,
