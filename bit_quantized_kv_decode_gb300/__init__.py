@@ -356,11 +356,11 @@ def _cache_ptrs(desc: CacheDesc, name: str, cache, device: int):
             _ptr(scale, name + " scale", _SCALES, n, device), _ptr(zero, name + " zero", _SCALES, n, device))
 
 
-def _apart(t: torch.Tensor, name: str, rows, tokens: int, heads, dim: int) -> None:
+def _apart(at: int, size: int, name: str, rows, tokens: int, heads, dim: int) -> None:
     """Refuses an output over the memory of rows that other CTAs may still read."""
-    at, end = t.data_ptr(), t.data_ptr() + t.numel() * t.element_size()
     for r, h in zip(rows, heads):
-        if tokens and r.data and r.data < end and at < r.data + ((tokens - 1) * r.stride_token + (h - 1) * r.stride_head + dim) * 2:
+        read = ((tokens - 1) * r.stride_token + (h - 1) * r.stride_head + dim) * 2
+        if tokens and r.data and at < r.data + read and r.data < at + size:
             raise ValueError(f"{name} overlaps the rows that are read")
 
 
@@ -371,14 +371,16 @@ def _outputs(q: torch.Tensor, T: int, Hq: int, D: int, out, lse, return_lse: boo
         po = out.data_ptr()
     else:
         po = _ptr(out, "out", (q.dtype,), T * Hq * D, device)
-        _apart(out, "out", rows, T, heads, D)
+        _apart(po, T * Hq * D * 2, "out", rows, T, heads, D)
     if lse is None:
         if not return_lse:
             return out, None, po, None
         lse = q.new_empty(T, Hq, dtype=torch.float32)
         return out, lse, po, lse.data_ptr()
     pl = _ptr(lse, "lse", (torch.float32,), T * Hq, device)
-    _apart(lse, "lse", rows, T, heads, D)
+    _apart(pl, T * Hq * 4, "lse", rows, T, heads, D)
+    if T and po < pl + T * Hq * 4 and pl < po + T * Hq * D * 2:
+        raise ValueError("lse overlaps out")
     return out, lse, po, pl
 
 
@@ -418,6 +420,22 @@ def prompt_attn(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu_seqlens: t
     return out if lse is None else (out, lse)
 
 
+def _windows_apart(kw, kwo, vw, vwo, size: int, kr: Rows, vr: Rows, T: int, H: int, D: int, element: int) -> None:
+    """Refuses windows (of `size` bytes each) that are written over memory that
+    the call reads or writes elsewhere."""
+    if kw and vw and (abs(kwo - vw) < size or abs(kwo - vwo) < size or abs(vwo - kw) < size):
+        raise ValueError("k_window and v_window share the same memory")
+    if kw and 0 < abs(kwo - kw) < size or vw and 0 < abs(vwo - vw) < size:
+        raise ValueError("a window's output overlaps it in part")
+    k, v = kr.data, vr.data
+    if T and k and v:
+        k_end = k + ((T - 1) * kr.stride_token + (H - 1) * kr.stride_head + D) * element
+        v_end = v + ((T - 1) * vr.stride_token + (H - 1) * vr.stride_head + D) * element
+        for o in (kwo, vwo):
+            if o and (o < k_end and k < o + size or o < v_end and v < o + size):
+                raise ValueError("a window overlaps the rows that are read")
+
+
 def append_chunk(desc: CacheDesc, k_new: torch.Tensor, v_new: torch.Tensor, cu_seqlens: torch.Tensor,
                  seq_lens: torch.Tensor, k_cache, v_cache, k_window: Optional[torch.Tensor] = None,
                  v_window: Optional[torch.Tensor] = None, page_table: Optional[torch.Tensor] = None,
@@ -443,7 +461,7 @@ def append_chunk(desc: CacheDesc, k_new: torch.Tensor, v_new: torch.Tensor, cu_s
     mb, pt = _blocks_per_sequence(B, page_table, max_blocks, dev, "append_chunk")
     if seq_lens is None:
         raise ValueError("seq_lens must be int32 [batch]")
-    windows = []
+    windows, size = [], B * H * BLOCK_TOKENS * D
     for name, w, o, scheme in (("k_window", k_window, k_window_out, desc.k_scheme),
                                ("v_window", v_window, v_window_out, desc.v_scheme)):
         if w is None:
@@ -451,12 +469,11 @@ def append_chunk(desc: CacheDesc, k_new: torch.Tensor, v_new: torch.Tensor, cu_s
                 raise ValueError(f"{name} is required (a channel-wise group runs along the block's tokens)")
             windows += [None, None]
             continue
-        size = B * H * BLOCK_TOKENS * D
         pw = _ptr(w, name, (torch.float32,), size, dev)
         windows += [pw, pw if o is None else _ptr(o, name + "_out", (torch.float32,), size, dev)]
     kw, kwo, vw, vwo = windows
-    if kwo is not None and kwo in (vw, vwo) or vwo is not None and vwo == kw:
-        raise ValueError("k_window and v_window are the same memory")
+    if kw or vw:
+        _windows_apart(kw, kwo, vw, vwo, size * 4, kr, vr, T, H, D, k_new.element_size())
     _launch(dev, "kvq_append_chunk", library().kvq_append_chunk, ctypes.byref(desc), _DTYPES[k_new.dtype],
             ctypes.byref(kr), ctypes.byref(vr), B, T, pcu, _ptr(seq_lens, "seq_lens", (torch.int32,), B, dev), pt, mb,
             kw, vw, kwo, vwo, *_cache_ptrs(desc, "k_cache", k_cache, dev), *_cache_ptrs(desc, "v_cache", v_cache, dev),
@@ -467,7 +484,10 @@ def append_chunk(desc: CacheDesc, k_new: torch.Tensor, v_new: torch.Tensor, cu_s
 def chunk_workspace_size(desc: CacheDesc, batch: int, total_tokens: int, num_q_heads: int, max_blocks: int) -> int:
     """Workspace bytes of a chunk_attn call with these sizes (the same for every
     batch, number of tokens and heads of a cache geometry)."""
-    d = ChunkDesc(desc, _lib.BF16, batch, total_tokens, num_q_heads, max_blocks, 1, 0.0, 0)
+    return _workspace_bytes(ChunkDesc(desc, _lib.BF16, batch, total_tokens, num_q_heads, max_blocks, 1, 0.0, 0))
+
+
+def _workspace_bytes(d: ChunkDesc) -> int:
     n = ctypes.c_size_t()
     _lib.check(library().kvq_chunk_workspace_size(ctypes.byref(d), ctypes.byref(n)), "kvq_chunk_workspace_size")
     return n.value
@@ -495,12 +515,19 @@ def chunk_attn(desc: CacheDesc, q: torch.Tensor, k_cache, v_cache, cu_seqlens: t
     out, lse, po, pl = _outputs(q, T, Hq, D, out, lse, return_lse, dev, (qr,), (Hq,))
     d = ChunkDesc(desc, _DTYPES[q.dtype], B, T, Hq, mb, 1 if causal else 0, sm_scale, flags)
     if workspace is None:
-        n = ctypes.c_size_t()
-        _lib.check(library().kvq_chunk_workspace_size(ctypes.byref(d), ctypes.byref(n)), "kvq_chunk_workspace_size")
-        workspace = torch.empty(n.value, dtype=torch.uint8, device=q.device)
-    size = workspace.numel()
+        size = _workspace_bytes(d)
+        workspace = torch.empty(size, dtype=torch.uint8, device=q.device)
+        pw = workspace.data_ptr()
+    else:
+        size = workspace.numel()
+        pw = _ptr(workspace, "workspace", (torch.uint8,), size, dev)
+        if T and qr.data:
+            read = ((T - 1) * qr.stride_token + (Hq - 1) * qr.stride_head + D) * 2
+            for p, n in (po, T * Hq * D * 2), (pl or 0, T * Hq * 4), (qr.data, read):
+                # (of a longer workspace, the first bytes are used)
+                if p < pw + size and pw < p + n and p < pw + _workspace_bytes(d):
+                    raise ValueError("workspace overlaps q, out or lse")
     _launch(dev, "kvq_chunk_attn", library().kvq_chunk_attn, ctypes.byref(d), ctypes.byref(qr), *pk, *pv, pcu,
-            _ptr(seq_lens, "seq_lens", (torch.int32,), B, dev), pt, po, pl,
-            _ptr(workspace, "workspace", (torch.uint8,), size, dev), size,
+            _ptr(seq_lens, "seq_lens", (torch.int32,), B, dev), pt, po, pl, pw, size,
             _ptr(dev_status, "dev_status", _STATUS, 1, dev))
     return out if lse is None else (out, lse)

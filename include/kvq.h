@@ -395,7 +395,9 @@ KVQ_API kvq_status kvq_prompt_attn(const kvq_prompt_desc* desc, const kvq_rows* 
  *   seq_lens   int32 [batch], tokens already cached; seq_lens[b] plus the
  *              chunk's length at most max_blocks * 128
  *   windows    fp32 [batch][num_kv_heads][128][head_dim], 16-byte aligned;
- *              window and window_out of a channel-wise scheme must be given
+ *              window and window_out of a channel-wise scheme must be given; a
+ *              window_out that is not its window shares no memory with it, and
+ *              none shares any with the other cache's or the rows
  * Device errors as kvq_append; a sequence with a bad length or a bad page is
  * skipped (that block of it), and where sequences behind a decreasing
  * cu_seqlens entry share rows, blocks of any sequence may be left as they were.
@@ -438,8 +440,9 @@ KVQ_API kvq_status kvq_chunk_workspace_size(const kvq_chunk_desc* desc, size_t* 
  *              over the rows that are read; rows outside every sequence are
  *              left as they were
  *   lse        fp32 [total_tokens][num_q_heads], or NULL
- *   workspace  >= kvq_chunk_workspace_size bytes, 256-byte aligned; needs no
- *              initialisation; concurrent calls need separate workspaces
+ *   workspace  >= kvq_chunk_workspace_size bytes, 256-byte aligned, apart from
+ *              q, out and lse; needs no initialisation; concurrent calls need
+ *              separate workspaces
  * Device errors: KVQ_DEV_BAD_SEQ_LEN (seq_lens: rows of that sequence get out =
  * 0, lse = -inf; cu_seqlens: that sequence is skipped, and a row that two
  * sequences have behind a decreasing entry holds either's result),
