@@ -11,6 +11,7 @@ import ctypes
 from typing import Optional, Tuple
 
 import torch
+from torch.autograd import forward_ad
 
 from . import _lib
 from ._lib import (CHANNELWISE, DEV_BAD_PAGE, DEV_BAD_SEQ_LEN, DEV_NONFINITE, DEV_TIMEOUT, FLAG_E2M1_V, FLAG_TEST_STALL,
@@ -286,7 +287,7 @@ def _rows(t: torch.Tensor, name: str, dtypes, tokens=None, heads=None, dim=None)
     if isinstance(t, torch.Tensor) and t.is_cuda and t.dim() == 3 and t.dtype in dtypes:
         n, h, d = t.shape
         if (tokens is None or n == tokens) and (heads is None or h == heads) and (dim is None or d == dim) and \
-                not (t.requires_grad and torch.is_grad_enabled()):
+                not (t.requires_grad and torch.is_grad_enabled()) and not _has_tangent(t):
             st, sh, sc = t.stride()
             if n == 1:
                 st = h * d  # a single token's (head's) stride is free
@@ -301,6 +302,11 @@ def _rows(t: torch.Tensor, name: str, dtypes, tokens=None, heads=None, dim=None)
     raise ValueError(_why_not_rows(t, name, dtypes, tokens, heads, dim))
 
 
+def _has_tangent(t: torch.Tensor) -> bool:
+    # (no level of forward-mode differentiation entered, as nearly always: nothing to unpack)
+    return getattr(forward_ad, "_current_level", 0) >= 0 and forward_ad.unpack_dual(t).tangent is not None
+
+
 def _why_not_rows(t, name, dtypes, tokens, heads, dim) -> str:
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         return f"{name} must be a CUDA tensor"
@@ -313,6 +319,8 @@ def _why_not_rows(t, name, dtypes, tokens, heads, dim) -> str:
             return f"{name} must have {want} {what}, got {got}"
     if t.requires_grad and torch.is_grad_enabled():
         return f"{name} requires a gradient: this operator has no backward pass (use torch.no_grad())"
+    if _has_tangent(t):
+        return f"{name} has a tangent: this operator has no derivative (unpack it first)"
     return (f"{name} must have contiguous channels, token and head strides that are multiples of 16 bytes (at least "
             f"head_dim elements) and a 16-byte aligned start; got strides {tuple(t.stride())}")
 
