@@ -15,15 +15,17 @@
 // so more loads in flight), ranges are formed on 16-bit pairs.
 // append_edges_kernel takes the rest in fp32 -- the first and last block of a
 // chunk, with the window's rows and the tokens that stay, and every block of
-// fp32 rows.  They write disjoint places and run side by side.
+// fp32 rows.  They write disjoint places; the second starts once the last CTA of
+// the first has, so that the two overlap in the first one's last wave.
 //
 // The work is one pass over the rows, and memory would bound it below about ten
 // instructions a value; it takes 16 with everything, so whole blocks are bound
 // by instructions and barriers (65,536 tokens x 8 heads of 128, bf16 to 4 bits,
-// K channel-wise, V token-wise: 87 us, 3.9 TB/s, 59% of the issue slots), edges
-// by the latency of one block (128 sequences of a token, windows re-quantised:
-// 49 us, 2.8 TB/s).  Slower when tried: 16 warps to a whole block (140 -> 164
-// us); K and V of a block in one CTA, V's loads under K's stores, gained 2%.
+// K channel-wise, V token-wise: 90 us, 3.8 TB/s, 67% of the issue slots; as fp32
+// rows, all of them edges: 242 us, 2.5 TB/s), edges by the latency of one block
+// (128 sequences of a token, windows re-quantised: 51 us, 2.7 TB/s).  Slower
+// when tried: 16 warps to a whole block (140 -> 164 us); K and V of a block in
+// one CTA, V's loads under K's stores, gained 2%.
 //
 // The code of a value is clamp(rint(fl(fl(x - z) / s))) in IEEE fp32.  With
 // d = fl(x - z) and r = fl(1 / s) once per group, the quotient is corrected once
@@ -45,7 +47,7 @@ namespace {
 
 // Warps of a block.  Edges: twice as many, each with half the tokens (8 of a
 // thread): their loads and stores depend on one another, so what counts is how
-// many warps wait at a time (128 sequences of a token: 67 -> 54 us).
+// many warps wait at a time (256 sequences of a token: 67 -> 54 us).
 constexpr int kBlockWarps = 8, kEdgeWarps = 16;
 
 __device__ __forceinline__ float min_nan(float a, float b) {
@@ -619,7 +621,7 @@ __device__ __forceinline__ void append_edge(const AppendParams& p) {
 template <typename T, int BITS, int W, Part PART>
 __global__ void __launch_bounds__(32 * kEdgeWarps, sizeof(Raw<T>) == 8 ? 2 : 1) append_edges_kernel(const AppendParams p) {
   append_edge<T, BITS, W, PART>(p);
-  // launched beside append_blocks_kernel: what follows in the stream waits for
+  // overlaps append_blocks_kernel: what follows in the stream waits for
   // this grid, which is not done before that one is
   asm volatile("griddepcontrol.wait;" ::: "memory");
 }

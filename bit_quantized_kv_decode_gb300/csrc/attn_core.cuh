@@ -1,6 +1,6 @@
-// What the attention kernels over rows of new tokens share: which rows a CTA
-// has, one softmax step of a 128 x 128 score tile in tensor memory, and the
-// epilogue.
+// What the attention kernels over rows of new tokens share: bounded waits,
+// arithmetic on pairs, one softmax step of a 128 x 128 score tile in tensor
+// memory, and the loops that issue a tile's MMAs.
 //
 // Rows of a tile are (token, query head of one KV group) pairs, token-major:
 // all heads of the group ride in one tile, so K and V are read once for them
@@ -276,11 +276,6 @@ template <bool FP16>
 __device__ __forceinline__ float row_lse(const RowState& st, float c) {
   return st.l > 0.f || isnan(st.l) ? (st.m * c + log2f(st.l) - shift_log2<FP16>()) * 0.6931471805599453f : -INFINITY;
 }
-
-// 3-D tensor map of a row tensor (channels, heads, tokens), 128-byte swizzle,
-// boxes of 64 channels x `heads` x `tokens`.  Defined in prompt_attn.cu.
-cudaError_t encode_rows_map(void* map, const Rows& r, int head_dim, int heads, int total, int box_heads, int box_tokens,
-                            bool fp16);
 
 }  // namespace rows
 }  // namespace kvq

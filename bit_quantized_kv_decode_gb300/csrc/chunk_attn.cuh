@@ -40,9 +40,9 @@
 // spends 0.75 us issuing 16 MMAs at the tensor cores' pace and the rest waiting
 // its turn; without dequantisation it would still be 1.1 us, without softmax
 // 1.1 us (64 ragged paged sequences up to 128K, 2 bits, 8 tokens at most:
-// 955 us, 1.1 TB/s; four drafted tokens of 8 sequences of 4K: 44 us).  Many rows:
+// 962 us, 1.1 TB/s; four drafted tokens of 8 sequences of 4K: 44 us).  Many rows:
 // the tensor cores run half of the time (512 tokens behind 32K cached ones,
-// 4 bits, 32 heads of 128: 276 us, 1.0 PFLOP/s).  The roles' code together has
+// 4 bits, 32 heads of 128: 278 us, 1.0 PFLOP/s).  The roles' code together has
 // to stay within the instruction cache: two pieces side by side in the dequantising
 // loop took 1.4 times as long, a straight-line softmax 1.2 times.  Slower too:
 // a second issuing warp (308 -> 355 us), a warp that waits for operands on the
@@ -84,7 +84,8 @@ __device__ __forceinline__ int key_tiles(const Seq& s, int t, int tok, int causa
 // costs beside its steps (Q, the epilogue, filling the pipeline), so that a CTA
 // with many short tiles is not the last.  (32 sequences at head dim 256: 156 us
 // without, 132 with 3, 137 with 6; head dim 128, 64 ragged sequences: 1063,
-// 1026 with 10; four drafted tokens: 55.6, 52 with 6 or 10, 56 with 16.)
+// 1026 with 10; four drafted tokens: 55.6, 52 with 6 or 10, 56 with 16.  Head dim
+// 64 has 128's, without a measurement of its own.)
 __device__ __forceinline__ int tile_cost(int head_dim) { return head_dim > 128 ? 3 : 8; }
 __device__ __forceinline__ int work_steps(int n) { return max(1, n); }
 __device__ __forceinline__ int tile_steps(const RowAttnParams& p, const Seq& s, int t, int tok) {

@@ -36,7 +36,10 @@
 
 namespace kvq {
 namespace rows {
+namespace {
 
+// 3-D tensor map of a row tensor (channels, heads, tokens), 128-byte swizzle,
+// boxes of 64 channels x `box_heads` x `box_tokens`.
 cudaError_t encode_rows_map(void* map, const Rows& r, int head_dim, int heads, int total, int box_heads, int box_tokens,
                             bool fp16) {
   static const PFN_cuTensorMapEncodeTiled_v12000 encode = [] {
@@ -59,8 +62,6 @@ cudaError_t encode_rows_map(void* map, const Rows& r, int head_dim, int heads, i
                             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   return e == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
 }
-
-namespace {
 
 template <int D>
 struct Shape {
