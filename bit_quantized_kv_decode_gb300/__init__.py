@@ -8,7 +8,7 @@ computation runs in the library's CUDA kernels; there is no other code path.
 from __future__ import annotations
 
 import ctypes
-from typing import Optional, Tuple
+from typing import NamedTuple, Optional, Tuple
 
 import torch
 from torch.autograd import forward_ad
@@ -25,7 +25,8 @@ __all__ = ["CacheDesc", "AttnDesc", "KvqError", "TOKENWISE", "CHANNELWISE", "OPE
            "DEV_BAD_SEQ_LEN", "DEV_BAD_PAGE", "DEV_NONFINITE", "DEV_TIMEOUT", "FLAG_TEST_STALL", "FLAG_TEST_STALL_MMA",
            "FLAG_E2M1_V", "cache_desc", "attn_desc", "cache_bytes", "block_bytes", "sz_per_block", "alloc_cache", "pack",
            "append", "dequant", "workspace_size", "decode_attn", "decode_attn_static", "merge", "library",
-           "prompt_attn", "append_chunk", "chunk_workspace_size", "chunk_attn"]
+           "prompt_attn", "append_chunk", "chunk_workspace_size", "chunk_attn", "rotary_table", "append_rotary",
+           "select_blocks", "sparse_workspace_size", "sparse_decode_attn"]
 
 
 def library() -> ctypes.CDLL:
@@ -444,20 +445,17 @@ def _windows_apart(kw, kwo, vw, vwo, size: int, kr: Rows, vr: Rows, T: int, H: i
                 raise ValueError("a window overlaps the rows that are read")
 
 
-def append_chunk(desc: CacheDesc, k_new: torch.Tensor, v_new: torch.Tensor, cu_seqlens: torch.Tensor,
-                 seq_lens: torch.Tensor, k_cache, v_cache, k_window: Optional[torch.Tensor] = None,
-                 v_window: Optional[torch.Tensor] = None, page_table: Optional[torch.Tensor] = None,
-                 max_blocks: Optional[int] = None, k_window_out: Optional[torch.Tensor] = None,
-                 v_window_out: Optional[torch.Tensor] = None, dev_status: Optional[torch.Tensor] = None):
-    """Append a ragged chunk of new tokens to the packed K and V caches: rows
-    [cu_seqlens[b], cu_seqlens[b + 1]) of k_new and v_new [T, Hkv, head_dim]
-    (bf16, fp16 or fp32, strided) go to positions seq_lens[b], ... of sequence
-    b.  The windows (fp32 [B, Hkv, 128, head_dim]) hold the raw rows of each
-    sequence's partial last block, as for append; they are updated in place
-    unless *_window_out is given.  A token-wise cache may do without, but append
-    must not follow inside a block written so: it quantises the whole block from
-    its window (chunks of one row do not).  The caller advances seq_lens
-    afterwards.  Returns (k_cache, v_cache)."""
+class _AppendArgs(NamedTuple):
+    device: int
+    rows: tuple    # element type, K rows, V rows, batch, tokens
+    places: tuple  # row offsets, lengths, page table, blocks per sequence
+    arrays: tuple  # windows and their outputs, the K cache, the V cache
+    status: Optional[int]
+
+
+def _append_args(desc, k_new, v_new, cu_seqlens, seq_lens, k_cache, v_cache, k_window, v_window, page_table, max_blocks,
+                 k_window_out, v_window_out, dev_status, what) -> _AppendArgs:
+    """The arguments of an append call, checked, as the library takes them."""
     H, D = desc.num_kv_heads, desc.head_dim
     kr = _rows(k_new, "k_new", _DTYPES, None, H, D)
     T = k_new.shape[0]
@@ -466,7 +464,7 @@ def append_chunk(desc: CacheDesc, k_new: torch.Tensor, v_new: torch.Tensor, cu_s
     if v_new.get_device() != dev:
         raise ValueError(f"k_new is on {k_new.device}, v_new on {v_new.device}")
     B, pcu = _starts(cu_seqlens, dev)
-    mb, pt = _blocks_per_sequence(B, page_table, max_blocks, dev, "append_chunk")
+    mb, pt = _blocks_per_sequence(B, page_table, max_blocks, dev, what)
     if seq_lens is None:
         raise ValueError("seq_lens must be int32 [batch]")
     windows, size = [], B * H * BLOCK_TOKENS * D
@@ -482,10 +480,30 @@ def append_chunk(desc: CacheDesc, k_new: torch.Tensor, v_new: torch.Tensor, cu_s
     kw, kwo, vw, vwo = windows
     if kw or vw:
         _windows_apart(kw, kwo, vw, vwo, size * 4, kr, vr, T, H, D, k_new.element_size())
-    _launch(dev, "kvq_append_chunk", library().kvq_append_chunk, ctypes.byref(desc), _DTYPES[k_new.dtype],
-            ctypes.byref(kr), ctypes.byref(vr), B, T, pcu, _ptr(seq_lens, "seq_lens", (torch.int32,), B, dev), pt, mb,
-            kw, vw, kwo, vwo, *_cache_ptrs(desc, "k_cache", k_cache, dev), *_cache_ptrs(desc, "v_cache", v_cache, dev),
-            _ptr(dev_status, "dev_status", _STATUS, 1, dev))
+    return _AppendArgs(dev, (_DTYPES[k_new.dtype], kr, vr, B, T),
+                       (pcu, _ptr(seq_lens, "seq_lens", (torch.int32,), B, dev), pt, mb),
+                       (kw, vw, kwo, vwo, *_cache_ptrs(desc, "k_cache", k_cache, dev),
+                        *_cache_ptrs(desc, "v_cache", v_cache, dev)), _ptr(dev_status, "dev_status", _STATUS, 1, dev))
+
+
+def append_chunk(desc: CacheDesc, k_new: torch.Tensor, v_new: torch.Tensor, cu_seqlens: torch.Tensor,
+                 seq_lens: torch.Tensor, k_cache, v_cache, k_window: Optional[torch.Tensor] = None,
+                 v_window: Optional[torch.Tensor] = None, page_table: Optional[torch.Tensor] = None,
+                 max_blocks: Optional[int] = None, k_window_out: Optional[torch.Tensor] = None,
+                 v_window_out: Optional[torch.Tensor] = None, dev_status: Optional[torch.Tensor] = None):
+    """Append a ragged chunk of new tokens to the packed K and V caches: rows
+    [cu_seqlens[b], cu_seqlens[b + 1]) of k_new and v_new [T, Hkv, head_dim]
+    (bf16, fp16 or fp32, strided) go to positions seq_lens[b], ... of sequence
+    b.  The windows (fp32 [B, Hkv, 128, head_dim]) hold the raw rows of each
+    sequence's partial last block, as for append; they are updated in place
+    unless *_window_out is given.  A token-wise cache may do without, but append
+    must not follow inside a block written so: it quantises the whole block from
+    its window (chunks of one row do not).  The caller advances seq_lens
+    afterwards.  Returns (k_cache, v_cache)."""
+    a = _append_args(desc, k_new, v_new, cu_seqlens, seq_lens, k_cache, v_cache, k_window, v_window, page_table, max_blocks,
+                     k_window_out, v_window_out, dev_status, "append_chunk")
+    _launch(a.device, "kvq_append_chunk", library().kvq_append_chunk, ctypes.byref(desc), *a.rows, *a.places, *a.arrays,
+            a.status)
     return k_cache, v_cache
 
 
@@ -537,5 +555,191 @@ def chunk_attn(desc: CacheDesc, q: torch.Tensor, k_cache, v_cache, cu_seqlens: t
                     raise ValueError("workspace overlaps q, out or lse")
     _launch(dev, "kvq_chunk_attn", library().kvq_chunk_attn, ctypes.byref(d), ctypes.byref(qr), *pk, *pv, pcu,
             _ptr(seq_lens, "seq_lens", (torch.int32,), B, dev), pt, po, pl, pw, size,
+            _ptr(dev_status, "dev_status", _STATUS, 1, dev))
+    return out if lse is None else (out, lse)
+
+
+def rotary_table(positions: int, dim: int, base: float = 10000.0, device="cuda") -> torch.Tensor:
+    """Angles for append_rotary: fp32 [positions, dim], the cosines of the dim / 2
+    angles p * base^(-2 i / dim) of position p, then their sines (in 64 bits,
+    rounded once).  A model with other frequencies fills such a tensor itself."""
+    inv = base ** (-torch.arange(0, dim, 2, dtype=torch.float64) / dim)
+    a = torch.arange(positions, dtype=torch.float64)[:, None] * inv
+    return torch.cat([a.cos(), a.sin()], 1).float().to(device)
+
+
+def _span(t: torch.Tensor):
+    """First and last address of a contiguous tensor."""
+    at = t.data_ptr()
+    return at, at + t.numel() * t.element_size()
+
+
+def _rows_span(r: Rows, tokens: int, heads: int, dim: int, element: int):
+    at = r.data or 0
+    return at, at + ((tokens - 1) * r.stride_token + (heads - 1) * r.stride_head + dim) * element
+
+
+def _disjoint(name: str, out, others) -> None:
+    a, e = out
+    for o in others:
+        if a < o[1] and o[0] < e:
+            raise ValueError(f"{name} overlaps another array of the call")
+
+
+def append_rotary(desc: CacheDesc, table: torch.Tensor, k_new: torch.Tensor, v_new: torch.Tensor, cu_seqlens: torch.Tensor,
+                  seq_lens: torch.Tensor, k_cache, v_cache, k_window: Optional[torch.Tensor] = None,
+                  v_window: Optional[torch.Tensor] = None, page_table: Optional[torch.Tensor] = None,
+                  max_blocks: Optional[int] = None, k_window_out: Optional[torch.Tensor] = None,
+                  v_window_out: Optional[torch.Tensor] = None, interleaved: bool = False,
+                  q: Optional[torch.Tensor] = None, q_out: Optional[torch.Tensor] = None,
+                  k_out: Optional[torch.Tensor] = None, dev_status: Optional[torch.Tensor] = None):
+    """append_chunk with K's rows turned by their positions on the way.
+
+    table: fp32 [positions, R] (rotary_table): the first R channels of a row at
+    position p are turned by the angles of table[p], as pairs (i, i + R / 2), or
+    (2 i, 2 i + 1) when interleaved.  K is quantised from the turned fp32 values;
+    k_window holds turned rows.  With q [T, Hq, head_dim], rows of the same
+    tokens and type, the turned queries are returned (q_out, made when not
+    given), else None; with k_out [T, Hkv, head_dim] the turned keys are written
+    there too, for prompt_attn.  Both are rounded once to the rows' type."""
+    a = _append_args(desc, k_new, v_new, cu_seqlens, seq_lens, k_cache, v_cache, k_window, v_window, page_table, max_blocks,
+                     k_window_out, v_window_out, dev_status, "append_rotary")
+    dev, D, H = a.device, desc.head_dim, desc.num_kv_heads
+    if not isinstance(table, torch.Tensor) or table.dim() != 2:
+        raise ValueError("table must be fp32 [positions, rotated channels]")
+    positions, dim = table.shape
+    rotary = _lib.Rotary(_ptr(table, "table", (torch.float32,), positions * dim, dev), positions, dim,
+                         1 if interleaved else 0)
+    dtype, T, size = (k_new.dtype,), a.rows[4], k_new.element_size()
+    qr, Hq, pq, pk = None, 0, None, None
+    if q is not None:
+        qr = _rows(q, "q", dtype, T, None, D)
+        Hq = q.shape[1]
+        if q.get_device() != dev:
+            raise ValueError(f"q is on {q.device}, k_new on {k_new.device}")
+        if q_out is None:
+            q_out = q.new_empty(T, Hq, D)
+        pq = _ptr(q_out, "q_out", dtype, T * Hq * D, dev)
+    elif q_out is not None:
+        raise ValueError("q_out without q")
+    if k_out is not None:
+        pk = _ptr(k_out, "k_out", dtype, T * H * D, dev)
+    if T and (pq or pk):
+        others = [_rows_span(r, T, h, D, size) for r, h in ((a.rows[1], H), (a.rows[2], H), (qr, Hq)) if r is not None]
+        others += [_span(t) for t in (k_window, v_window, k_window_out, v_window_out, table, cu_seqlens, seq_lens, page_table,
+                                      *k_cache, *v_cache) if t is not None]
+        for name, t in (("q_out", q_out), ("k_out", k_out)):
+            if t is not None:
+                _disjoint(name, _span(t), others)
+                others.append(_span(t))
+    _launch(dev, "kvq_append_rotary", library().kvq_append_rotary, ctypes.byref(desc), a.rows[0], ctypes.byref(rotary),
+            None if qr is None else ctypes.byref(qr), Hq, *a.rows[1:], *a.places, *a.arrays, pq, pk, a.status)
+    return q_out
+
+
+def _step_q(desc: CacheDesc, q: torch.Tensor):
+    """(batch, query heads, device, address) of a decode step's queries."""
+    if not isinstance(q, torch.Tensor) or not q.is_cuda or q.dtype is not torch.bfloat16 or q.dim() != 3 or \
+            q.shape[2] != desc.head_dim or not q.is_contiguous():
+        raise ValueError("q must be a contiguous bf16 CUDA tensor [batch, num_q_heads, head_dim]")
+    if (q.requires_grad and torch.is_grad_enabled()) or _has_tangent(q):
+        raise ValueError("q requires a gradient or has a tangent: this operator has no derivative")
+    return q.shape[0], q.shape[1], q.get_device(), q.data_ptr()
+
+
+def select_blocks(desc: CacheDesc, q: torch.Tensor, k_cache, seq_lens: torch.Tensor, budget: int, first: int = 1,
+                  last: int = 1, page_table: Optional[torch.Tensor] = None, max_blocks: Optional[int] = None,
+                  blocks: Optional[torch.Tensor] = None, counts: Optional[torch.Tensor] = None,
+                  dev_status: Optional[torch.Tensor] = None):
+    """The blocks of 128 tokens that a decode step's queries q [B, Hq, head_dim]
+    (bf16) may look at, per sequence and KV head: the first `first`, the last
+    `last`, and those whose keys can score highest by the scales and offsets of a
+    channel-wise K cache, `budget` in all.  Returns (blocks int32 [B, Hkv,
+    budget], in order, -1 behind the last; counts int32 [B, Hkv]), as
+    sparse_decode_attn takes them."""
+    B, Hq, dev, pq = _step_q(desc, q)
+    mb, pt = _blocks_per_sequence(B, page_table, max_blocks, dev, "select_blocks")
+    if seq_lens is None:
+        raise ValueError("seq_lens must be int32 [batch]")
+    H = desc.num_kv_heads
+    _, ks, kz = _cache_ptrs(desc, "k_cache", k_cache, dev)
+    if budget < 1:
+        raise ValueError("budget must be at least 1")
+    given = blocks is not None or counts is not None
+    if blocks is None:
+        blocks = torch.empty(B, H, budget, dtype=torch.int32, device=q.device)
+    if counts is None:
+        counts = torch.empty(B, H, dtype=torch.int32, device=q.device)
+    pb, pc = _ptr(blocks, "blocks", (torch.int32,), B * H * budget, dev), _ptr(counts, "counts", (torch.int32,), B * H, dev)
+    if given:
+        others = [_span(t) for t in (q, *k_cache, seq_lens, page_table) if t is not None]
+        _disjoint("blocks", _span(blocks), others + [_span(counts)])
+        _disjoint("counts", _span(counts), others)
+    d = _lib.SelectDesc(desc, B, Hq, mb, budget, first, last)
+    _launch(dev, "kvq_select_blocks", library().kvq_select_blocks, ctypes.byref(d), pq, ks, kz,
+            _ptr(seq_lens, "seq_lens", (torch.int32,), B, dev), pt, pb, pc, _ptr(dev_status, "dev_status", _STATUS, 1, dev))
+    return blocks, counts
+
+
+def sparse_workspace_size(desc: CacheDesc, batch: int, num_q_heads: int, list_len: int) -> int:
+    """Workspace bytes of a sparse_decode_attn call with these sizes (may be 0)."""
+    return _sparse_bytes(_lib.SparseDesc(desc, batch, num_q_heads, 1, list_len, 0.0, 0))
+
+
+def _sparse_bytes(d) -> int:
+    n = ctypes.c_size_t()
+    _lib.check(library().kvq_sparse_workspace_size(ctypes.byref(d), ctypes.byref(n)), "kvq_sparse_workspace_size")
+    return n.value
+
+
+def sparse_decode_attn(desc: CacheDesc, q: torch.Tensor, k_cache, v_cache, seq_lens: torch.Tensor, blocks: torch.Tensor,
+                       counts: torch.Tensor, page_table: Optional[torch.Tensor] = None, max_blocks: Optional[int] = None,
+                       sm_scale: float = 0.0, out: Optional[torch.Tensor] = None, lse: Optional[torch.Tensor] = None,
+                       return_lse: bool = False, workspace: Optional[torch.Tensor] = None,
+                       dev_status: Optional[torch.Tensor] = None, flags: int = 0):
+    """Decode attention of q [B, Hq, head_dim] (bf16) over the blocks listed for
+    each sequence and KV head alone: blocks int32 [B, Hkv, list_len] (block
+    numbers of the sequence, in any order), of which counts int32 [B, Hkv] are
+    read.  Returns out [B, Hq, head_dim] in bf16, and with return_lse (or an lse
+    buffer) also lse fp32 [B, Hq]."""
+    B, Hq, dev, pq = _step_q(desc, q)
+    mb, pt = _blocks_per_sequence(B, page_table, max_blocks, dev, "sparse_decode_attn")
+    H, D = desc.num_kv_heads, desc.head_dim
+    if not isinstance(blocks, torch.Tensor) or blocks.dim() != 3 or tuple(blocks.shape[:2]) != (B, H):
+        raise ValueError("blocks must be int32 [batch, num_kv_heads, list_len]")
+    if seq_lens is None or counts is None:
+        raise ValueError("seq_lens must be int32 [batch], counts int32 [batch, num_kv_heads]")
+    n = blocks.shape[2]
+    kc, vc = _cache_ptrs(desc, "k_cache", k_cache, dev), _cache_ptrs(desc, "v_cache", v_cache, dev)
+    pb, pc = _ptr(blocks, "blocks", (torch.int32,), B * H * n, dev), _ptr(counts, "counts", (torch.int32,), B * H, dev)
+    d = _lib.SparseDesc(desc, B, Hq, mb, n, sm_scale, flags)
+    need = _sparse_bytes(d)
+    written = []
+    if out is None:
+        out = torch.empty_like(q)
+    else:
+        written.append(("out", out))
+    if lse is None:
+        lse = torch.empty(B, Hq, dtype=torch.float32, device=q.device) if return_lse else None
+    else:
+        written.append(("lse", lse))
+    size = need
+    if workspace is None:
+        workspace = torch.empty(need, dtype=torch.uint8, device=q.device) if need else None
+        pw = workspace.data_ptr() if need else None
+    else:
+        size = workspace.numel()
+        pw = _ptr(workspace, "workspace", (torch.uint8,), size, dev)
+    po, pl = _ptr(out, "out", (q.dtype,), B * Hq * D, dev), _ptr(lse, "lse", (torch.float32,), B * Hq, dev)
+    spans = [(name, _span(t)) for name, t in written]
+    if need and size >= need:
+        spans.append(("workspace", (pw, pw + need)))  # (of a longer one, the first bytes are used)
+    if spans:
+        others = [_span(t) for t in (q, blocks, counts, seq_lens, page_table) if t is not None]
+        for name, span in spans:
+            _disjoint(name, span, others)
+            others.append(span)
+    _launch(dev, "kvq_sparse_decode_attn", library().kvq_sparse_decode_attn, ctypes.byref(d), pq, *kc, *vc,
+            _ptr(seq_lens, "seq_lens", (torch.int32,), B, dev), pt, pb, pc, po, pl, pw, size,
             _ptr(dev_status, "dev_status", _STATUS, 1, dev))
     return out if lse is None else (out, lse)

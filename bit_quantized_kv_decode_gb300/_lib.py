@@ -31,7 +31,8 @@ PATH_GENERAL = 1
 # Every symbol include/kvq.h declares.
 EXPORTS = ("kvq_status_string", "kvq_version", "kvq_cache_bytes", "kvq_pack", "kvq_append", "kvq_dequant",
            "kvq_decode_workspace_size", "kvq_decode_path", "kvq_decode_attn", "kvq_decode_attn_static", "kvq_merge",
-           "kvq_prompt_attn", "kvq_append_chunk", "kvq_chunk_workspace_size", "kvq_chunk_attn")
+           "kvq_prompt_attn", "kvq_append_chunk", "kvq_chunk_workspace_size", "kvq_chunk_attn",
+           "kvq_append_rotary", "kvq_select_blocks", "kvq_sparse_workspace_size", "kvq_sparse_decode_attn")
 
 
 class CacheDesc(ctypes.Structure):
@@ -60,6 +61,23 @@ class ChunkDesc(ctypes.Structure):
     _fields_ = [("cache", CacheDesc), ("dtype", ctypes.c_int32), ("batch", ctypes.c_int32),
                 ("total_tokens", ctypes.c_int32), ("num_q_heads", ctypes.c_int32), ("max_blocks", ctypes.c_int32),
                 ("causal", ctypes.c_int32), ("sm_scale", ctypes.c_float), ("flags", ctypes.c_uint32)]
+
+
+class Rotary(ctypes.Structure):
+    _fields_ = [("angles", ctypes.c_void_p), ("positions", ctypes.c_int32), ("dim", ctypes.c_int32),
+                ("interleaved", ctypes.c_int32)]
+
+
+class SelectDesc(ctypes.Structure):
+    _fields_ = [("cache", CacheDesc), ("batch", ctypes.c_int32), ("num_q_heads", ctypes.c_int32),
+                ("max_blocks", ctypes.c_int32), ("budget", ctypes.c_int32), ("first", ctypes.c_int32),
+                ("last", ctypes.c_int32)]
+
+
+class SparseDesc(ctypes.Structure):
+    _fields_ = [("cache", CacheDesc), ("batch", ctypes.c_int32), ("num_q_heads", ctypes.c_int32),
+                ("max_blocks", ctypes.c_int32), ("list_len", ctypes.c_int32), ("sm_scale", ctypes.c_float),
+                ("flags", ctypes.c_uint32)]
 
 
 class KvqError(RuntimeError):
@@ -117,6 +135,15 @@ def load(path: str | None = None) -> ctypes.CDLL:
     lib.kvq_chunk_workspace_size.argtypes = [ctypes.POINTER(ChunkDesc), ctypes.POINTER(SZ)]
     lib.kvq_chunk_attn.restype = I32
     lib.kvq_chunk_attn.argtypes = [ctypes.POINTER(ChunkDesc), R] + [P] * 12 + [SZ, P, P]
+    lib.kvq_append_rotary.restype = I32
+    lib.kvq_append_rotary.argtypes = [ctypes.POINTER(CacheDesc), I32, ctypes.POINTER(Rotary), R, I32, R, R, I32, I32, P, P,
+                                      P, I32] + [P] * 14
+    lib.kvq_select_blocks.restype = I32
+    lib.kvq_select_blocks.argtypes = [ctypes.POINTER(SelectDesc)] + [P] * 9
+    lib.kvq_sparse_workspace_size.restype = I32
+    lib.kvq_sparse_workspace_size.argtypes = [ctypes.POINTER(SparseDesc), ctypes.POINTER(SZ)]
+    lib.kvq_sparse_decode_attn.restype = I32
+    lib.kvq_sparse_decode_attn.argtypes = [ctypes.POINTER(SparseDesc)] + [P] * 14 + [SZ, P, P]
     _ = U32
     if path is None:
         _LIB = lib

@@ -44,6 +44,12 @@ __device__ __forceinline__ SeqRows seq_rows(const int32_t* cu, int b, int total)
 
 cudaError_t launch_prompt_attn(const RowAttnParams& p, cudaStream_t stream);
 
+// Rotation of the first `dim` channels of a row by its position: angles
+// [positions][dim], cosines and then sines.
+struct Turn {
+  const float* angles;
+  int dim, interleaved;
+};
 struct AppendParams {
   Rows x[2];  // K, V rows
   int dtype;
@@ -58,7 +64,24 @@ struct AppendParams {
   uint32_t* dev_status;
   int scheme[2];
   int bits, head_dim, group, num_kv_heads, num_pages, max_blocks, batch, total;
+  long long most;  // tokens a sequence may have
+  Turn turn;       // append_rotary: K's
 };
 cudaError_t launch_append_chunk(const AppendParams& p, cudaStream_t stream);
+cudaError_t launch_append_rotary(const AppendParams& p, cudaStream_t stream);
+
+// Rows turned by their positions and written as rows of the same type
+// (append_rotary.cu): queries, and keys where an attention over rows follows.
+struct TurnRowsParams {
+  Rows x[2];    // q, k
+  void* out[2];  // [total][heads][head_dim]
+  int heads[2];  // 0: none
+  int dtype, head_dim, batch, total;
+  const int32_t* cu;
+  const int32_t* seq_lens;
+  long long most;
+  Turn turn;
+};
+cudaError_t launch_turn_rows(const TurnRowsParams& p, cudaStream_t stream);
 
 }  // namespace kvq

@@ -25,6 +25,8 @@
 //   * channel-wise V: the K-steps of each token group accumulate into their
 //     own output block: O += s_g * partial_g + z_g * sum_(l in g) p_l.
 #pragma once
+#include <type_traits>
+
 #include "decode.cuh"
 #include "decode_general.h"
 
@@ -305,12 +307,52 @@ __device__ __forceinline__ int gen_find(const int* ps, int B, int c) {
   return lo;
 }
 
+// ------------------------------------------------- lists of blocks (ListParams)
+// Range r of unit u (CTA u * splits + r): {u, first entry, end, the sequence's
+// length}; {-1, ...} where there is none.  A unit's n entries are cut into
+// min(splits, n) ranges.
+__device__ __forceinline__ int4 listed_range(const ListParams& p, int cta) {
+  const int u = cta / p.splits, r = cta % p.splits, b = u / p.units_per_seq;
+  const ListedUnit w = listed_unit(p, u);
+  if (w.bad && r == 0 && threadIdx.x == 0) report(p.dev_status, KVQ_DEV_BAD_SEQ_LEN);
+  const int nr = min(p.splits, w.n);
+  if (r < nr) return make_int4(u, (int)((long long)r * w.n / nr), (int)((long long)(r + 1) * w.n / nr), w.len);
+  if (p.splits == 1) {  // nothing to attend to, and no merge to say so
+    const size_t row0 = (size_t)b * p.num_q_heads + (size_t)(u % p.units_per_seq) * p.gq;
+    for (int e = threadIdx.x; e < p.gq * p.head_dim; e += kThreads) p.out[row0 * p.head_dim + e] = 0;
+    if (threadIdx.x < p.gq && p.lse != nullptr) p.lse[row0 + threadIdx.x] = -INFINITY;
+  }
+  return make_int4(-1, 0, 0, 0);
+}
+// {page, valid tokens} of entry j of unit u's list; a bad entry or page is
+// reported and has no tokens (page 0 is copied in its place, and not read).
+__device__ __forceinline__ int2 listed_block(const ListParams& p, int u, int b, int j, int len) {
+  const int at = p.blocks[(size_t)u * p.list_len + j];
+  if (at < 0 || at >= (len + kBlockTokens - 1) / kBlockTokens) {
+    report(p.dev_status, KVQ_DEV_BAD_PAGE);
+    return make_int2(0, 0);
+  }
+  const int page = p.page_table ? p.page_table[(size_t)b * p.max_blocks + at] : b * p.max_blocks + at;
+  if (page < 0 || page >= p.num_pages) {
+    report(p.dev_status, KVQ_DEV_BAD_PAGE);
+    return make_int2(0, 0);
+  }
+  return make_int2(page, min(kBlockTokens, len - at * kBlockTokens));
+}
+__device__ __forceinline__ uint16_t bf16_bits(float x) {
+  uint16_t r;
+  asm("cvt.rn.bf16.f32 %0, %1;" : "=h"(r) : "f"(x));
+  return r;
+}
+
 // NH: query heads per unit (4, or 8 with every KV block read once); they
 // come in quads of 4 -- one 16-column block (4 heads x 3 E4M3 or 2 BF16
 // parts) per quad of Q', S, P' and O.
-template <int BITS, bool KCW, bool VCW, int D, int G, bool BF16, int NH>
+// LISTED: the range is one of the unit's list of blocks (ListParams) instead
+// of one of its sequence; the CTA finds it by itself, without a plan.
+template <int BITS, bool KCW, bool VCW, int D, int G, bool BF16, int NH, bool LISTED = false>
 __global__ void __launch_bounds__(kThreads, gen_min_ctas(BITS, D, G, KCW, VCW, BF16, NH))
-decode_general_kernel(const GenParams p, int stages) {
+decode_general_kernel(const std::conditional_t<LISTED, ListParams, GenParams> p, int stages) {
   constexpr int kKBytes = kBlockTokens * D * BITS / 8;  // K (and V) codes of a block
   constexpr int kElems = BF16 ? 16 : 32;                // contraction elements per MMA
   constexpr int kCm = BF16 ? 256 : 128;                 // bytes of one B block per 8 rows
@@ -357,7 +399,8 @@ decode_general_kernel(const GenParams p, int stages) {
   float* red_z = red_m + 64;                                      // [2][32][4] per-group p (z) sums
   float* qsz_s = red_z + 256;  // [8][8] token-wise K q sums (NH = 8); channel-wise K, kMultSmem: the multipliers
   int* pend = reinterpret_cast<int*>(qsz_s + 64);                 // [4] block whose copy into stage s is in flight
-  uint64_t* bars = reinterpret_cast<uint64_t*>(qsz_s + 64 + 16);  // (12 spare words) stages [4], mma, drain
+  int* tokens = pend + 4;                                         // LISTED: [4] valid tokens of the block in stage s
+  uint64_t* bars = reinterpret_cast<uint64_t*>(qsz_s + 64 + 16);  // (8 spare words) stages [4], mma, drain
   uint32_t* tbase = reinterpret_cast<uint32_t*>(bars + 6);
   volatile int* fail = reinterpret_cast<volatile int*>(tbase + 1);  // a wait ran out (see cta_wait)
 
@@ -366,20 +409,34 @@ decode_general_kernel(const GenParams p, int stages) {
   const int cta = blockIdx.x;
   grid_dep_wait();    // the plan kernel's assignments (this kernel may start while it runs)
   grid_dep_launch();  // the merge kernel may launch (it waits for this grid to complete)
-  const int4 asg = p.assign[cta];  // written by general_plan_kernel: {b | unit << 16, j0, j1, length}
-  if (asg.x < 0) return;           // no work left for this CTA
-  const int b = asg.x & 0xffff, uh = asg.x >> 16, kvh = uh >> p.kv_shift;
+  int4 asg;
+  if constexpr (LISTED) asg = listed_range(p, cta);
+  else asg = p.assign[cta];  // written by general_plan_kernel: {b | unit << 16, j0, j1, length}
+  if (asg.x < 0) return;     // no work left for this CTA
+  const int b = LISTED ? asg.x / p.units_per_seq : asg.x & 0xffff;
+  const int uh = LISTED ? asg.x % p.units_per_seq : asg.x >> 16, kvh = uh >> p.kv_shift;
   const int j0 = asg.y, j1 = asg.z, len = asg.w;
   const size_t row0 = (size_t)b * p.num_q_heads + (size_t)uh * p.gq;  // first query head of the unit
   float* part_o = p.part_o + (size_t)cta * p.gq * D;  // this CTA's slot: [gq][D] and [gq]
   float* part_lse = p.part_lse + (size_t)cta * p.gq;
 
   const uint64_t limit = p.wait_limit_ns;
+  // LISTED: {page, valid tokens} of the block that this lane of the last warp
+  // copies next -- lane i takes the range's blocks i, i + 32, ... -- asked for
+  // 32 blocks ahead, as a list entry, a page id and a copy follow one another
+  int2 next = make_int2(0, 0);
   auto load = [&](int j, int s) {  // one thread: block j of the unit into stage s
-    int page = p.page_table ? p.page_table[(size_t)b * p.max_blocks + j] : b * p.max_blocks + j;
-    if (page < 0 || page >= p.num_pages) {
-      report(p.dev_status, KVQ_DEV_BAD_PAGE);
-      page = 0;
+    int page;
+    if constexpr (LISTED) {
+      page = next.x;
+      tokens[s] = next.y;
+      if (j + 32 < j1) next = listed_block(p, asg.x, b, j + 32, len);
+    } else {
+      page = p.page_table ? p.page_table[(size_t)b * p.max_blocks + j] : b * p.max_blocks + j;
+      if (page < 0 || page >= p.num_pages) {
+        report(p.dev_status, KVQ_DEV_BAD_PAGE);
+        page = 0;
+      }
     }
     const size_t blk = (size_t)page * p.num_kv_heads + kvh;
     unsigned char* st = smem + s * L.stage_bytes;
@@ -394,7 +451,12 @@ decode_general_kernel(const GenParams p, int stages) {
     bulk_g2s(sz + 3 * szb, p.v_zero + blk * NSZ, szb, &bars[s]);
     pend[s] = j;
   };
-  if (tid == 0) {  // the first copies go out before the rest of the set-up
+  // the thread that copies block j
+  auto loads = [&](int j) { return tid == (LISTED ? kRefillTid + ((j - j0) & 31) : kRefillTid); };
+  if (LISTED && tid >= kRefillTid && j0 + tid - kRefillTid < j1) {
+    if constexpr (LISTED) next = listed_block(p, asg.x, b, j0 + tid - kRefillTid, len);
+  }
+  if (tid == (LISTED ? kRefillTid : 0)) {  // the first copies go out before the rest of the set-up
     for (int i = 0; i < 4; ++i) pend[i] = -1;
     *fail = 0;
     for (int i = 0; i < stages; ++i) mbar_init(&bars[i], 1);
@@ -402,10 +464,15 @@ decode_general_kernel(const GenParams p, int stages) {
     mbar_init(&bars[stages], ((p.flags & KVQ_FLAG_TEST_STALL_MMA) && cta == 0) ? 2u : 1u);
     mbar_init(&bars[stages + 1], 1);
     fence_barrier_init();
-    for (int i = 0; i < stages && j0 + i < j1; ++i) {
+    for (int i = 0; !LISTED && i < stages && j0 + i < j1; ++i) {
       if (i == 0 && (p.flags & KVQ_FLAG_TEST_STALL) && blockIdx.x == 0) continue;  // test hook: withhold one block
       load(j0 + i, i);
     }
+  }
+  if (LISTED && warp == kThreads / 32 - 1) {
+    __syncwarp();  // the barriers are there
+    const int i = tid - kRefillTid;
+    if (i < stages && j0 + i < j1 && !(i == 0 && (p.flags & KVQ_FLAG_TEST_STALL) && blockIdx.x == 0)) load(j0 + i, i);
   }
 
   for (int i = tid; i < (L.scratch_off - L.q_off) / 16; i += kThreads)
@@ -543,7 +610,15 @@ decode_general_kernel(const GenParams p, int stages) {
     const uint16_t* kzz = ksz + NSZ;
     const uint16_t* vsz = kzz + NSZ;
     const uint16_t* vzz = vsz + NSZ;
-    const int nv = min(kBlockTokens, len - j * kBlockTokens);  // valid tokens of the block
+    const int nv = LISTED ? tokens[s] : min(kBlockTokens, len - j * kBlockTokens);  // valid tokens of the block
+    if (LISTED && nv <= 0) {  // a bad entry of the list: no tokens
+      __syncthreads();        // every thread has read that
+      if (loads(j + stages)) {
+        pend[s] = -1;
+        if (j + stages < j1) load(j + stages, s);
+      }
+      continue;
+    }
     const int l = tid;
     const bool valid = l < nv;
 
@@ -823,7 +898,7 @@ decode_general_kernel(const GenParams p, int stages) {
         }
         tc_commit(mma_bar);
       }
-      if (kEarlyRefill && pass == 0 && tid == kRefillTid) {  // nothing reads the stage after this barrier
+      if (kEarlyRefill && pass == 0 && loads(j + stages)) {  // nothing reads the stage after this barrier
         pend[s] = -1;
         if (j + stages < j1) load(j + stages, s);
       }
@@ -884,7 +959,7 @@ decode_general_kernel(const GenParams p, int stages) {
       tc_fence_before();
       __syncthreads();  // stage s, Q', P', S / O and the reduction buffers are free again
       if (*fail) { ok = false; break; }
-      if (tid == kRefillTid) {
+      if (loads(j + stages)) {
         pend[s] = -1;
         if (j + stages < j1) load(j + stages, s);
       }
@@ -930,13 +1005,29 @@ decode_general_kernel(const GenParams p, int stages) {
       if (c < D) {
 #pragma unroll
         for (int k = 0; k < NH; ++k)
-          if (k < p.gq) part_o[k * D + c] = (oacc[hf][k] + zacc[hf][k]) / l_run[k];
+          if (k < p.gq) {
+            float o = (oacc[hf][k] + zacc[hf][k]) / l_run[k];
+            if constexpr (LISTED) {
+              if (l_run[k] == 0.f) o = 0.f;  // every entry of the range was bad
+              if (p.splits == 1) p.out[(row0 + k) * D + c] = bf16_bits(o);
+              else part_o[k * D + c] = o;
+            } else {
+              part_o[k * D + c] = o;
+            }
+          }
       }
     }
 #pragma unroll
     for (int k = 0; k < NH; ++k)
-      if (tid == k && k < p.gq)
-        part_lse[k] = (m_run[k] + __log2f(l_run[k])) * 0.69314718055994530942f;
+      if (tid == k && k < p.gq) {
+        const float v = (m_run[k] + __log2f(l_run[k])) * 0.69314718055994530942f;
+        if constexpr (LISTED) {
+          if (p.splits > 1) part_lse[k] = v;
+          else if (p.lse != nullptr) p.lse[row0 + k] = v;
+        } else {
+          part_lse[k] = v;
+        }
+      }
   } else if (tid == 0) {
     report(p.dev_status, KVQ_DEV_TIMEOUT);
   }
@@ -957,9 +1048,9 @@ decode_general_kernel(const GenParams p, int stages) {
   }
 }
 
-template <int BITS, bool KCW, bool VCW, int D, int G, bool BF16, int NH>
-cudaError_t launch_instance(const GenParams& p, int grid, const GenLaunch& shape, cudaStream_t stream) {
-  auto kern = decode_general_kernel<BITS, KCW, VCW, D, G, BF16, NH>;
+template <int BITS, bool KCW, bool VCW, int D, int G, bool BF16, int NH, class Params>
+cudaError_t launch_instance(const Params& p, int grid, const GenLaunch& shape, cudaStream_t stream) {
+  auto kern = decode_general_kernel<BITS, KCW, VCW, D, G, BF16, NH, std::is_same<Params, ListParams>::value>;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)shape.smem);
   if (e != cudaSuccess) return e;
   // programmatic dependent launch: the CTAs start while the plan kernel runs
@@ -977,8 +1068,8 @@ cudaError_t launch_instance(const GenParams& p, int grid, const GenLaunch& shape
   return cudaLaunchKernelEx(&cfg, kern, p, (int)shape.stages);
 }
 
-template <int BITS, int D, int G, bool BF16, int NH>
-cudaError_t launch_schemes(bool kcw, bool vcw, const GenParams& p, int grid, const GenLaunch& shape, cudaStream_t s) {
+template <int BITS, int D, int G, bool BF16, int NH, class Params>
+cudaError_t launch_schemes(bool kcw, bool vcw, const Params& p, int grid, const GenLaunch& shape, cudaStream_t s) {
   if (!kcw && !vcw) return launch_instance<BITS, false, false, D, G, BF16, NH>(p, grid, shape, s);
   if (!kcw && vcw) return launch_instance<BITS, false, true, D, G, BF16, NH>(p, grid, shape, s);
   if (kcw && !vcw) return launch_instance<BITS, true, false, D, G, BF16, NH>(p, grid, shape, s);

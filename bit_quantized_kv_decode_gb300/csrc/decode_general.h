@@ -32,6 +32,29 @@ struct GenParams {
   uint32_t nibble_mul, minus_one;  // 2^28 and 2^32 - 1 (see DecodeParams)
 };
 
+// Attention over lists of blocks (sparse_decode.cu): unit u = sequence *
+// units_per_seq + KV head attends to entries [0, counts[u]) of blocks[u], which
+// are block numbers of the sequence.  A unit's list is cut into at most
+// `splits` ranges, one CTA and one part slot each; with one, the CTA writes the
+// output itself.
+struct ListParams : GenParams {
+  const int32_t* blocks;  // [units][list_len]
+  const int32_t* counts;  // [units]
+  uint16_t* out;          // bf16 [B][Hq][head_dim]
+  float* lse;             // [B][Hq] or null
+  int list_len, splits, head_dim;
+};
+// A unit's entries and its sequence's length; none where either is bad.
+struct ListedUnit {
+  int n, len;
+  bool bad;
+};
+__device__ __forceinline__ ListedUnit listed_unit(const ListParams& p, int u) {
+  const int len = p.seq_lens[u / p.units_per_seq], n = p.counts[u];
+  const bool bad = len < 0 || len > p.max_blocks * kBlockTokens || n < 0 || n > p.list_len;
+  return {bad ? 0 : n, bad ? 0 : len, bad};
+}
+
 // Byte offsets in shared memory and column offsets in tensor memory.
 //   tensor memory: [A: K codes, then V codes of the block][S and O]
 //   (the V codes replace the K codes once QK^T is done; O replaces S once

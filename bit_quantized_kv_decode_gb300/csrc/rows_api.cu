@@ -50,6 +50,52 @@ float scale_log2(float sm_scale, int head_dim) {
   return (sm_scale > 0.0f ? sm_scale : 1.0f / std::sqrt((float)head_dim)) * 1.4426950408889634f;
 }
 
+// The arguments of an append call, checked, as the kernels take them.
+kvq_status append_params(const kvq_cache_desc* cache, int32_t dtype, const kvq_rows* k, const kvq_rows* v, int32_t batch,
+                         int32_t total_tokens, const int32_t* cu_seqlens, const int32_t* seq_lens,
+                         const int32_t* page_table, int32_t max_blocks, const float* k_window, const float* v_window,
+                         float* k_window_out, float* v_window_out, uint8_t* k_codes, uint16_t* k_scale,
+                         uint16_t* k_zero, uint8_t* v_codes, uint16_t* v_scale, uint16_t* v_zero, uint32_t* dev_status,
+                         AppendParams* params) {
+  kvq_status s = check_cache(cache);
+  if (s != KVQ_OK) return s;
+  if (dtype != KVQ_BF16 && dtype != KVQ_FP16 && dtype != KVQ_FP32) return KVQ_ERR_INVALID_ARG;
+  if (batch < 1 || batch > 65535 || total_tokens < 0 || max_blocks < 1 || max_blocks > (1 << 23) ||
+      cache->num_kv_heads > 65535)
+    return KVQ_ERR_INVALID_ARG;
+  if (page_table == nullptr && (long long)batch * max_blocks > cache->num_pages) return KVQ_ERR_INVALID_ARG;
+  const int size = dtype == KVQ_FP32 ? 4 : 2;
+  if (total_tokens > 0 && (!rows_ok(k, size) || !rows_ok(v, size))) return KVQ_ERR_INVALID_ARG;
+  if (cu_seqlens == nullptr || seq_lens == nullptr) return KVQ_ERR_INVALID_ARG;
+  const void* ints[] = {cu_seqlens, seq_lens, page_table};
+  for (const void* ptr : ints)
+    if (!aligned4(ptr)) return KVQ_ERR_INVALID_ARG;
+  const void* arrays[] = {k_codes, k_scale, k_zero, v_codes, v_scale, v_zero};
+  for (const void* ptr : arrays)
+    if (ptr == nullptr || !aligned16(ptr)) return KVQ_ERR_INVALID_ARG;
+  const float* window[2] = {k_window, v_window};
+  float* window_out[2] = {k_window_out, v_window_out};
+  for (int i = 0; i < 2; ++i) {
+    if ((window[i] == nullptr) != (window_out[i] == nullptr)) return KVQ_ERR_INVALID_ARG;
+    if (window[i] == nullptr && (i ? cache->v_scheme : cache->k_scheme) == KVQ_CHANNELWISE) return KVQ_ERR_INVALID_ARG;
+    if (!aligned16(window[i]) || !aligned16(window_out[i])) return KVQ_ERR_INVALID_ARG;
+  }
+  AppendParams& p = *params;
+  p = AppendParams{};
+  if (total_tokens > 0) { p.x[0] = rows_of(k); p.x[1] = rows_of(v); }
+  p.dtype = dtype;
+  p.cu = cu_seqlens; p.seq_lens = seq_lens; p.page_table = page_table;
+  for (int i = 0; i < 2; ++i) { p.window[i] = window[i]; p.window_out[i] = window_out[i]; }
+  p.codes[0] = k_codes; p.scale[0] = k_scale; p.zero[0] = k_zero;
+  p.codes[1] = v_codes; p.scale[1] = v_scale; p.zero[1] = v_zero;
+  p.dev_status = dev_status; p.scheme[0] = cache->k_scheme; p.scheme[1] = cache->v_scheme;
+  p.bits = cache->bits; p.head_dim = cache->head_dim; p.group = group_of(cache);
+  p.num_kv_heads = cache->num_kv_heads; p.num_pages = cache->num_pages; p.max_blocks = max_blocks;
+  p.batch = batch; p.total = total_tokens;
+  p.most = (long long)max_blocks * kBlockTokens;
+  return KVQ_OK;
+}
+
 }  // namespace
 }  // namespace kvq
 
@@ -88,43 +134,48 @@ KVQ_API kvq_status kvq_append_chunk(const kvq_cache_desc* cache, int32_t dtype, 
                                     float* v_window_out, uint8_t* k_codes, uint16_t* k_scale, uint16_t* k_zero,
                                     uint8_t* v_codes, uint16_t* v_scale, uint16_t* v_zero, uint32_t* dev_status,
                                     void* stream) {
-  kvq_status s = check_cache(cache);
+  AppendParams p;
+  kvq_status s = append_params(cache, dtype, k, v, batch, total_tokens, cu_seqlens, seq_lens, page_table, max_blocks,
+                               k_window, v_window, k_window_out, v_window_out, k_codes, k_scale, k_zero, v_codes,
+                               v_scale, v_zero, dev_status, &p);
+  if (s == KVQ_OK) s = check_device(nullptr);
   if (s != KVQ_OK) return s;
-  if (dtype != KVQ_BF16 && dtype != KVQ_FP16 && dtype != KVQ_FP32) return KVQ_ERR_INVALID_ARG;
-  if (batch < 1 || batch > 65535 || total_tokens < 0 || max_blocks < 1 || max_blocks > (1 << 23) ||
-      cache->num_kv_heads > 65535)
+  return launch_append_chunk(p, static_cast<cudaStream_t>(stream)) == cudaSuccess ? KVQ_OK : KVQ_ERR_CUDA;
+}
+
+KVQ_API kvq_status kvq_append_rotary(const kvq_cache_desc* cache, int32_t dtype, const kvq_rotary* rotary,
+                                     const kvq_rows* q, int32_t num_q_heads, const kvq_rows* k, const kvq_rows* v,
+                                     int32_t batch, int32_t total_tokens, const int32_t* cu_seqlens,
+                                     const int32_t* seq_lens, const int32_t* page_table, int32_t max_blocks,
+                                     const float* k_window, const float* v_window, float* k_window_out,
+                                     float* v_window_out, uint8_t* k_codes, uint16_t* k_scale, uint16_t* k_zero,
+                                     uint8_t* v_codes, uint16_t* v_scale, uint16_t* v_zero, void* q_out, void* k_out,
+                                     uint32_t* dev_status, void* stream) {
+  AppendParams p;
+  kvq_status s = append_params(cache, dtype, k, v, batch, total_tokens, cu_seqlens, seq_lens, page_table, max_blocks,
+                               k_window, v_window, k_window_out, v_window_out, k_codes, k_scale, k_zero, v_codes,
+                               v_scale, v_zero, dev_status, &p);
+  if (s != KVQ_OK) return s;
+  if (rotary == nullptr || rotary->angles == nullptr || !aligned16(rotary->angles) || rotary->positions < 1 ||
+      (rotary->interleaved != 0 && rotary->interleaved != 1))
     return KVQ_ERR_INVALID_ARG;
-  if (page_table == nullptr && (long long)batch * max_blocks > cache->num_pages) return KVQ_ERR_INVALID_ARG;
-  const int size = dtype == KVQ_FP32 ? 4 : 2;
-  if (total_tokens > 0 && (!rows_ok(k, size) || !rows_ok(v, size))) return KVQ_ERR_INVALID_ARG;
-  if (cu_seqlens == nullptr || seq_lens == nullptr) return KVQ_ERR_INVALID_ARG;
-  const void* ints[] = {cu_seqlens, seq_lens, page_table};
-  for (const void* ptr : ints)
-    if (!aligned4(ptr)) return KVQ_ERR_INVALID_ARG;
-  const void* arrays[] = {k_codes, k_scale, k_zero, v_codes, v_scale, v_zero};
-  for (const void* ptr : arrays)
-    if (ptr == nullptr || !aligned16(ptr)) return KVQ_ERR_INVALID_ARG;
-  const float* window[2] = {k_window, v_window};
-  float* window_out[2] = {k_window_out, v_window_out};
-  for (int i = 0; i < 2; ++i) {
-    if ((window[i] == nullptr) != (window_out[i] == nullptr)) return KVQ_ERR_INVALID_ARG;
-    if (window[i] == nullptr && (i ? cache->v_scheme : cache->k_scheme) == KVQ_CHANNELWISE) return KVQ_ERR_INVALID_ARG;
-    if (!aligned16(window[i]) || !aligned16(window_out[i])) return KVQ_ERR_INVALID_ARG;
-  }
+  if (rotary->dim < 16 || rotary->dim % 16 != 0 || rotary->dim > cache->head_dim) return KVQ_ERR_UNSUPPORTED;
+  const bool queries = q != nullptr && total_tokens > 0;
+  if ((q != nullptr) != (q_out != nullptr) && total_tokens > 0) return KVQ_ERR_INVALID_ARG;
+  if (queries && (!rows_ok(q, dtype == KVQ_FP32 ? 4 : 2) || num_q_heads < 1 || num_q_heads > 65535)) return KVQ_ERR_INVALID_ARG;
+  if (!aligned16(q_out) || !aligned16(k_out)) return KVQ_ERR_INVALID_ARG;
   s = check_device(nullptr);
   if (s != KVQ_OK) return s;
-  AppendParams p{};
-  if (total_tokens > 0) { p.x[0] = rows_of(k); p.x[1] = rows_of(v); }
-  p.dtype = dtype;
-  p.cu = cu_seqlens; p.seq_lens = seq_lens; p.page_table = page_table;
-  for (int i = 0; i < 2; ++i) { p.window[i] = window[i]; p.window_out[i] = window_out[i]; }
-  p.codes[0] = k_codes; p.scale[0] = k_scale; p.zero[0] = k_zero;
-  p.codes[1] = v_codes; p.scale[1] = v_scale; p.zero[1] = v_zero;
-  p.dev_status = dev_status; p.scheme[0] = cache->k_scheme; p.scheme[1] = cache->v_scheme;
-  p.bits = cache->bits; p.head_dim = cache->head_dim; p.group = group_of(cache);
-  p.num_kv_heads = cache->num_kv_heads; p.num_pages = cache->num_pages; p.max_blocks = max_blocks;
-  p.batch = batch; p.total = total_tokens;
-  return launch_append_chunk(p, static_cast<cudaStream_t>(stream)) == cudaSuccess ? KVQ_OK : KVQ_ERR_CUDA;
+  p.turn = Turn{rotary->angles, rotary->dim, rotary->interleaved};
+  if (rotary->positions < p.most) p.most = rotary->positions;
+  TurnRowsParams t{};
+  if (queries) { t.x[0] = rows_of(q); t.out[0] = q_out; t.heads[0] = num_q_heads; }
+  if (k_out != nullptr) { t.x[1] = p.x[0]; t.out[1] = k_out; t.heads[1] = p.num_kv_heads; }
+  t.dtype = dtype; t.head_dim = p.head_dim; t.batch = batch; t.total = total_tokens;
+  t.cu = cu_seqlens; t.seq_lens = seq_lens; t.most = p.most; t.turn = p.turn;
+  const cudaStream_t st = static_cast<cudaStream_t>(stream);
+  if (launch_append_rotary(p, st) != cudaSuccess) return KVQ_ERR_CUDA;
+  return launch_turn_rows(t, st) == cudaSuccess ? KVQ_OK : KVQ_ERR_CUDA;
 }
 
 KVQ_API kvq_status kvq_chunk_workspace_size(const kvq_chunk_desc* d, size_t* bytes) {

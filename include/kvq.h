@@ -19,8 +19,13 @@
  * lse[b, h] = ln sum_l exp(S_l), with x_hat = s * code + z and code unsigned.
  *
  * Before and between decode steps: attention over whole prompts
- * (kvq_prompt_attn), their rows quantised into the cache (kvq_append_chunk),
- * and attention of a chunk of new tokens over it (kvq_chunk_attn).
+ * (kvq_prompt_attn), their rows quantised into the cache (kvq_append_chunk,
+ * kvq_append_rotary with the position rotation on the way), and attention of a
+ * chunk of new tokens over it (kvq_chunk_attn).
+ *
+ * Decode steps over long caches: the blocks that a query may look at
+ * (kvq_select_blocks) and decode attention over them alone
+ * (kvq_sparse_decode_attn).
  *
  * Cache format (this library's; the pages leave it open)
  * -------------------------------------------------------
@@ -175,6 +180,39 @@ typedef struct kvq_chunk_desc {
   float sm_scale;       /* <= 0 selects 1/sqrt(head_dim) */
   uint32_t flags;       /* 0 or KVQ_FLAG_TEST_STALL */
 } kvq_chunk_desc;
+
+/* Rotation of the first `dim` channels of a row by its position p
+ * (kvq_append_rotary): pairs (x1, x2), channel i with i + dim / 2 or 2 i with
+ * 2 i + 1, become (x1 cos a - x2 sin a, x2 cos a + x1 sin a), a the angle of
+ * pair i at p. */
+typedef struct kvq_rotary {
+  const float* angles; /* fp32 [positions][dim]: cos of the dim / 2 angles, then their sin; 16-byte aligned */
+  int32_t positions;
+  int32_t dim;         /* a multiple of 16, at most head_dim */
+  int32_t interleaved; /* 0: pairs (i, i + dim / 2); 1: (2 i, 2 i + 1) */
+} kvq_rotary;
+
+/* Selection of blocks (kvq_select_blocks). */
+typedef struct kvq_select_desc {
+  kvq_cache_desc cache; /* k_scheme: KVQ_CHANNELWISE */
+  int32_t batch;        /* sequences, 1 to 65535 */
+  int32_t num_q_heads;  /* 1, 2, 4 or 8 times num_kv_heads */
+  int32_t max_blocks;   /* page_table row length, at most 16384; contiguous: blocks per sequence */
+  int32_t budget;       /* blocks of a list, first and last among them */
+  int32_t first;        /* leading blocks of a sequence that every list has */
+  int32_t last;         /* ... and trailing ones */
+} kvq_select_desc;
+
+/* Decode attention over lists of blocks (kvq_sparse_decode_attn). */
+typedef struct kvq_sparse_desc {
+  kvq_cache_desc cache;
+  int32_t batch;       /* sequences, 1 to 65535 */
+  int32_t num_q_heads; /* 1, 2, 4 or 8 times num_kv_heads */
+  int32_t max_blocks;  /* page_table row length; contiguous: blocks per sequence */
+  int32_t list_len;    /* entries of a list's row */
+  float sm_scale;      /* <= 0 selects 1/sqrt(head_dim) */
+  uint32_t flags;      /* 0 or KVQ_FLAG_TEST_STALL, KVQ_FLAG_TEST_STALL_MMA */
+} kvq_sparse_desc;
 
 /* Human-readable name of a status code (static storage). */
 KVQ_API const char* kvq_status_string(kvq_status status);
@@ -412,6 +450,34 @@ KVQ_API kvq_status kvq_append_chunk(const kvq_cache_desc* cache, int32_t dtype, 
                                     uint8_t* v_codes, uint16_t* v_scale, uint16_t* v_zero, uint32_t* dev_status,
                                     void* stream);
 
+/*
+ * kvq_append_chunk with K's rows turned by their positions on the way: row
+ * cu_seqlens[b] + i is the token at position p = seq_lens[b] + i.  The turned
+ * values are fp32 -- fl(fl(x1 c) - fl(x2 s)), fl(fl(x2 c) + fl(x1 s)), no fused
+ * products -- and are quantised as they are: the cache and K's window equal
+ * what kvq_append_chunk makes of fp32 rows turned so (the window holds turned
+ * rows).  V is appended as it is.
+ * Queries of the same tokens are turned beside it, and keys where an attention
+ * over rows follows, both rounded once to the rows' type:
+ *   q          rows [total_tokens][num_q_heads][head_dim] of type dtype, or
+ *              NULL (then q_out is NULL; num_q_heads is ignored)
+ *   q_out      [total_tokens][num_q_heads][head_dim] of type dtype, contiguous,
+ *              16-byte aligned, apart from every other array
+ *   k_out      the same with num_kv_heads, or NULL
+ * Rows outside every sequence, and those of a sequence that is skipped, are
+ * left as they were.  Other arguments and device errors as kvq_append_chunk; a
+ * sequence that reaches past rotary->positions is skipped with
+ * KVQ_DEV_BAD_SEQ_LEN.
+ */
+KVQ_API kvq_status kvq_append_rotary(const kvq_cache_desc* cache, int32_t dtype, const kvq_rotary* rotary,
+                                     const kvq_rows* q, int32_t num_q_heads, const kvq_rows* k, const kvq_rows* v,
+                                     int32_t batch, int32_t total_tokens, const int32_t* cu_seqlens,
+                                     const int32_t* seq_lens, const int32_t* page_table, int32_t max_blocks,
+                                     const float* k_window, const float* v_window, float* k_window_out,
+                                     float* v_window_out, uint8_t* k_codes, uint16_t* k_scale, uint16_t* k_zero,
+                                     uint8_t* v_codes, uint16_t* v_scale, uint16_t* v_zero, void* q_out, void* k_out,
+                                     uint32_t* dev_status, void* stream);
+
 /* Workspace bytes kvq_chunk_attn needs for `desc` (host only, no device
  * needed): 20 or 40 MB, set by the cache's geometry alone, so that one buffer
  * serves calls of any batch, number of tokens and heads. */
@@ -454,6 +520,66 @@ KVQ_API kvq_status kvq_chunk_attn(const kvq_chunk_desc* desc, const kvq_rows* q,
                                   const uint16_t* v_scale, const uint16_t* v_zero, const int32_t* cu_seqlens,
                                   const int32_t* seq_lens, const int32_t* page_table, void* out, float* lse,
                                   void* workspace, size_t workspace_bytes, uint32_t* dev_status, void* stream);
+
+/*
+ * The blocks that the queries of a decode step may look at, for every sequence
+ * and KV head, from the cache's scales and offsets alone.  K is channel-wise:
+ * channel c of token group g holds values in [z_gc, z_gc + m s_gc], m = 2^bits
+ * - 1, so that no token of the group scores more than
+ *   sum_h max_{k in that box} q_h . k = sum_c (Q_c z_gc + m P_c s_gc),
+ *   Q = sum_h q_h,  P = sum_h max(q_h, 0)   (h: the query heads of the KV head)
+ * summed over the heads.  A block's score is the largest of its groups that
+ * have a token; one that is not a number counts as minus infinity, as does a
+ * bad page.  The list holds the first `first` and the last `last` blocks of the
+ * sequence and the others with the largest scores, `budget` in all (every block
+ * where the sequence has no more), in ascending order.  Scores are compared as
+ * if computed without rounding (to fp64's); of equal ones the lowest index is
+ * taken.
+ *   q          bf16 [batch][num_q_heads][head_dim], 16-byte aligned
+ *   seq_lens   int32 [batch], each in [0, max_blocks * 128]
+ *   page_table int32 [batch][max_blocks] or NULL (contiguous)
+ *   blocks     int32 [batch][num_kv_heads][budget]: block numbers of the
+ *              sequence, -1 behind the last
+ *   counts     int32 [batch][num_kv_heads]
+ * Token-wise K (whose scales say nothing of single channels) and max_blocks >
+ * 16384: KVQ_ERR_UNSUPPORTED.  first + last > budget: KVQ_ERR_INVALID_ARG.
+ * Device errors: KVQ_DEV_BAD_SEQ_LEN (empty lists), KVQ_DEV_BAD_PAGE.
+ */
+KVQ_API kvq_status kvq_select_blocks(const kvq_select_desc* desc, const uint16_t* q, const uint16_t* k_scale,
+                                     const uint16_t* k_zero, const int32_t* seq_lens, const int32_t* page_table,
+                                     int32_t* blocks, int32_t* counts, uint32_t* dev_status, void* stream);
+
+/* Workspace bytes kvq_sparse_decode_attn needs for `desc` (host only, no device
+ * needed; may be 0). */
+KVQ_API kvq_status kvq_sparse_workspace_size(const kvq_sparse_desc* desc, size_t* bytes);
+
+/*
+ * Decode attention over lists of blocks, one list per sequence and KV head: the
+ * query heads of KV head h of sequence b attend to the tokens of the blocks
+ * blocks[b][h][0 .. counts[b][h] - 1] of the sequence, the tokens at or past
+ * its length left out.  Entries may stand in any order; a block that is listed
+ * twice counts twice.  Computed as kvq_decode_attn with KVQ_OPERANDS_FP8.
+ *   q          bf16 [batch][num_q_heads][head_dim]
+ *   seq_lens   int32 [batch], each in [0, max_blocks * 128]
+ *   page_table int32 [batch][max_blocks] or NULL (contiguous)
+ *   blocks     int32 [batch][num_kv_heads][list_len]
+ *   counts     int32 [batch][num_kv_heads], each in [0, list_len]
+ *   out        bf16 [batch][num_q_heads][head_dim], rounded once; nothing to
+ *              attend to: 0
+ *   lse        fp32 [batch][num_q_heads] (nothing to attend to: -inf), or NULL
+ *   workspace  >= kvq_sparse_workspace_size bytes, 256-byte aligned (NULL where
+ *              that is 0); needs no initialisation; concurrent calls need
+ *              separate workspaces
+ * Device errors: KVQ_DEV_BAD_SEQ_LEN (a bad length or count: nothing to attend
+ * to), KVQ_DEV_BAD_PAGE (an entry that is no block of the sequence, or a bad
+ * page: that entry has no tokens), KVQ_DEV_TIMEOUT.
+ */
+KVQ_API kvq_status kvq_sparse_decode_attn(const kvq_sparse_desc* desc, const uint16_t* q, const uint8_t* k_codes,
+                                          const uint16_t* k_scale, const uint16_t* k_zero, const uint8_t* v_codes,
+                                          const uint16_t* v_scale, const uint16_t* v_zero, const int32_t* seq_lens,
+                                          const int32_t* page_table, const int32_t* blocks, const int32_t* counts,
+                                          uint16_t* out, float* lse, void* workspace, size_t workspace_bytes,
+                                          uint32_t* dev_status, void* stream);
 
 #ifdef __cplusplus
 }
