@@ -8,7 +8,7 @@ computation runs in the library's CUDA kernels; there is no other code path.
 from __future__ import annotations
 
 import ctypes
-from typing import NamedTuple, Optional, Tuple
+from typing import Optional, Tuple
 
 import torch
 from torch.autograd import forward_ad
@@ -445,17 +445,12 @@ def _windows_apart(kw, kwo, vw, vwo, size: int, kr: Rows, vr: Rows, T: int, H: i
                 raise ValueError("a window overlaps the rows that are read")
 
 
-class _AppendArgs(NamedTuple):
-    device: int
-    rows: tuple    # element type, K rows, V rows, batch, tokens
-    places: tuple  # row offsets, lengths, page table, blocks per sequence
-    arrays: tuple  # windows and their outputs, the K cache, the V cache
-    status: Optional[int]
-
-
 def _append_args(desc, k_new, v_new, cu_seqlens, seq_lens, k_cache, v_cache, k_window, v_window, page_table, max_blocks,
-                 k_window_out, v_window_out, dev_status, what) -> _AppendArgs:
-    """The arguments of an append call, checked, as the library takes them."""
+                 k_window_out, v_window_out, dev_status, what):
+    """The arguments of an append call, checked, as the library takes them: the
+    device, the K and the V rows, and a tuple of batch, tokens, row offsets,
+    lengths, page table, blocks per sequence, windows and their outputs, the K
+    cache, the V cache, the status word."""
     H, D = desc.num_kv_heads, desc.head_dim
     kr = _rows(k_new, "k_new", _DTYPES, None, H, D)
     T = k_new.shape[0]
@@ -480,10 +475,9 @@ def _append_args(desc, k_new, v_new, cu_seqlens, seq_lens, k_cache, v_cache, k_w
     kw, kwo, vw, vwo = windows
     if kw or vw:
         _windows_apart(kw, kwo, vw, vwo, size * 4, kr, vr, T, H, D, k_new.element_size())
-    return _AppendArgs(dev, (_DTYPES[k_new.dtype], kr, vr, B, T),
-                       (pcu, _ptr(seq_lens, "seq_lens", (torch.int32,), B, dev), pt, mb),
-                       (kw, vw, kwo, vwo, *_cache_ptrs(desc, "k_cache", k_cache, dev),
-                        *_cache_ptrs(desc, "v_cache", v_cache, dev)), _ptr(dev_status, "dev_status", _STATUS, 1, dev))
+    return dev, kr, vr, (B, T, pcu, _ptr(seq_lens, "seq_lens", (torch.int32,), B, dev), pt, mb, kw, vw, kwo, vwo,
+                         *_cache_ptrs(desc, "k_cache", k_cache, dev), *_cache_ptrs(desc, "v_cache", v_cache, dev)), \
+        _ptr(dev_status, "dev_status", _STATUS, 1, dev)
 
 
 def append_chunk(desc: CacheDesc, k_new: torch.Tensor, v_new: torch.Tensor, cu_seqlens: torch.Tensor,
@@ -500,10 +494,10 @@ def append_chunk(desc: CacheDesc, k_new: torch.Tensor, v_new: torch.Tensor, cu_s
     must not follow inside a block written so: it quantises the whole block from
     its window (chunks of one row do not).  The caller advances seq_lens
     afterwards.  Returns (k_cache, v_cache)."""
-    a = _append_args(desc, k_new, v_new, cu_seqlens, seq_lens, k_cache, v_cache, k_window, v_window, page_table, max_blocks,
-                     k_window_out, v_window_out, dev_status, "append_chunk")
-    _launch(a.device, "kvq_append_chunk", library().kvq_append_chunk, ctypes.byref(desc), *a.rows, *a.places, *a.arrays,
-            a.status)
+    dev, kr, vr, rest, status = _append_args(desc, k_new, v_new, cu_seqlens, seq_lens, k_cache, v_cache, k_window, v_window,
+                                             page_table, max_blocks, k_window_out, v_window_out, dev_status, "append_chunk")
+    _launch(dev, "kvq_append_chunk", library().kvq_append_chunk, ctypes.byref(desc), _DTYPES[k_new.dtype], ctypes.byref(kr),
+            ctypes.byref(vr), *rest, status)
     return k_cache, v_cache
 
 
@@ -602,16 +596,17 @@ def append_rotary(desc: CacheDesc, table: torch.Tensor, k_new: torch.Tensor, v_n
     tokens and type, the turned queries are returned (q_out, made when not
     given), else None; with k_out [T, Hkv, head_dim] the turned keys are written
     there too, for prompt_attn.  Both are rounded once to the rows' type."""
-    a = _append_args(desc, k_new, v_new, cu_seqlens, seq_lens, k_cache, v_cache, k_window, v_window, page_table, max_blocks,
-                     k_window_out, v_window_out, dev_status, "append_rotary")
-    dev, D, H = a.device, desc.head_dim, desc.num_kv_heads
+    dev, kr, vr, rest, status = _append_args(desc, k_new, v_new, cu_seqlens, seq_lens, k_cache, v_cache, k_window, v_window,
+                                             page_table, max_blocks, k_window_out, v_window_out, dev_status, "append_rotary")
     if not isinstance(table, torch.Tensor) or table.dim() != 2:
         raise ValueError("table must be fp32 [positions, rotated channels]")
     positions, dim = table.shape
     rotary = _lib.Rotary(_ptr(table, "table", (torch.float32,), positions * dim, dev), positions, dim,
                          1 if interleaved else 0)
-    dtype, T, size = (k_new.dtype,), a.rows[4], k_new.element_size()
+    T, H, D = k_new.shape
+    dtype = (k_new.dtype,)
     qr, Hq, pq, pk = None, 0, None, None
+    written = []
     if q is not None:
         qr = _rows(q, "q", dtype, T, None, D)
         Hq = q.shape[1]
@@ -619,21 +614,26 @@ def append_rotary(desc: CacheDesc, table: torch.Tensor, k_new: torch.Tensor, v_n
             raise ValueError(f"q is on {q.device}, k_new on {k_new.device}")
         if q_out is None:
             q_out = q.new_empty(T, Hq, D)
-        pq = _ptr(q_out, "q_out", dtype, T * Hq * D, dev)
+            pq = q_out.data_ptr()
+        else:
+            pq = _ptr(q_out, "q_out", dtype, T * Hq * D, dev)
+            written.append(("q_out", q_out))
     elif q_out is not None:
         raise ValueError("q_out without q")
     if k_out is not None:
         pk = _ptr(k_out, "k_out", dtype, T * H * D, dev)
-    if T and (pq or pk):
-        others = [_rows_span(r, T, h, D, size) for r, h in ((a.rows[1], H), (a.rows[2], H), (qr, Hq)) if r is not None]
+        written.append(("k_out", k_out))
+    if T and written:
+        size = k_new.element_size()
+        others = [_rows_span(r, T, h, D, size) for r, h in ((kr, H), (vr, H), (qr, Hq)) if r is not None]
         others += [_span(t) for t in (k_window, v_window, k_window_out, v_window_out, table, cu_seqlens, seq_lens, page_table,
-                                      *k_cache, *v_cache) if t is not None]
-        for name, t in (("q_out", q_out), ("k_out", k_out)):
-            if t is not None:
-                _disjoint(name, _span(t), others)
-                others.append(_span(t))
-    _launch(dev, "kvq_append_rotary", library().kvq_append_rotary, ctypes.byref(desc), a.rows[0], ctypes.byref(rotary),
-            None if qr is None else ctypes.byref(qr), Hq, *a.rows[1:], *a.places, *a.arrays, pq, pk, a.status)
+                                      dev_status, *k_cache, *v_cache) if t is not None]
+        for name, t in written:
+            _disjoint(name, _span(t), others)
+            others.append(_span(t))
+    _launch(dev, "kvq_append_rotary", library().kvq_append_rotary, ctypes.byref(desc), _DTYPES[k_new.dtype],
+            ctypes.byref(rotary), None if qr is None else ctypes.byref(qr), Hq, ctypes.byref(kr), ctypes.byref(vr), *rest, pq,
+            pk, status)
     return q_out
 
 
@@ -714,32 +714,37 @@ def sparse_decode_attn(desc: CacheDesc, q: torch.Tensor, k_cache, v_cache, seq_l
     pb, pc = _ptr(blocks, "blocks", (torch.int32,), B * H * n, dev), _ptr(counts, "counts", (torch.int32,), B * H, dev)
     d = _lib.SparseDesc(desc, B, Hq, mb, n, sm_scale, flags)
     need = _sparse_bytes(d)
-    written = []
+    pq, pn = q.data_ptr(), _ptr(seq_lens, "seq_lens", (torch.int32,), B, dev)
+    spans = []  # what the caller gave to be written
     if out is None:
         out = torch.empty_like(q)
+        po = out.data_ptr()
     else:
-        written.append(("out", out))
+        po = _ptr(out, "out", (q.dtype,), B * Hq * D, dev)
+        spans.append(("out", (po, po + B * Hq * D * 2)))
     if lse is None:
         lse = torch.empty(B, Hq, dtype=torch.float32, device=q.device) if return_lse else None
+        pl = None if lse is None else lse.data_ptr()
     else:
-        written.append(("lse", lse))
-    size = need
+        pl = _ptr(lse, "lse", (torch.float32,), B * Hq, dev)
+        spans.append(("lse", (pl, pl + B * Hq * 4)))
     if workspace is None:
-        workspace = torch.empty(need, dtype=torch.uint8, device=q.device) if need else None
-        pw = workspace.data_ptr() if need else None
+        size, pw = need, None
+        if need:
+            workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
+            pw = workspace.data_ptr()
     else:
         size = workspace.numel()
         pw = _ptr(workspace, "workspace", (torch.uint8,), size, dev)
-    po, pl = _ptr(out, "out", (q.dtype,), B * Hq * D, dev), _ptr(lse, "lse", (torch.float32,), B * Hq, dev)
-    spans = [(name, _span(t)) for name, t in written]
-    if need and size >= need:
-        spans.append(("workspace", (pw, pw + need)))  # (of a longer one, the first bytes are used)
+        if size >= need > 0:
+            spans.append(("workspace", (pw, pw + need)))  # (of a longer one, the first bytes are used)
     if spans:
-        others = [_span(t) for t in (q, blocks, counts, seq_lens, page_table) if t is not None]
+        others = [(pq, pq + B * Hq * D * 2), (pb, pb + B * H * n * 4), (pc, pc + B * H * 4), (pn, pn + B * 4)]
+        if pt:
+            others.append((pt, pt + B * mb * 4))
         for name, span in spans:
             _disjoint(name, span, others)
             others.append(span)
-    _launch(dev, "kvq_sparse_decode_attn", library().kvq_sparse_decode_attn, ctypes.byref(d), pq, *kc, *vc,
-            _ptr(seq_lens, "seq_lens", (torch.int32,), B, dev), pt, pb, pc, po, pl, pw, size,
-            _ptr(dev_status, "dev_status", _STATUS, 1, dev))
+    _launch(dev, "kvq_sparse_decode_attn", library().kvq_sparse_decode_attn, ctypes.byref(d), pq, *kc, *vc, pn, pt, pb, pc, po,
+            pl, pw, size, _ptr(dev_status, "dev_status", _STATUS, 1, dev))
     return out if lse is None else (out, lse)

@@ -44,6 +44,12 @@ namespace kvq {
 namespace {
 
 template <typename T, int BITS, int W>
+__global__ void __launch_bounds__(32 * kBlockWarps, kBlockCtas) append_blocks_kernel(const AppendParams p) {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // the edges' kernel runs beside this one
+  append_block<T, BITS, W>(p, blockIdx.z & 1, blockIdx.z >> 1);
+}
+
+template <typename T, int BITS, int W>
 cudaError_t launch_w(const AppendParams& p, cudaStream_t stream) {
   constexpr bool kHalf = sizeof(Raw<T>) == 8;
   const unsigned heads = (unsigned)p.num_kv_heads, planes = (unsigned)(2 * (p.head_dim / W));

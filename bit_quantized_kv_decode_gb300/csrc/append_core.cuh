@@ -665,10 +665,8 @@ __device__ __forceinline__ void reduce_group2(uint32_t (&v)[N], int lg) {
   for (; o > 0; o >>= 1) v[0] = min2<T>(v[0], __shfl_xor_sync(0xffffffffu, v[0], o));
 }
 
-// (four CTAs to an SM: 64 registers, two of them spilled at 4 bits, and still
-// 8% faster than three with 80, as their loads and barriers overlap better)
 template <typename T, int BITS, int W>
-__global__ void __launch_bounds__(32 * kBlockWarps, 4) append_blocks_kernel(const AppendParams p) {
+__device__ __forceinline__ void append_block(const AppendParams& p, int which, int slab) {
   constexpr int kWarps = kBlockWarps, kThreads = 32 * kWarps, kWarpTok = kBlockTokens / kWarps;  // tokens of a warp
   constexpr int kLanes = W / 4, kTok = kWarpTok * kLanes / 32, kPer = 128 / BITS;
   constexpr int kPieces = W * BITS;
@@ -683,9 +681,8 @@ __global__ void __launch_bounds__(32 * kBlockWarps, 4) append_blocks_kernel(cons
   __shared__ __align__(16) float ranges[2][kWarps][W];
   __shared__ __align__(16) uint16_t s_out[128 * 4], z_out[128 * 4];
   __shared__ int found[2];
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // the edges' kernel runs beside this one
   const int D = p.head_dim;
-  const int h = blockIdx.y, which = blockIdx.z & 1, slab = blockIdx.z >> 1;
+  const int h = blockIdx.y;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   if (warp == 0) find_block<kWhole, 0>(p, blockIdx.x, found);
   __syncthreads();
@@ -852,6 +849,11 @@ __global__ void __launch_bounds__(32 * kBlockWarps, 4) append_blocks_kernel(cons
     zo[at] = z_out[e];
   }
 }
+
+// Four CTAs of 256 threads to an SM: 64 registers, two of them spilled at 4
+// bits, and still 8% faster than three with 80, as their loads and barriers
+// overlap better.
+constexpr int kBlockCtas = 4;
 
 }  // namespace
 }  // namespace kvq

@@ -68,12 +68,11 @@ struct AppendParams {
   Turn turn;       // append_rotary: K's
 };
 cudaError_t launch_append_chunk(const AppendParams& p, cudaStream_t stream);
-cudaError_t launch_append_rotary(const AppendParams& p, cudaStream_t stream);
 
 // Rows turned by their positions and written as rows of the same type
 // (append_rotary.cu): queries, and keys where an attention over rows follows.
 struct TurnRowsParams {
-  Rows x[2];    // q, k
+  Rows x[2];     // q, k
   void* out[2];  // [total][heads][head_dim]
   int heads[2];  // 0: none
   int dtype, head_dim, batch, total;
@@ -82,6 +81,6 @@ struct TurnRowsParams {
   long long most;
   Turn turn;
 };
-cudaError_t launch_turn_rows(const TurnRowsParams& p, cudaStream_t stream);
+cudaError_t launch_append_rotary(const AppendParams& p, const TurnRowsParams& rows, cudaStream_t stream);
 
 }  // namespace kvq

@@ -173,9 +173,7 @@ KVQ_API kvq_status kvq_append_rotary(const kvq_cache_desc* cache, int32_t dtype,
   if (k_out != nullptr) { t.x[1] = p.x[0]; t.out[1] = k_out; t.heads[1] = p.num_kv_heads; }
   t.dtype = dtype; t.head_dim = p.head_dim; t.batch = batch; t.total = total_tokens;
   t.cu = cu_seqlens; t.seq_lens = seq_lens; t.most = p.most; t.turn = p.turn;
-  const cudaStream_t st = static_cast<cudaStream_t>(stream);
-  if (launch_append_rotary(p, st) != cudaSuccess) return KVQ_ERR_CUDA;
-  return launch_turn_rows(t, st) == cudaSuccess ? KVQ_OK : KVQ_ERR_CUDA;
+  return launch_append_rotary(p, t, static_cast<cudaStream_t>(stream)) == cudaSuccess ? KVQ_OK : KVQ_ERR_CUDA;
 }
 
 KVQ_API kvq_status kvq_chunk_workspace_size(const kvq_chunk_desc* d, size_t* bytes) {

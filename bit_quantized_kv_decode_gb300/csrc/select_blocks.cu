@@ -54,9 +54,6 @@ __host__ __device__ constexpr int keys_room(int max_blocks) { return (max_blocks
 __host__ __device__ constexpr size_t copies_at(int max_blocks) {
   return ((size_t)keys_room(max_blocks) + (max_blocks + 127) / 128 * 4) * 4;
 }
-__device__ __forceinline__ void copy16(void* dst_smem, const void* src) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(dst_smem)), "l"(src) : "memory");
-}
 
 // The larger of each half of two fp16 pairs, NaN if either is.
 __device__ __forceinline__ uint32_t max_nan_2(uint32_t a, uint32_t b) {
@@ -594,8 +591,10 @@ cudaError_t launch_nt(const SelectParams& p, int ranks, cudaStream_t stream) {
   const size_t ring = (size_t)NT * kAhead * 32, exact = (size_t)p.max_blocks * 8;
   const size_t smem = copies_at(p.max_blocks) + (ring > exact ? ring : exact);
   const auto kernel = select_kernel<D, NG, NT>;
-  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-  if (e != cudaSuccess) return e;
+  if (smem > 40 * 1024) {  // (less, with the static part, is granted without asking)
+    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    if (e != cudaSuccess) return e;
+  }
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(p.batch * p.num_kv_heads * ranks));
   cfg.blockDim = dim3(NT);
