@@ -3,7 +3,10 @@
 // The first R channels of a row at position p are pairs (x1, x2) -- channel i
 // with i + R / 2, or neighbours -- that become
 //   (fl(fl(x1 c) - fl(x2 s)), fl(fl(x2 c) + fl(x1 s))),  c, s = cos, sin of the pair's angle at p,
-// in fp32.  K goes into the cache from there, without a rounding to the rows'
+// in fp32, on pairs of values: product, product times sign plus product, where the
+// sign is a number that the compiler does not know (Turn::one), so that it does
+// not make an addition and then one fused operation of it.  K goes into the cache
+// from there, without a rounding to the rows'
 // type between; turned queries (and keys, where attention over rows follows)
 // are rounded to it once.
 #include <cuda_bf16.h>
@@ -97,7 +100,7 @@ __global__ void __launch_bounds__(32 * kEdgeWarps, 2) rotary_k_kernel(const Appe
       for (int i = 0; i < kTok; ++i, at += p.turn.dim) {
         const float4 v = raw[i].get();
         const float2 c = angle2(at), s = angle2(at + half);
-        const uint64_t sign = rows::pair(-1.f, 1.f);
+        const uint64_t sign = rows::pair(-p.turn.one, p.turn.one);
         float4 y;
         rows::unpair(rows::fma2(rows::mul2(rows::pair(v.y, v.x), rows::pair(s.x, s.x)), sign,
                                 rows::mul2(rows::pair(v.x, v.y), rows::pair(c.x, c.x))), y.x, y.y);
@@ -108,7 +111,8 @@ __global__ void __launch_bounds__(32 * kEdgeWarps, 2) rotary_k_kernel(const Appe
     } else {
       const float* at = my_angles + (on ? upper ? hc - half : hc : 0);
       const int away = on ? upper ? -half : half : 0;  // the partner, in channels
-      const uint64_t sign = upper ? rows::pair(1.f, 1.f) : rows::pair(-1.f, -1.f);
+      const float one = upper ? p.turn.one : -p.turn.one;
+      const uint64_t sign = rows::pair(one, one);
       long long other = row0 + (long long)min(head_of(q, ch), H - 1) * p.x[0].sh + hc + away;
 #pragma unroll
       for (int i = 0; i < kTok; ++i, at += p.turn.dim, other += p.x[0].st) {
@@ -401,7 +405,7 @@ __global__ void __launch_bounds__(kTurnThreads) turn_rows_kernel(const TurnRowsP
     c[0] = ca.x; c[1] = ca.y; c[2] = cb.x; c[3] = cb.y;
     sn[0] = sa.x; sn[1] = sa.y; sn[2] = sb.x; sn[3] = sb.y;
   }
-  const uint64_t minus = rows::pair(-1.f, -1.f), plus = rows::pair(1.f, 1.f);
+  const uint64_t minus = rows::pair(-p.turn.one, -p.turn.one), plus = rows::pair(p.turn.one, p.turn.one);
   void* out = key ? p.out[1] : p.out[0];
 #pragma unroll
   for (int k = 0; k < kPasses; ++k) {

@@ -166,7 +166,7 @@ KVQ_API kvq_status kvq_append_rotary(const kvq_cache_desc* cache, int32_t dtype,
   if (!aligned16(q_out) || !aligned16(k_out)) return KVQ_ERR_INVALID_ARG;
   s = check_device(nullptr);
   if (s != KVQ_OK) return s;
-  p.turn = Turn{rotary->angles, rotary->dim, rotary->interleaved};
+  p.turn = Turn{rotary->angles, rotary->dim, rotary->interleaved, 1.0f};
   if (rotary->positions < p.most) p.most = rotary->positions;
   TurnRowsParams t{};
   if (queries) { t.x[0] = rows_of(q); t.out[0] = q_out; t.heads[0] = num_q_heads; }

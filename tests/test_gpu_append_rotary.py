@@ -127,6 +127,21 @@ def test_types_key_rows_and_separate_windows(dtype, interleaved, schemes):
         assert torch.equal(a, b)
 
 
+@pytest.mark.parametrize("interleaved", [False, True])
+@pytest.mark.parametrize("dim,rotary", [(64, 64), (128, 128), (128, 96), (256, 256), (256, 144)])
+def test_to_the_last_bit(dim, rotary, interleaved):
+    """fp32 queries equal single operations bit by bit (a fused one would differ in a quarter of them), and so do the
+    codes, scales and offsets of millions of 16-bit keys, of which some would differ."""
+    s = Setup(4, (1, 1), dim, 32, 2, torch.float32, rotary, interleaved, old=[0], new=[1000], paged=False)
+    q = s.rotary(*s.copies(), q=s.q)
+    assert torch.equal(q, turn(s.q, s.table[s.position], interleaved))
+    for schemes in ((1, 0), (0, 0)):
+        s = Setup(4, schemes, dim, 32, 8, torch.bfloat16, rotary, interleaved, old=[0, 0], new=[4096, 1024], seed=3)
+        got = s.copies()
+        s.rotary(*got)
+        s.check_equal(got, s.reference())
+
+
 @pytest.mark.parametrize("bits", [2, 4])
 @pytest.mark.parametrize("dim,group", [(64, 32), (128, 128), (256, 64)])
 def test_token_wise_without_windows(bits, dim, group):
