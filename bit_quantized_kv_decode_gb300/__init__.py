@@ -665,14 +665,18 @@ def select_blocks(desc: CacheDesc, q: torch.Tensor, k_cache, seq_lens: torch.Ten
     _, ks, kz = _cache_ptrs(desc, "k_cache", k_cache, dev)
     if budget < 1:
         raise ValueError("budget must be at least 1")
-    given = blocks is not None or counts is not None
-    if blocks is None:
-        blocks = torch.empty(B, H, budget, dtype=torch.int32, device=q.device)
-    if counts is None:
-        counts = torch.empty(B, H, dtype=torch.int32, device=q.device)
-    pb, pc = _ptr(blocks, "blocks", (torch.int32,), B * H * budget, dev), _ptr(counts, "counts", (torch.int32,), B * H, dev)
-    if given:
-        others = [_span(t) for t in (q, *k_cache, seq_lens, page_table) if t is not None]
+    if blocks is None and counts is None:
+        blocks = torch.empty((B, H, budget), dtype=torch.int32, device=q.device)
+        counts = torch.empty((B, H), dtype=torch.int32, device=q.device)
+        pb, pc = blocks.data_ptr(), counts.data_ptr()
+    else:
+        if blocks is None:
+            blocks = torch.empty((B, H, budget), dtype=torch.int32, device=q.device)
+        if counts is None:
+            counts = torch.empty((B, H), dtype=torch.int32, device=q.device)
+        pb = _ptr(blocks, "blocks", (torch.int32,), B * H * budget, dev)
+        pc = _ptr(counts, "counts", (torch.int32,), B * H, dev)
+        others = [_span(t) for t in (q, *k_cache, seq_lens, page_table, dev_status) if t is not None]
         _disjoint("blocks", _span(blocks), others + [_span(counts)])
         _disjoint("counts", _span(counts), others)
     d = _lib.SelectDesc(desc, B, Hq, mb, budget, first, last)
@@ -713,38 +717,41 @@ def sparse_decode_attn(desc: CacheDesc, q: torch.Tensor, k_cache, v_cache, seq_l
     kc, vc = _cache_ptrs(desc, "k_cache", k_cache, dev), _cache_ptrs(desc, "v_cache", v_cache, dev)
     pb, pc = _ptr(blocks, "blocks", (torch.int32,), B * H * n, dev), _ptr(counts, "counts", (torch.int32,), B * H, dev)
     d = _lib.SparseDesc(desc, B, Hq, mb, n, sm_scale, flags)
-    need = _sparse_bytes(d)
-    pq, pn = q.data_ptr(), _ptr(seq_lens, "seq_lens", (torch.int32,), B, dev)
-    spans = []  # what the caller gave to be written
+    pn = _ptr(seq_lens, "seq_lens", (torch.int32,), B, dev)
+    written = out is not None or lse is not None
     if out is None:
         out = torch.empty_like(q)
         po = out.data_ptr()
     else:
         po = _ptr(out, "out", (q.dtype,), B * Hq * D, dev)
-        spans.append(("out", (po, po + B * Hq * D * 2)))
-    if lse is None:
-        lse = torch.empty(B, Hq, dtype=torch.float32, device=q.device) if return_lse else None
-        pl = None if lse is None else lse.data_ptr()
-    else:
+    if lse is not None:
         pl = _ptr(lse, "lse", (torch.float32,), B * Hq, dev)
-        spans.append(("lse", (pl, pl + B * Hq * 4)))
-    if workspace is None:
-        size, pw = need, None
-        if need:
-            workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
-            pw = workspace.data_ptr()
+    elif return_lse:
+        lse = torch.empty((B, Hq), dtype=torch.float32, device=q.device)
+        pl = lse.data_ptr()
     else:
+        pl = None
+    given = workspace is not None
+    if given:
         size = workspace.numel()
         pw = _ptr(workspace, "workspace", (torch.uint8,), size, dev)
-        if size >= need > 0:
-            spans.append(("workspace", (pw, pw + need)))  # (of a longer one, the first bytes are used)
-    if spans:
-        others = [(pq, pq + B * Hq * D * 2), (pb, pb + B * H * n * 4), (pc, pc + B * H * 4), (pn, pn + B * 4)]
-        if pt:
-            others.append((pt, pt + B * mb * 4))
-        for name, span in spans:
-            _disjoint(name, span, others)
-            others.append(span)
+    else:
+        size, pw = _sparse_bytes(d), None
+        if size:
+            workspace = torch.empty(size, dtype=torch.uint8, device=q.device)
+            pw = workspace.data_ptr()
+    if written or given:
+        spans = ((po, B * Hq * D * 2), (pl or 0, B * Hq * 4 if pl else 0), (pq, B * Hq * D * 2), (pb, B * H * n * 4),
+                 (pc, B * H * 4), (pn, B * 4), (pt or 0, B * mb * 4 if pt else 0))
+        if given:
+            for at, length in spans:
+                # (of a longer workspace, the first bytes are used)
+                if at < pw + size and pw < at + length and at < pw + _sparse_bytes(d):
+                    raise ValueError("workspace overlaps another array of the call")
+        if written:
+            spans = [(at, at + length) for at, length in spans]
+            _disjoint("out", spans[0], spans[1:])
+            _disjoint("lse", spans[1], spans[2:])
     _launch(dev, "kvq_sparse_decode_attn", library().kvq_sparse_decode_attn, ctypes.byref(d), pq, *kc, *vc, pn, pt, pb, pc, po,
             pl, pw, size, _ptr(dev_status, "dev_status", _STATUS, 1, dev))
     return out if lse is None else (out, lse)
