@@ -600,6 +600,8 @@ def append_rotary(desc: CacheDesc, table: torch.Tensor, k_new: torch.Tensor, v_n
                                              page_table, max_blocks, k_window_out, v_window_out, dev_status, "append_rotary")
     if not isinstance(table, torch.Tensor) or table.dim() != 2:
         raise ValueError("table must be fp32 [positions, rotated channels]")
+    if (table.requires_grad and torch.is_grad_enabled()) or _has_tangent(table):
+        raise ValueError("table requires a gradient or has a tangent: this operator has no derivative")
     positions, dim = table.shape
     rotary = _lib.Rotary(_ptr(table, "table", (torch.float32,), positions * dim, dev), positions, dim,
                          1 if interleaved else 0)
@@ -750,6 +752,7 @@ def sparse_decode_attn(desc: CacheDesc, q: torch.Tensor, k_cache, v_cache, seq_l
                     raise ValueError("workspace overlaps another array of the call")
         if written:
             spans = [(at, at + length) for at, length in spans]
+            spans += [_span(t) for t in (*k_cache, *v_cache, dev_status) if t is not None]
             _disjoint("out", spans[0], spans[1:])
             _disjoint("lse", spans[1], spans[2:])
     _launch(dev, "kvq_sparse_decode_attn", library().kvq_sparse_decode_attn, ctypes.byref(d), pq, *kc, *vc, pn, pt, pb, pc, po,

@@ -21,15 +21,18 @@ constexpr int kSmemPerSm = 228 * 1024, kSmemReserved = 1024;
 int sparse_splits(long long units, int list_len) {
   long long best = -1;
   int splits = 1;
-  for (int s = 1; s <= list_len; ++s) {
-    const long long blocks = (list_len + s - 1) / s, ctas = units * s;
-    const long long alone = 12 * blocks, shared = ctas * (5 * blocks + 8) / kSms;
+  int blocks = list_len;  // of a range
+  for (int s = 1;; s = (list_len - 1) / (blocks - 1) + 1) {  // (the next s with fewer: those between add only CTAs)
+    if (units * (s - 1) > 32 * kSms) break;
+    blocks = (list_len + s - 1) / s;
+    const long long ctas = units * s;
+    const long long alone = 12LL * blocks, shared = ctas * (5 * blocks + 8) / kSms;
     const long long cost = (alone > shared ? alone : shared) + alone / 2 + (s > 1 ? 30 : 0);
     if (best < 0 || cost < best) {
       best = cost;
       splits = s;
     }
-    if (ctas > 32 * kSms) break;  // more only adds CTAs
+    if (blocks == 1) break;
   }
   return splits;
 }
