@@ -94,6 +94,17 @@ def test_large_and_not_finite_queries():
     check(c, bad, 9)
 
 
+@pytest.mark.parametrize("small", [-100, -115, -128])
+def test_products_that_fp32_does_not_hold(small):
+    """Queries times scales and offsets of 2^-20: below 2^-149 in part, or altogether."""
+    c = Cache(4, (1, 0), 2, [128 * 40, 128 * 50], seed=11)
+    for t in c.k[1:]:
+        t.copy_((t.float() * 2.0 ** -20).half())
+    q = (c.queries(4).float() * 2.0 ** small).to(torch.bfloat16)
+    assert q.any()
+    check(c, q, 9)
+
+
 def test_bad_lengths_and_pages():
     import bit_quantized_kv_decode_gb300 as kvq
     c = Cache(4, (1, 0), 2, [128 * 40, 128 * 30, 128 * 20], seed=8)
