@@ -49,6 +49,14 @@ __global__ void __launch_bounds__(32 * kBlockWarps, kBlockCtas) append_blocks_ke
   append_block<T, BITS, W>(p, blockIdx.z & 1, blockIdx.z >> 1);
 }
 
+template <typename T, int BITS, int W, Part PART>
+__global__ void __launch_bounds__(32 * kEdgeWarps, sizeof(Raw<T>) == 8 ? 2 : 1) append_edges_kernel(const AppendParams p) {
+  append_edge<T, BITS, W, PART, false>(p);
+  // overlaps append_blocks_kernel: what follows in the stream waits for
+  // this grid, which is not done before that one is
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+}
+
 template <typename T, int BITS, int W>
 cudaError_t launch_w(const AppendParams& p, cudaStream_t stream) {
   constexpr bool kHalf = sizeof(Raw<T>) == 8;
@@ -61,10 +69,7 @@ cudaError_t launch_w(const AppendParams& p, cudaStream_t stream) {
       if (e != cudaSuccess) return e;
     }
   }
-  // one edge per sequence, two where a chunk of two tokens or more can cross
-  // into the next block; every block: one more for each 128 tokens past that
-  const long long two = p.batch < p.total / 2 ? p.batch : p.total / 2;
-  const long long blocks = p.batch + two + (kHalf ? 0 : (p.total - 2 * two) / kBlockTokens);
+  const long long blocks = edge_blocks(p.batch, p.total, kHalf);
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)blocks, heads, planes);
   cfg.blockDim = dim3(32 * kEdgeWarps);
@@ -74,7 +79,7 @@ cudaError_t launch_w(const AppendParams& p, cudaStream_t stream) {
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = whole ? 1 : 0;
-  return cudaLaunchKernelEx(&cfg, append_edges_kernel<T, BITS, W, kHalf ? kEdges : kEvery, false>, p);
+  return cudaLaunchKernelEx(&cfg, append_edges_kernel<T, BITS, W, kHalf ? kEdges : kEvery>, p);
 }
 
 template <typename T>

@@ -193,39 +193,30 @@ __device__ __forceinline__ void find_block(const AppendParams& p, int rank, int*
 }
 
 // Channel-wise groups of a tile, by the whole block: the warps' ranges in
-// `ranges` ([low, high][warp][channel]) become scales and offsets ([s,
-// z][token group][channel]); their 16-bit forms go to s_out, z_out.
+// `ranges` ([low, high][warp][channel]) become `groups_of` ([scale, offset,
+// scale's reciprocal][token group][channel]); the 16-bit forms go to s_out, z_out.
 template <int BITS, int W, int NW>
-__device__ __forceinline__ void channel_groups(float (*ranges)[NW][W], int groups, int gw, uint16_t* s_out,
-                                               uint16_t* z_out, uint32_t* dev_status) {
-  constexpr int kThreads = 32 * NW, kEach = 512 / kThreads;  // groups * W <= 512
-  const int tid = threadIdx.x;
-  Group mine[kEach];
+__device__ __forceinline__ void channel_groups(const float (*ranges)[NW][W], float (*groups_of)[4][W], int groups, int gw,
+                                               uint16_t* s_out, uint16_t* z_out, uint32_t* dev_status) {
+  constexpr int kThreads = 32 * NW, kStep = NW / 4;  // (a group has NW / 4 warps at least)
   __syncthreads();
+  for (int e = threadIdx.x; e < groups * W; e += kThreads) {
+    const int g = e / W, c = e % W;
+    float a = INFINITY, z = -INFINITY;
+    for (int w = g * gw; w < (g + 1) * gw; w += kStep) {
 #pragma unroll
-  for (int k = 0; k < kEach; ++k) {
-    const int e = tid + k * kThreads;
-    if (e < groups * W) {
-      const int g = e / W, c = e % W;
-      float a = INFINITY, z = -INFINITY;
-      for (int w = g * gw; w < (g + 1) * gw; ++w) {
-        a = min_nan(a, ranges[0][w][c]);
-        z = max_nan(z, ranges[1][w][c]);
+      for (int i = 0; i < kStep; ++i) {
+        a = min_nan(a, ranges[0][w + i][c]);
+        z = max_nan(z, ranges[1][w + i][c]);
       }
-      mine[k] = group_of_range(a, z, (float)((1 << BITS) - 1));
-      if (isnan(mine[k].s)) report(dev_status, KVQ_DEV_NONFINITE);
-      s_out[e] = mine[k].s_bits;
-      z_out[e] = mine[k].z_bits;
     }
-  }
-  __syncthreads();
-#pragma unroll
-  for (int k = 0; k < kEach; ++k) {
-    const int e = tid + k * kThreads;
-    if (e < groups * W) {
-      ranges[0][e / W][e % W] = mine[k].s;
-      ranges[1][e / W][e % W] = mine[k].z;
-    }
+    const Group mine = group_of_range(a, z, (float)((1 << BITS) - 1));
+    if (isnan(mine.s)) report(dev_status, KVQ_DEV_NONFINITE);
+    s_out[e] = mine.s_bits;
+    z_out[e] = mine.z_bits;
+    groups_of[0][g][c] = mine.s;
+    groups_of[1][g][c] = mine.z;
+    groups_of[2][g][c] = reciprocal(mine.s);
   }
   __syncthreads();
 }
@@ -259,18 +250,30 @@ __device__ __forceinline__ float4 turned(const AppendParams& p, float4 v, long l
                      __fadd_rn(__fmul_rn(v.z, c.z), __fmul_rn(w.z, s.z)), __fadd_rn(__fmul_rn(v.w, c.w), __fmul_rn(w.w, s.w)));
 }
 
+// CTAs of append_edge in x: one per sequence; one more where a chunk of two tokens
+// or more can cross into the next block; and where the edges' kernel takes whole
+// blocks too, one for each 128 tokens past that.  None but the sequences' where
+// there are no more tokens than sequences.
+inline long long edge_blocks(long long batch, long long total, bool whole_apart) {
+  if (total <= batch) return batch;
+  const long long two = batch < total / 2 ? batch : total / 2;
+  return batch + two + (whole_apart ? 0 : (total - 2 * two) / kBlockTokens);
+}
+
 template <typename T, int BITS, int W, Part PART, bool TURN>  // W: channels of the slab; TURN: K's rows are turned
 __device__ __forceinline__ void append_edge(const AppendParams& p) {
   constexpr int kWarps = kEdgeWarps, kThreads = 32 * kWarps, kWarpTok = kBlockTokens / kWarps;  // tokens of a warp
   constexpr int kLanes = W / 4;                 // lanes that share a token
   constexpr int kTok = kWarpTok * kLanes / 32;  // tokens of a thread (8 or 4)
+  constexpr int kLgTok = kTok == 8 ? 3 : 2;
+  static_assert(1 << kLgTok == kTok, "tokens of a thread");
   constexpr int kPer = 128 / BITS;              // codes of a 16-byte piece
   constexpr int kPieces = W * BITS;             // 16-byte pieces of the slab's block: 128 W BITS / 128
   constexpr float kMax = (float)((1 << BITS) - 1);
   // packed block: K [chunk][128 tokens], V [chunk][W channels], a piece of padding per chunk against bank conflicts
   __shared__ __align__(16) unsigned char packed[(kPieces + W * BITS / 64 + 8) * 16];
-  // channel-wise: ranges per warp, then s / z (as [group][W]); token-wise: s, z of every (token, group)
-  __shared__ __align__(16) float ranges[2][kWarps][W];
+  // channel-wise: ranges per warp, and groups; token-wise: s, z of every (token, group)
+  __shared__ __align__(16) float ranges[2][kWarps][W], groups_of[3][4][W];
   float(*lo_s)[W] = ranges[0], (*hi_s)[W] = ranges[1];
   __shared__ __align__(16) uint16_t s_out[128 * 4], z_out[128 * 4];
   __shared__ int found[2];
@@ -278,29 +281,63 @@ __device__ __forceinline__ void append_edge(const AppendParams& p) {
   const int h = blockIdx.y, which = blockIdx.z & 1, slab = blockIdx.z >> 1;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const bool lead = h == 0 && blockIdx.z == 0;
-  // the first `batch` CTAs take the first block of a sequence each (every thread
-  // looks for itself), the others what more there is
-  int b = blockIdx.x, nth = 0;
-  if (blockIdx.x >= p.batch) {
-    if (warp == 0) find_block<PART, 1>(p, blockIdx.x - p.batch, found);
-    __syncthreads();
-    b = found[0];
-    nth = found[1];
-    if (b < 0) return;
-  }
-  const Chunk chunk = load_chunk(p, b);
-  if (blockIdx.x < p.batch) {
+  // The first `batch` CTAs take the first block of a sequence each (every thread
+  // looks for itself), the others what more there is.  With no more tokens than
+  // sequences there are no others: n tokens touch n blocks at most, so the CTAs
+  // of sequences without any are as many as what more there is, and take it when
+  // they have copied their window.
+  auto copy_window = [&](int seq, int held) {  // (of a sequence without new tokens: to another window)
+    float* to = p.window_out[which];
+    if (to == nullptr || to == p.window[which]) return;
+    const size_t at = ((size_t)seq * p.num_kv_heads + h) * kBlockTokens * D + slab * W;
+    for (int e = tid; e < held % kBlockTokens * kLanes; e += kThreads) {
+      const size_t i = at + (size_t)(e / kLanes) * D + e % kLanes * 4;
+      *reinterpret_cast<float4*>(to + i) = *reinterpret_cast<const float4*>(p.window[which] + i);
+    }
+  };
+  int b = blockIdx.x, nth = 0, rank = (int)blockIdx.x - p.batch;
+  const bool alone = gridDim.x == p.batch;
+  bool first = rank < 0;
+  Chunk chunk;
+  while (true) {
+    if (!first) {
+      if (warp == 0) find_block<PART, 1>(p, rank, found);
+      __syncthreads();
+      b = found[0];
+      nth = found[1];
+      if (b < 0) return;
+    }
+    chunk = load_chunk(p, b);
+    if (!first) break;
+    const bool none = chunk.bad || chunk.rows.n == 0;
     if (chunk.bad && lead && tid == 0) report(p.dev_status, KVQ_DEV_BAD_SEQ_LEN);
-    if (part_blocks<PART>(chunk) <= 0) return;
-    nth = block_of<PART>(chunk, 0);
+    if (!none) {
+      if (part_blocks<PART>(chunk) <= 0) return;
+      nth = block_of<PART>(chunk, 0);
+      break;
+    }
+    if (!chunk.bad) copy_window(b, chunk.len);
+    if (!alone) return;
+    if (tid == 0) found[0] = 0;
+    __syncthreads();
+    int before = 0;
+    for (int i = tid; i < b; i += kThreads) {
+      const Chunk c = load_chunk(p, i);
+      before += c.bad || c.rows.n == 0;
+    }
+    if (before != 0) atomicAdd(&found[0], before);
+    __syncthreads();
+    rank = found[0];
+    __syncthreads();
+    first = false;
   }
   const SeqRows s = chunk.rows;
   const int len = chunk.len, end = len + s.n;
   const int j = len / kBlockTokens + nth, t0 = j * kBlockTokens;
   const int nv = min(kBlockTokens, end - t0);  // rows of this block
   const int from = min(max(len - t0, 0), nv);  // ... that were there before
-  // (asked for now, needed at the end; an empty chunk may be at the end of its table)
-  const int page = s.n == 0 ? -1 : p.page_table ? p.page_table[(size_t)b * p.max_blocks + j] : b * p.max_blocks + j;
+  // (asked for now, needed at the end)
+  const int page = p.page_table ? p.page_table[(size_t)b * p.max_blocks + j] : b * p.max_blocks + j;
   const bool tokenwise = p.scheme[which] == KVQ_TOKENWISE;
   const size_t win_at = ((size_t)b * p.num_kv_heads + h) * kBlockTokens * D + slab * W;
   const float* win = p.window[which] ? p.window[which] + win_at : nullptr;
@@ -318,7 +355,7 @@ __device__ __forceinline__ void append_edge(const AppendParams& p) {
   float x[kTok][4];
   {
     Raw<T> raw[kTok];
-    if (from == 0 && nv == kBlockTokens) {  // a whole block of new tokens, as most are
+    if (warp * kWarpTok >= from && (warp + 1) * kWarpTok <= nv) {  // this warp's are all new
 #pragma unroll
       for (int i = 0; i < kTok; ++i)
         raw[i].load(rows.data, (long long)(s.first + t0 + tok + i - len) * rows.st + at0);
@@ -328,8 +365,9 @@ __device__ __forceinline__ void append_edge(const AppendParams& p) {
         x[i][0] = v.x; x[i][1] = v.y; x[i][2] = v.z; x[i][3] = v.w;
       }
     } else {
-      // all loads before the first use.  Earlier tokens: for a group along the
-      // tokens, or to be copied to another window.
+      // all loads before the first use, and no code for what is not there: what
+      // bounds a step of one token is how many instructions a warp has.  Earlier
+      // tokens: for a group along the tokens, or to be copied to another window.
       const bool old = win != nullptr && (!tokenwise || p.window_out[which] != p.window[which]);
 #pragma unroll
       for (int i = 0; i < kTok; ++i) {
@@ -338,17 +376,19 @@ __device__ __forceinline__ void append_edge(const AppendParams& p) {
         if (old && t < from) v = *reinterpret_cast<const float4*>(win + (size_t)t * D + ch);
         x[i][0] = v.x; x[i][1] = v.y; x[i][2] = v.z; x[i][3] = v.w;
       }
+      if ((warp + 1) * kWarpTok > from && warp * kWarpTok < nv) {  // new ones among the warp's
 #pragma unroll
-      for (int i = 0; i < kTok; ++i) {
-        const int t = tok + i;
-        if (t >= from && t < nv) raw[i].load(rows.data, (long long)(s.first + t0 + t - len) * rows.st + at0);
-      }
+        for (int i = 0; i < kTok; ++i) {
+          const int t = tok + i;
+          if (t >= from && t < nv) raw[i].load(rows.data, (long long)(s.first + t0 + t - len) * rows.st + at0);
+        }
 #pragma unroll
-      for (int i = 0; i < kTok; ++i) {
-        const int t = tok + i;
-        if (t >= from && t < nv) {
-          const float4 v = value(raw[i], tok + i, ch);
-          x[i][0] = v.x; x[i][1] = v.y; x[i][2] = v.z; x[i][3] = v.w;
+        for (int i = 0; i < kTok; ++i) {
+          const int t = tok + i;
+          if (t >= from && t < nv) {
+            const float4 v = value(raw[i], tok + i, ch);
+            x[i][0] = v.x; x[i][1] = v.y; x[i][2] = v.z; x[i][3] = v.w;
+          }
         }
       }
     }
@@ -361,6 +401,7 @@ __device__ __forceinline__ void append_edge(const AppendParams& p) {
   if (win != nullptr && end > last) {
     float* wout = p.window_out[which] + win_at;
     if (last == t0 && (nth == 0 || len % kBlockTokens == 0)) {
+      if (warp * kWarpTok < nv && (wout != win || (warp + 1) * kWarpTok > from))
 #pragma unroll
       for (int i = 0; i < kTok; ++i) {
         const int t = tok + i;
@@ -378,13 +419,12 @@ __device__ __forceinline__ void append_edge(const AppendParams& p) {
       }
     }
   }
-  if (s.n == 0) return;
   if (page < 0 || page >= p.num_pages) {
     if (lead && tid == 0) report(p.dev_status, KVQ_DEV_BAD_PAGE);
     return;
   }
-  const int G = p.group, gps = W / G;  // channel groups of a token in this slab (token-wise)
-  const int nsz = kBlockTokens * D / G;
+  const int G = p.group, lgG = 31 - __clz(G), gps = W >> lgG;  // channel groups of a token in this slab (token-wise)
+  const int nsz = kBlockTokens * D >> lgG;
   const size_t blk = (size_t)page * p.num_kv_heads + h;
 
   // Where codes go.  K, one token: the thread's 4 codes are 16 (8) bits of the
@@ -432,7 +472,7 @@ __device__ __forceinline__ void append_edge(const AppendParams& p) {
     put_none();
   } else if (tokenwise) {
     // ranges of the thread's tokens over its 4 channels, then over the group's lanes
-    const int lg = G / 4, gl = lane & (lg - 1);  // lanes of a group, place in it
+    const int lg = G >> 2, gl = lane & (lg - 1);  // lanes of a group, place in it
     float mn[kTok], mx[kTok];
 #pragma unroll
     for (int i = 0; i < kTok; ++i) {
@@ -443,15 +483,15 @@ __device__ __forceinline__ void append_edge(const AppendParams& p) {
     reduce_group<kTok, true>(mx, lg);
     float4* sz = reinterpret_cast<float4*>(ranges);  // [token][group] s, z, 1 / s: at most 128 x W / 32 of them
     static_assert(sizeof(ranges) >= 128 * (W / 32) * sizeof(float4), "table");
-    const int each = kTok / lg > 1 ? kTok / lg : 1, share = lg / kTok > 1 ? lg / kTok : 1;
+    const int each = kTok > lg ? kTok >> (lgG - 2) : 1, share = lg > kTok ? lg / kTok : 1;
 #pragma unroll
     for (int k = 0; k < 2; ++k) {
-      if (k < each && gl % share == 0) {
-        const int t = tok + (each > 1 ? gl * each + k : gl / share);
+      if (k < each && (gl & (share - 1)) == 0) {
+        const int t = tok + (each > 1 ? gl * each + k : gl >> (lg > kTok ? lgG - 2 - kLgTok : 0));
         const bool live = t >= from && t < nv;
         const Group g = live ? group_of_range(mn[k], mx[k], kMax) : Group{0.f, 0.f, 0, 0};
         if (isnan(g.s)) report(p.dev_status, KVQ_DEV_NONFINITE);
-        const int e = t * gps + ch / G;
+        const int e = t * gps + (ch >> lgG);
         sz[e] = make_float4(g.s, g.z, reciprocal(g.s), 0.f);
         s_out[e] = g.s_bits;
         z_out[e] = g.z_bits;
@@ -461,7 +501,7 @@ __device__ __forceinline__ void append_edge(const AppendParams& p) {
     uint32_t acc[kWords][4] = {};
 #pragma unroll
     for (int i = 0; i < kTok; ++i) {
-      float4 g = sz[(tok + i) * gps + ch / G];
+      float4 g = sz[(tok + i) * gps + (ch >> lgG)];
       if (isnan(g.x)) {
         g.x = 0.f;
         x[i][0] = x[i][1] = x[i][2] = x[i][3] = 0.f;
@@ -515,24 +555,25 @@ __device__ __forceinline__ void append_edge(const AppendParams& p) {
     }
     *reinterpret_cast<float4*>(&lo_s[warp][ch]) = make_float4(mn[0], mn[1], mn[2], mn[3]);
     *reinterpret_cast<float4*>(&hi_s[warp][ch]) = make_float4(mx[0], mx[1], mx[2], mx[3]);
-    const int gw = G / kWarpTok, groups = kBlockTokens / G;  // warps of a token group, token groups
-    channel_groups<BITS, W, kWarps>(ranges, groups, gw, s_out, z_out, p.dev_status);
+    const int gw = G / kWarpTok, groups = kBlockTokens >> lgG;  // warps of a token group, token groups
+    channel_groups<BITS, W, kWarps>(ranges, groups_of, groups, gw, s_out, z_out, p.dev_status);
     if (past) {
       put_none();
     } else {
-      const int g = warp * kWarpTok / G;
-      const float4 s4 = *reinterpret_cast<const float4*>(&lo_s[g][ch]);
-      const float4 z4 = *reinterpret_cast<const float4*>(&hi_s[g][ch]);
-      float sc[4] = {s4.x, s4.y, s4.z, s4.w}, rc[4];
-      const float zc[4] = {z4.x, z4.y, z4.z, z4.w};
+      const int g = warp * kWarpTok >> lgG;
+      const float4 s4 = *reinterpret_cast<const float4*>(&groups_of[0][g][ch]);
+      const float4 z4 = *reinterpret_cast<const float4*>(&groups_of[1][g][ch]);
+      const float4 r4 = *reinterpret_cast<const float4*>(&groups_of[2][g][ch]);
+      float sc[4] = {s4.x, s4.y, s4.z, s4.w};
+      const float zc[4] = {z4.x, z4.y, z4.z, z4.w}, rc[4] = {r4.x, r4.y, r4.z, r4.w};
+      if (isnan(s4.x + s4.y + s4.z + s4.w)) {
 #pragma unroll
-      for (int c = 0; c < 4; ++c) {
-        if (isnan(sc[c])) {
-          sc[c] = 0.f;
+        for (int c = 0; c < 4; ++c)
+          if (isnan(sc[c])) {
+            sc[c] = 0.f;
 #pragma unroll
-          for (int i = 0; i < kTok; ++i) x[i][c] = 0.f;
-        }
-        rc[c] = reciprocal(sc[c]);
+            for (int i = 0; i < kTok; ++i) x[i][c] = 0.f;
+          }
       }
       uint64_t sn[2], zn[2], r2[2];
 #pragma unroll
@@ -541,7 +582,7 @@ __device__ __forceinline__ void append_edge(const AppendParams& p) {
         zn[c] = rows::pair(-zc[2 * c], -zc[2 * c + 1]);
         r2[c] = rows::pair(rc[2 * c], rc[2 * c + 1]);
       }
-      if (nv < kBlockTokens) {  // tokens past the end have code 0
+      if ((warp + 1) * kWarpTok > nv) {  // tokens past the end have code 0
 #pragma unroll
         for (int i = 0; i < kTok; ++i)
           if (tok + i >= nv) {
@@ -601,26 +642,19 @@ __device__ __forceinline__ void append_edge(const AppendParams& p) {
   uint16_t* so = p.scale[which] + blk * nsz;
   uint16_t* zo = p.zero[which] + blk * nsz;
   if (tokenwise) {  // entry token * (D / G) + group
+    const int lg_gps = 31 - __clz(gps);
     for (int e = tid + keep * gps; e < kBlockTokens * gps; e += kThreads) {
-      const int t = e / gps, at = t * (D / G) + slab * gps + e - t * gps;
+      const int t = e >> lg_gps, at = t * (D >> lgG) + slab * gps + e - t * gps;
       so[at] = s_out[e];
       zo[at] = z_out[e];
     }
   } else {  // entry token group * D + channel
-    for (int e = tid; e < kBlockTokens / G * W; e += kThreads) {
+    for (int e = tid; e < (kBlockTokens >> lgG) * W; e += kThreads) {
       const int at = e / W * D + slab * W + e % W;
       so[at] = s_out[e];
       zo[at] = z_out[e];
     }
   }
-}
-
-template <typename T, int BITS, int W, Part PART, bool TURN>
-__global__ void __launch_bounds__(32 * kEdgeWarps, sizeof(Raw<T>) == 8 ? 2 : 1) append_edges_kernel(const AppendParams p) {
-  append_edge<T, BITS, W, PART, TURN>(p);
-  // overlaps append_blocks_kernel: what follows in the stream waits for
-  // this grid, which is not done before that one is
-  asm volatile("griddepcontrol.wait;" ::: "memory");
 }
 
 // ------------------------------------------------------- whole blocks
@@ -678,7 +712,7 @@ __device__ __forceinline__ void append_block(const AppendParams& p, int which, i
   constexpr int kPlane = W / 4 + 2;
   __shared__ __align__(16) unsigned char packed[BITS * 4 * kPlane * 16];
   static_assert(BITS * 4 * kPlane >= kPieces + W / kPer, "K's padding fits too");
-  __shared__ __align__(16) float ranges[2][kWarps][W];
+  __shared__ __align__(16) float ranges[2][kWarps][W], groups_of[3][4][W];
   __shared__ __align__(16) uint16_t s_out[128 * 4], z_out[128 * 4];
   __shared__ int found[2];
   const int D = p.head_dim;
@@ -797,20 +831,19 @@ __device__ __forceinline__ void append_block(const AppendParams& p, int which, i
     a = wide<T>(hi.x);
     c = wide<T>(hi.y);
     *reinterpret_cast<float4*>(&ranges[1][warp][ch]) = make_float4(a.x, a.y, c.x, c.y);
-    channel_groups<BITS, W, kWarps>(ranges, kBlockTokens / G, G / kWarpTok, s_out, z_out, p.dev_status);
+    channel_groups<BITS, W, kWarps>(ranges, groups_of, kBlockTokens / G, G / kWarpTok, s_out, z_out, p.dev_status);
     const int g = warp * kWarpTok / G;
-    const float4 s4 = *reinterpret_cast<const float4*>(&ranges[0][g][ch]);
-    const float4 z4 = *reinterpret_cast<const float4*>(&ranges[1][g][ch]);
+    const float4 s4 = *reinterpret_cast<const float4*>(&groups_of[0][g][ch]);
+    const float4 z4 = *reinterpret_cast<const float4*>(&groups_of[1][g][ch]);
     float sc[4] = {s4.x, s4.y, s4.z, s4.w};
     uint32_t keep[2] = {0xffffffffu, 0xffffffffu};
-    float rc[4];
+    const float4 r4 = *reinterpret_cast<const float4*>(&groups_of[2][g][ch]);
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
       if (isnan(sc[k])) {
         sc[k] = 0.f;
         keep[k / 2] &= k & 1 ? 0x0000ffffu : 0xffff0000u;
       }
-      rc[k] = reciprocal(sc[k]);
     }
     if ((keep[0] & keep[1]) != 0xffffffffu) {
 #pragma unroll
@@ -818,7 +851,7 @@ __device__ __forceinline__ void append_block(const AppendParams& p, int which, i
     }
     const uint64_t sn[2] = {rows::pair(-sc[0], -sc[1]), rows::pair(-sc[2], -sc[3])};
     const uint64_t zn[2] = {rows::pair(-z4.x, -z4.y), rows::pair(-z4.z, -z4.w)};
-    const uint64_t r[2] = {rows::pair(rc[0], rc[1]), rows::pair(rc[2], rc[3])};
+    const uint64_t r[2] = {rows::pair(r4.x, r4.y), rows::pair(r4.z, r4.w)};
 #pragma unroll
     for (int i = 0; i < kTok; ++i) emit(i, sn, zn, r);
   }

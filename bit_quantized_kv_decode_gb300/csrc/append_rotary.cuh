@@ -79,11 +79,12 @@ __global__ void __launch_bounds__(32 * kEdgeWarps, 2) rotary_k_kernel(const Appe
   constexpr int kPer = 128 / BITS, kPieces = kColumn * BITS;  // codes of a 16-byte piece, pieces of a column
   constexpr float kMax = (float)((1 << BITS) - 1);
   __shared__ __align__(16) unsigned char packed[kColumn / kPer * 129 * 16];  // [chunk][128 tokens], a piece of padding
-  __shared__ __align__(16) float ranges[2][kWarps][kColumn];  // channel-wise: ranges, then s and z; token-wise: of every group
+  // channel-wise: ranges per warp, and groups; token-wise: s, z of every group
+  __shared__ __align__(16) float ranges[2][kWarps][kColumn], groups_of[3][4][kColumn];
   __shared__ __align__(16) uint16_t s_out[128 * 4], z_out[128 * 4];
   __shared__ int found[2];
   let_next_start();
-  const int D = p.head_dim, H = p.num_kv_heads, G = p.group;
+  const int D = p.head_dim, H = p.num_kv_heads, G = p.group, lgG = 31 - __clz(G);
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, tok = warp * kTok, ch = lane * 4;
   const int columns = (H * D + kColumn - 1) / kColumn, pieces = (columns + each - 1) / each;
   for (int item = blockIdx.x; item < p.total / kBlockTokens * pieces; item += gridDim.x) {
@@ -99,7 +100,7 @@ __global__ void __launch_bounds__(32 * kEdgeWarps, 2) rotary_k_kernel(const Appe
     // head and channel of column q's channel c
     auto head_of = [&](int q, int c) { return D == 64 ? 2 * q + (c >> 6) : D == 256 ? q >> 1 : q; };
     auto channel_of = [&](int q, int c) { return D == 64 ? c & 63 : D == 256 ? (q & 1) * kColumn + c : c; };
-    const int half = p.turn.dim >> 1, nsz = kBlockTokens * D / G;
+    const int half = p.turn.dim >> 1, nsz = kBlockTokens * D >> lgG;
     const bool near = p.turn.interleaved != 0, tokenwise = p.scheme[0] == KVQ_TOKENWISE;
     const long long row0 = ((long long)p.cu[b] + j * kBlockTokens - len + tok) * p.x[0].st;
     const float* angles = p.turn.angles + (size_t)(j * kBlockTokens) * p.turn.dim;  // of the block's tokens
@@ -180,9 +181,9 @@ __global__ void __launch_bounds__(32 * kEdgeWarps, 2) rotary_k_kernel(const Appe
         if (BITS == 4) *reinterpret_cast<uint16_t*>(k_at + i * 16) = (uint16_t)w;
         else k_at[i * 16] = (unsigned char)w;
       };
-      const int gps = kColumn / G;  // channel groups of a token, in the column
+      const int gps = kColumn >> lgG;  // channel groups of a token, in the column
       if (tokenwise) {
-        const int lg = G / 4, gl = lane & (lg - 1);  // lanes of a group, place in it
+        const int lg = G >> 2, gl = lane & (lg - 1);  // lanes of a group, place in it
         float mn[kTok], mx[kTok];
 #pragma unroll
         for (int i = 0; i < kTok; ++i) {
@@ -193,10 +194,11 @@ __global__ void __launch_bounds__(32 * kEdgeWarps, 2) rotary_k_kernel(const Appe
         reduce_group<kTok, true>(mx, lg);
         float4* sz = reinterpret_cast<float4*>(ranges);  // [token][group] -s, -z, 1 / s
         static_assert(sizeof(ranges) >= 128 * (kColumn / 32) * sizeof(float4), "table");
-        const int share = lg / kTok;  // (lg >= kTok: a lane has one value at most)
-        if (gl % share == 0) {
+        const int lg_share = lgG - 2 - 3;  // lg / kTok lanes to a value (lg >= kTok: a lane has one at most)
+        static_assert(kTok == 8, "values of a group");
+        if ((gl & ((1 << lg_share) - 1)) == 0) {
           const Group g = group_of_range(mn[0], mx[0], kMax);
-          const int e = (tok + gl / share) * gps + ch / G;
+          const int e = (tok + (gl >> lg_share)) * gps + (ch >> lgG);
           if (isnan(g.s)) report(p.dev_status, KVQ_DEV_NONFINITE);
           sz[e] = make_float4(-g.s, -g.z, reciprocal(g.s), 0.f);
           s_out[e] = g.s_bits;
@@ -205,7 +207,7 @@ __global__ void __launch_bounds__(32 * kEdgeWarps, 2) rotary_k_kernel(const Appe
         __syncwarp();  // a group's lanes are one warp's
 #pragma unroll
         for (int i = 0; i < kTok; ++i) {
-          float4 g = sz[(tok + i) * gps + ch / G];
+          float4 g = sz[(tok + i) * gps + (ch >> lgG)];
           if (isnan(g.x)) {
             g.x = 0.f;
             x[i][0] = x[i][1] = x[i][2] = x[i][3] = 0.f;
@@ -226,23 +228,24 @@ __global__ void __launch_bounds__(32 * kEdgeWarps, 2) rotary_k_kernel(const Appe
         }
         *reinterpret_cast<float4*>(&ranges[0][warp][ch]) = make_float4(mn[0], mn[1], mn[2], mn[3]);
         *reinterpret_cast<float4*>(&ranges[1][warp][ch]) = make_float4(mx[0], mx[1], mx[2], mx[3]);
-        channel_groups<BITS, kColumn, kWarps>(ranges, kBlockTokens / G, G / kTok, s_out, z_out, p.dev_status);
-        const int g = tok / G;
-        const float4 s4 = *reinterpret_cast<const float4*>(&ranges[0][g][ch]);
-        const float4 z4 = *reinterpret_cast<const float4*>(&ranges[1][g][ch]);
-        float sc[4] = {s4.x, s4.y, s4.z, s4.w}, rc[4];
+        channel_groups<BITS, kColumn, kWarps>(ranges, groups_of, kBlockTokens >> lgG, G / kTok, s_out, z_out, p.dev_status);
+        const int g = tok >> lgG;
+        const float4 s4 = *reinterpret_cast<const float4*>(&groups_of[0][g][ch]);
+        const float4 z4 = *reinterpret_cast<const float4*>(&groups_of[1][g][ch]);
+        const float4 r4 = *reinterpret_cast<const float4*>(&groups_of[2][g][ch]);
+        float sc[4] = {s4.x, s4.y, s4.z, s4.w};
+        if (isnan(s4.x + s4.y + s4.z + s4.w)) {
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          if (isnan(sc[c])) {
-            sc[c] = 0.f;
+          for (int c = 0; c < 4; ++c)
+            if (isnan(sc[c])) {
+              sc[c] = 0.f;
 #pragma unroll
-            for (int i = 0; i < kTok; ++i) x[i][c] = 0.f;
-          }
-          rc[c] = reciprocal(sc[c]);
+              for (int i = 0; i < kTok; ++i) x[i][c] = 0.f;
+            }
         }
         const uint64_t sn[2] = {rows::pair(-sc[0], -sc[1]), rows::pair(-sc[2], -sc[3])};
         const uint64_t zn[2] = {rows::pair(-z4.x, -z4.y), rows::pair(-z4.z, -z4.w)};
-        const uint64_t r[2] = {rows::pair(rc[0], rc[1]), rows::pair(rc[2], rc[3])};
+        const uint64_t r[2] = {rows::pair(r4.x, r4.y), rows::pair(r4.z, r4.w)};
 #pragma unroll
         for (int i = 0; i < kTok; ++i) put(i, sn, zn, r);
       }
@@ -256,10 +259,11 @@ __global__ void __launch_bounds__(32 * kEdgeWarps, 2) rotary_k_kernel(const Appe
                                     ((size_t)(c / kPer) * kBlockTokens + t) * 16) =
               *reinterpret_cast<const uint4*>(packed + (chunk * 129 + t) * 16);
       }
-      for (int e = tid; e < kBlockTokens * kColumn / G; e += kThreads) {
-        const int first = tokenwise ? e % gps * G : e % kColumn;  // the entry's (first) channel in the column
+      const int lg_gps = 7 - lgG;  // of kColumn channels
+      for (int e = tid; e < kBlockTokens * kColumn >> lgG; e += kThreads) {
+        const int first = tokenwise ? (e & (gps - 1)) << lgG : e % kColumn;  // the entry's (first) channel in the column
         const int h = head_of(q, first), c = channel_of(q, first);
-        const size_t at = ((size_t)page * H + h) * nsz + (tokenwise ? e / gps * (D / G) + c / G : e / kColumn * D + c);
+        const size_t at = ((size_t)page * H + h) * nsz + (tokenwise ? (e >> lg_gps) * (D >> lgG) + (c >> lgG) : e / kColumn * D + c);
         if (h < H) {
           p.scale[0][at] = s_out[e];
           p.zero[0][at] = z_out[e];
@@ -313,8 +317,7 @@ cudaError_t launch_w(const AppendParams& p, const TurnRowsParams& rows, cudaStre
     if (whole) e = chain.launch(dim3((unsigned)(p.total / kBlockTokens), heads, slabs), 32 * kBlockWarps, 0, rotary_v_kernel<T, BITS, W>, p);
     if (e != cudaSuccess) return e;
   }
-  const long long two = p.batch < p.total / 2 ? p.batch : p.total / 2;  // (as for append_chunk's edges)
-  const long long blocks = p.batch + two + (whole ? 0 : (p.total - 2 * two) / kBlockTokens);
+  const long long blocks = edge_blocks(p.batch, p.total, whole);
   const dim3 grid((unsigned)blocks, heads, 2 * slabs);
   if constexpr (kHalf) {
     if (whole) return chain.launch(grid, 32 * kEdgeWarps, 0, rotary_edges_kernel<T, BITS, W, kEdges>, p);
