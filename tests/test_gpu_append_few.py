@@ -64,3 +64,13 @@ def test_refused_entries_among_them(rotary):
         s.total[b] = s.old[b]
         s.x = [[t[:n] for t, n in zip(x, s.total)] for x in s.x]
     s.check(s.window)
+
+
+@pytest.mark.parametrize("rotary", [False, True])
+@pytest.mark.parametrize("dtype,dim", [("bf16", 128), ("fp32", 64), ("fp16", 256)])
+@pytest.mark.parametrize("tokens", [1, 2, 9, 17])
+def test_chunks_that_start_at_every_place(rotary, dtype, dim, tokens):
+    """Begun blocks of every length up to some warps' tokens, and up to the block's end."""
+    s = Setup(4, (1, 1), dim, 64, 2, DTYPES[dtype], True, tokens, list(range(33)) + list(range(110, 129)), [tokens] * 52)
+    (rotary_call if rotary else Setup.call)(s)
+    s.check(s.window)
