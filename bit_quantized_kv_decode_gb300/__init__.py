@@ -557,6 +557,8 @@ def rotary_table(positions: int, dim: int, base: float = 10000.0, device="cuda")
     """Angles for append_rotary: fp32 [positions, dim], the cosines of the dim / 2
     angles p * base^(-2 i / dim) of position p, then their sines (in 64 bits,
     rounded once).  A model with other frequencies fills such a tensor itself."""
+    if dim < 2 or dim % 2:
+        raise ValueError("dim must be even: every angle is a pair's")
     inv = base ** (-torch.arange(0, dim, 2, dtype=torch.float64) / dim)
     a = torch.arange(positions, dtype=torch.float64)[:, None] * inv
     return torch.cat([a.cos(), a.sin()], 1).float().to(device)
@@ -665,8 +667,8 @@ def select_blocks(desc: CacheDesc, q: torch.Tensor, k_cache, seq_lens: torch.Ten
         raise ValueError("seq_lens must be int32 [batch]")
     H = desc.num_kv_heads
     _, ks, kz = _cache_ptrs(desc, "k_cache", k_cache, dev)
-    if budget < 1:
-        raise ValueError("budget must be at least 1")
+    if budget < 1 or max(budget, first, last) >= 1 << 31:
+        raise ValueError("budget must be at least 1, and with first and last a 32-bit number")
     if blocks is None and counts is None:
         blocks = torch.empty((B, H, budget), dtype=torch.int32, device=q.device)
         counts = torch.empty((B, H), dtype=torch.int32, device=q.device)

@@ -21,9 +21,9 @@
 // The work is one pass over the rows, and memory would bound it below about ten
 // instructions a value; it takes 16 with everything, so whole blocks are bound
 // by instructions and barriers (65,536 tokens x 8 heads of 128, bf16 to 4 bits,
-// K channel-wise, V token-wise: 90 us, 3.8 TB/s, 67% of the issue slots; as fp32
-// rows, all of them edges: 242 us, 2.5 TB/s), edges by the latency of one block
-// (128 sequences of a token, windows re-quantised: 51 us, 2.7 TB/s).  Slower
+// K channel-wise, V token-wise: 86 us, 4.0 TB/s, 66% of the issue slots; as fp32
+// rows, all of them edges: 212 us, 2.9 TB/s), edges by the latency of one block
+// (128 sequences of a token, windows re-quantised: 39 us, 3.6 TB/s).  Slower
 // when tried: 16 warps to a whole block (140 -> 164 us); K and V of a block in
 // one CTA, V's loads under K's stores, gained 2%.
 //

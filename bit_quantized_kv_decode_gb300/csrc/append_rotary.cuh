@@ -10,7 +10,11 @@
 // where attention over rows follows) are rounded to it once.
 //
 // A call is one chain of kernels -- whole blocks of K, rows, whole blocks of V,
-// edges -- that write disjoint places and overlap.
+// edges -- that write disjoint places and overlap.  It is one pass over the rows:
+// 32,768 tokens of 32 query and 8 KV heads of 128, bf16 to 4 bits, turned K given
+// back: 153 us, 5.1 TB/s, most of it the rows' kernel at memory's rate; a token of
+// each of 128 sequences: 41 us, 3.4 TB/s, set by the number of instructions that a
+// warp of a begun block goes through.
 #pragma once
 #include "append_core.cuh"
 
@@ -67,10 +71,11 @@ __global__ void __launch_bounds__(32 * kBlockWarps, kBlockCtas) rotary_v_kernel(
 // is another lane's, but for heads of 256 (CROSS), where it may be of the other
 // column and is loaded, as are the angles, which would not fit twice.
 //
-// One column takes its CTA 7,000 cycles of loads, barriers and arithmetic in turn,
-// so this kernel is bound by neither memory nor instructions; it is launched first,
-// with one CTA to an SM where there are rows to turn, whose kernel then runs beside
-// it, and two where there are none.
+// A column is loads, barriers and arithmetic in turn, so this kernel is bound by
+// neither memory nor instructions (32,768 tokens x 8 heads of 128: 15% and 30%).  It
+// is launched first, with one CTA to an SM where there are rows to turn: 62 us by
+// itself, 1.4 times what two take, but the rows' kernel then runs beside it (the
+// call: 168 -> 157 us).
 constexpr int kColumn = 128, kSms = 152;
 
 template <typename T, int BITS, bool CROSS>

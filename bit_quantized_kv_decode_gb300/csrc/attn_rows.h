@@ -49,7 +49,7 @@ cudaError_t launch_prompt_attn(const RowAttnParams& p, cudaStream_t stream);
 struct Turn {
   const float* angles;
   int dim, interleaved;
-  float one;  // 1, at run time (append_rotary.cu)
+  float one;  // 1, at run time (append_rotary.cuh)
 };
 struct AppendParams {
   Rows x[2];  // K, V rows

@@ -79,6 +79,10 @@ __device__ __forceinline__ void eight(const uint4* at, float (&x)[8]) {
   for (int i = 0; i < 8; ++i) x[i] = i & 1 ? __uint_as_float(w[i / 2] & 0xffff0000u) : bf16_value(w[i / 2] & 0xffffu);
 }
 
+// The cluster's barrier, in halves.
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire;" ::: "memory"); }
+
 struct Shared {
   uint4 q[8 * 256 / 8];  // the query heads
   float bound;  // the cluster's largest sum of magnitudes
@@ -262,6 +266,10 @@ __global__ void __launch_bounds__(NT, 1024 / NT) select_kernel(const SelectParam
       sh.high = 0u;
       sh.in = sh.found = 0;
     }
+    if (ranks > 1) {  // (now, while there is nothing that it would wait for: with the copies under way it takes longer)
+      __syncthreads();
+      cluster_arrive();
+    }
     // A warp takes kRows blocks at a time, 8 channels a lane; its lanes copy what
     // they will read to places of their own in shared memory, kAhead steps ahead:
     // more bytes under way than registers would hold.
@@ -331,7 +339,7 @@ __global__ void __launch_bounds__(NT, 1024 / NT) select_kernel(const SelectParam
       }
     }
     uint32_t zmax[4] = {0u, 0u, 0u, 0u}, smax[4] = {0u, 0u, 0u, 0u};  // largest magnitudes of the channels, fp16 pairs
-    if (ranks > 1) cluster.sync();  // every CTA of the list is there
+    if (ranks > 1) cluster_wait();  // every CTA of the list is there, and the first one's numbers
     uint32_t* out = cluster.map_shared_rank(keys, 0);
     uint32_t low = 0xffffffffu, high = 0u;
     for (int i0 = from; i0 < to; i0 += 64) {
@@ -426,8 +434,13 @@ __global__ void __launch_bounds__(NT, 1024 / NT) select_kernel(const SelectParam
       atomicMin(&first->low, low);
       atomicMax(&first->high, high);
     }
-    if (ranks > 1) cluster.sync();
-    else __syncthreads();
+    if (ranks > 1) {
+      cluster_arrive();
+      if (rank != 0) return;  // (nothing of this CTA's is read by others)
+      cluster_wait();
+    } else {
+      __syncthreads();
+    }
   }
   if (rank != 0) return;
 

@@ -3,11 +3,14 @@ written to the cache, attention over the turned rows, then decode steps that tur
 and append a token, select blocks and attend to those; each call against the
 definition in 64 bits, and the same steps from one captured graph."""
 import math
+import os
+import re
 
 import pytest
 import torch
 
 import kvq_synth as synth
+from tests.conftest import ROOT
 from tests.rows_testlib import HALF_STEP, assert_rows_close, attend64, starts
 from tests.sparse_testlib import Cache, assert_sparse_close, attend_lists64, scores64, select64
 
@@ -120,3 +123,26 @@ def test_prompt_then_decode_over_selected_blocks(bits, schemes, dim, group, rota
     rms = want.square().mean().sqrt()
     assert ((out.float() - want).abs() <= 3e-2 * rms + 2.0 ** -8 * (want.abs() + 3e-2 * rms)).all()
     assert ((lse - want_lse).abs() <= 1e-2).all()
+
+
+def test_readme_example():
+    import bit_quantized_kv_decode_gb300 as kvq
+    with open(os.path.join(ROOT, "README.md")) as f:
+        blocks = re.findall(r"```python\n(.*?)```", f.read(), re.S)
+    example = next(b for b in blocks if "select_blocks" in b)
+    B, hkv, per = 3, 2, 4
+    c = Served(4, (1, 0), hkv, 128, 128, B, 8, 5)
+    q, k, v = c.rows(B * 600, per)
+    table = kvq.rotary_table(8 * 128, 128)
+    kvq.append_rotary(c.desc, table, k, v, starts([600] * B).cuda(), c.lens, c.k, c.v, *c.window, page_table=c.table)
+    c.lens += 600
+    q, k, v = c.rows(B, per)
+    names = dict(kvq=kvq, desc=c.desc, positions=8 * 128, q=q, k=k, v=v, lens=c.lens, kc=c.k, vc=c.v, k_window=c.window[0],
+                 v_window=c.window[1], table=c.table, budget=3, one_each=torch.arange(B + 1, dtype=torch.int32, device="cuda"))
+    exec(example, names)
+    c.lengths = [601] * B
+    assert c.lens.tolist() == c.lengths
+    assert_turned(names["turned"], q, table[torch.full((B,), 600)], False)
+    lists = [[select64(row, 3, 1, 1) for row in score] for score in scores64(c, names["turned"])]
+    assert names["blocks"].tolist() == lists and (names["counts"] == 3).all()
+    assert_sparse_close(names["out"], None, *attend_lists64(c, names["turned"], lists))

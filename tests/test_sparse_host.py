@@ -156,6 +156,9 @@ def test_rotary_table():
     a = p[:, None] * 500000.0 ** (-torch.arange(16, dtype=torch.float64) / 16)
     assert t.shape == (70000, 32) and t.dtype == torch.float32
     assert torch.equal(t[[0, 1, 69999]], torch.cat([a.cos(), a.sin()], 1).float())
+    for dim in (0, 15, -2):
+        with pytest.raises(ValueError, match="even"):
+            kvq.rotary_table(8, dim, device="cpu")
 
 
 def test_wrappers_refuse_host_tensors():
@@ -221,7 +224,8 @@ def test_wrappers_refuse_bad_tensors():
            lambda: g.append(k_window=None), lambda: g.append(k_new=g.k.float()), lambda: g.append(k_new=g.k.clone().requires_grad_()),
            lambda: g.append(max_blocks=None), lambda: g.append(k_cache=short), lambda: g.append(seq_lens=None),
            lambda: g.select(q=half), lambda: g.select(q=g.q[0]), lambda: g.select(q=wide[::2]), lambda: g.select(q=g.q[..., :64]),
-           lambda: g.select(q=g.q.clone().requires_grad_()), lambda: g.select(budget=0), lambda: g.select(seq_lens=g.lens[:1]),
+           lambda: g.select(q=g.q.clone().requires_grad_()), lambda: g.select(budget=0), lambda: g.select(first=1 << 32), lambda: g.select(last=1 << 32),
+           lambda: g.select(seq_lens=g.lens[:1]),
            lambda: g.select(seq_lens=None), lambda: g.select(max_blocks=None), lambda: g.select(k_cache=short),
            lambda: g.select(blocks=g.blocks.long()), lambda: g.select(counts=g.counts[:1]),
            lambda: g.select(page_table=g.blocks[:, 0].long()),
