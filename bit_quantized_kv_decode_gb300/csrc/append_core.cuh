@@ -253,7 +253,9 @@ __device__ __forceinline__ float4 turned(const AppendParams& p, float4 v, long l
 // CTAs of append_edge in x: one per sequence; one more where a chunk of two tokens
 // or more can cross into the next block; and where the edges' kernel takes whole
 // blocks too, one for each 128 tokens past that.  None but the sequences' where
-// there are no more tokens than sequences.
+// there are no more tokens than sequences (a token each of 1,024, of 512 or of 100
+// of them: 244, 163, 87 us; with more CTAs, of which none has a block, 512: 280,
+// 100: 85).
 inline long long edge_blocks(long long batch, long long total, bool whole_apart) {
   if (total <= batch) return batch;
   const long long two = batch < total / 2 ? batch : total / 2;
@@ -282,10 +284,10 @@ __device__ __forceinline__ void append_edge(const AppendParams& p) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const bool lead = h == 0 && blockIdx.z == 0;
   // The first `batch` CTAs take the first block of a sequence each (every thread
-  // looks for itself), the others what more there is.  With no more tokens than
-  // sequences there are no others: n tokens touch n blocks at most, so the CTAs
-  // of sequences without any are as many as what more there is, and take it when
-  // they have copied their window.
+  // looks for itself), the others what more there is.  Without others
+  // (edge_blocks) there are no more tokens than sequences: n tokens touch n blocks
+  // at most, so the CTAs of sequences without any are as many as what more there
+  // is, and take it when they have copied their window.
   auto copy_window = [&](int seq, int held) {  // (of a sequence without new tokens: to another window)
     float* to = p.window_out[which];
     if (to == nullptr || to == p.window[which]) return;
@@ -317,17 +319,20 @@ __device__ __forceinline__ void append_edge(const AppendParams& p) {
       break;
     }
     if (!chunk.bad) copy_window(b, chunk.len);
-    if (!alone) return;
-    if (tid == 0) found[0] = 0;
+    if (!alone || p.total < 2) return;
+    if (tid == 0) found[0] = found[1] = 0;
     __syncthreads();
-    int before = 0;
-    for (int i = tid; i < b; i += kThreads) {
+    int before = 0, more = 0;  // such CTAs before this one; blocks that there are for them
+    for (int i = tid; i < p.batch; i += kThreads) {
       const Chunk c = load_chunk(p, i);
-      before += c.bad || c.rows.n == 0;
+      if (c.bad || c.rows.n == 0) before += i < b;
+      else more += max(0, part_blocks<PART>(c) - 1);
     }
     if (before != 0) atomicAdd(&found[0], before);
+    if (more != 0) atomicAdd(&found[1], more);
     __syncthreads();
     rank = found[0];
+    if (rank >= found[1]) return;
     __syncthreads();
     first = false;
   }
