@@ -125,8 +125,12 @@ __global__ void __launch_bounds__(32 * kEdgeWarps, 2) rotary_k_kernel(const Appe
       __syncthreads();
     }
     const float* my_angles = (CROSS ? angles : near_angles) + tok * p.turn.dim;
-    auto angle4 = [](const float* at) { return CROSS ? __ldg(reinterpret_cast<const float4*>(at)) : *reinterpret_cast<const float4*>(at); };
-    auto angle2 = [](const float* at) { return CROSS ? __ldg(reinterpret_cast<const float2*>(at)) : *reinterpret_cast<const float2*>(at); };
+    auto angle4 = [](const float* at) {
+      return CROSS ? __ldg(reinterpret_cast<const float4*>(at)) : *reinterpret_cast<const float4*>(at);
+    };
+    auto angle2 = [](const float* at) {
+      return CROSS ? __ldg(reinterpret_cast<const float2*>(at)) : *reinterpret_cast<const float2*>(at);
+    };
     for (int q = q0; q < q1; ++q) {
       load(q);
       if (q + 1 < q1 && tid < 2 * kBlockTokens) {  // (the next column's rows are on their way to L2 meanwhile: two lines a row)
@@ -301,7 +305,8 @@ cudaError_t launch_w(const AppendParams& p, const TurnRowsParams& rows, cudaStre
   cudaError_t e = cudaSuccess;
   if constexpr (kHalf) {
     if (whole) {
-      const long long columns = (p.num_kv_heads * p.head_dim + kColumn - 1) / kColumn, tiles = p.total / kBlockTokens * columns;
+      const long long columns = (p.num_kv_heads * p.head_dim + kColumn - 1) / kColumn;
+      const long long tiles = p.total / kBlockTokens * columns;
       const int each = tiles < 2 * 912 ? 1 : 2;  // (two once every SM has six items)
       const long long items = p.total / kBlockTokens * ((columns + each - 1) / each), most = turn ? kSms : 2 * kSms;
       const dim3 grid((unsigned)(items < most ? items : most));
@@ -319,7 +324,8 @@ cudaError_t launch_w(const AppendParams& p, const TurnRowsParams& rows, cudaStre
   if (turn) e = launch_turn_rows(rows, chain);
   if (e != cudaSuccess) return e;
   if constexpr (kHalf) {
-    if (whole) e = chain.launch(dim3((unsigned)(p.total / kBlockTokens), heads, slabs), 32 * kBlockWarps, 0, rotary_v_kernel<T, BITS, W>, p);
+    const dim3 grid((unsigned)(p.total / kBlockTokens), heads, slabs);
+    if (whole) e = chain.launch(grid, 32 * kBlockWarps, 0, rotary_v_kernel<T, BITS, W>, p);
     if (e != cudaSuccess) return e;
   }
   const long long blocks = edge_blocks(p.batch, p.total, whole);

@@ -95,7 +95,8 @@ KVQ_API kvq_status kvq_sparse_decode_attn(const kvq_sparse_desc* d, const uint16
   if (!aligned4(page_table) || !aligned4(lse)) return KVQ_ERR_INVALID_ARG;
   if (page_table == nullptr && (long long)d->batch * d->max_blocks > d->cache.num_pages) return KVQ_ERR_INVALID_ARG;
   const SparsePlan plan = sparse_plan(d);
-  if (plan.total > 0 && (workspace == nullptr || (reinterpret_cast<uintptr_t>(workspace) & 255u) != 0 || workspace_bytes < plan.total))
+  if (plan.total > 0 && (workspace == nullptr || (reinterpret_cast<uintptr_t>(workspace) & 255u) != 0 ||
+                         workspace_bytes < plan.total))
     return KVQ_ERR_WORKSPACE;
   s = check_device(nullptr);
   if (s != KVQ_OK) return s;

@@ -116,7 +116,8 @@ cudaError_t launch_merge_of(const ListParams& p, cudaStream_t stream) {
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return many ? cudaLaunchKernelEx(&cfg, listed_merge_kernel<D, kRows>, p) : cudaLaunchKernelEx(&cfg, listed_merge_kernel<D, 1>, p);
+  return many ? cudaLaunchKernelEx(&cfg, listed_merge_kernel<D, kRows>, p)
+              : cudaLaunchKernelEx(&cfg, listed_merge_kernel<D, 1>, p);
 }
 
 }  // namespace
@@ -160,7 +161,8 @@ cudaError_t launch_sparse_decode(const kvq_cache_desc& cache, const SparsePlan& 
                                               : (wide ? launch_listed_d256_h8 : launch_listed_d256);
   cudaError_t e = launch(cache.bits, kcw, vcw, group_of(&cache), p, plan.units * plan.splits, plan.launch, stream);
   if (e != cudaSuccess || plan.splits == 1) return e;
-  return cache.head_dim == 64 ? launch_merge_of<64>(p, stream) : cache.head_dim == 128 ? launch_merge_of<128>(p, stream) : launch_merge_of<256>(p, stream);
+  if (cache.head_dim == 64) return launch_merge_of<64>(p, stream);
+  return cache.head_dim == 128 ? launch_merge_of<128>(p, stream) : launch_merge_of<256>(p, stream);
 }
 
 }  // namespace kvq
