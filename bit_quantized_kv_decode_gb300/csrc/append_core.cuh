@@ -254,7 +254,7 @@ __device__ __forceinline__ float4 turned(const AppendParams& p, float4 v, long l
 // or more can cross into the next block; and where the edges' kernel takes whole
 // blocks too, one for each 128 tokens past that.  None but the sequences' where
 // there are no more tokens than sequences (a token each of 1,024, of 512 or of 100
-// of them: 244, 163, 87 us; with more CTAs, of which none has a block, 512: 280,
+// of them: 244, 163, 60 us; with more CTAs, of which none has a block, 512: 280,
 // 100: 85).
 inline long long edge_blocks(long long batch, long long total, bool whole_apart) {
   if (total <= batch) return batch;
@@ -319,7 +319,11 @@ __device__ __forceinline__ void append_edge(const AppendParams& p) {
       break;
     }
     if (!chunk.bad) copy_window(b, chunk.len);
-    if (!alone || p.total < 2) return;
+    // Sequences with tokens are p.total at most, so that b - p.total such CTAs
+    // come before this one, and there are p.total - 1 blocks at most for all of
+    // them.  (Else every one of them would read the lengths of the whole batch: 8
+    // tokens of 65,532 sequences 8.1 ms, as it is 0.28.)
+    if (!alone || p.total < 2 || b - p.total >= p.total - 1) return;
     if (tid == 0) found[0] = found[1] = 0;
     __syncthreads();
     int before = 0, more = 0;  // such CTAs before this one; blocks that there are for them
