@@ -58,10 +58,15 @@ __global__ void __launch_bounds__(kMergeThreads) listed_merge_kernel(const ListP
   const float* lses = p.part_lse + (size_t)u * p.splits * p.gq + k;
   const float* parts = p.part_o + ((size_t)u * p.splits * p.gq + k) * D + lane * V;
   float m = -INFINITY;
-  for (int s = lane; s < nr; s += 32) m = fmaxf(m, lses[(size_t)s * p.gq]);
+  bool some = false;
+  for (int s = lane; s < nr; s += 32) {
+    const float x = lses[(size_t)s * p.gq];
+    m = fmaxf(m, x);
+    some |= x != -INFINITY;  // (the maximum passes over what is not a number: m alone would not tell)
+  }
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-  const bool none = m == -INFINITY;  // no entry, or bad ones alone
+  const bool none = !__any_sync(0xffffffffu, some);  // no entry, or bad ones alone
   float t = 0.f;
   for (int s = lane; s < nr; s += 32) t += none ? 0.f : expf(lses[(size_t)s * p.gq] - m);
 #pragma unroll
