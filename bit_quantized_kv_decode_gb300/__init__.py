@@ -627,8 +627,15 @@ def append_rotary(desc: CacheDesc, table: torch.Tensor, k_new: torch.Tensor, v_n
     if k_out is not None:
         pk = _ptr(k_out, "k_out", dtype, T * H * D, dev)
         written.append(("k_out", k_out))
+    size = k_new.element_size()
+    if T:  # (the windows, against what append_chunk does not read)
+        others = [_span(table)]
+        if qr is not None:
+            others.append(_rows_span(qr, T, Hq, D, size))
+        for o in rest[8:10]:
+            if o:
+                _disjoint("a window", (o, o + rest[0] * H * BLOCK_TOKENS * D * 4), others)
     if T and written:
-        size = k_new.element_size()
         others = [_rows_span(r, T, h, D, size) for r, h in ((kr, H), (vr, H), (qr, Hq)) if r is not None]
         others += [_span(t) for t in (k_window, v_window, k_window_out, v_window_out, table, cu_seqlens, seq_lens, page_table,
                                       dev_status, *k_cache, *v_cache) if t is not None]

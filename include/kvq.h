@@ -465,9 +465,9 @@ KVQ_API kvq_status kvq_append_chunk(const kvq_cache_desc* cache, int32_t dtype, 
  *              16-byte aligned, apart from every other array
  *   k_out      the same with num_kv_heads, or NULL
  * Rows outside every sequence, and those of a sequence that is skipped, are
- * left as they were.  Other arguments and device errors as kvq_append_chunk; a
- * sequence that reaches past rotary->positions is skipped with
- * KVQ_DEV_BAD_SEQ_LEN.
+ * left as they were.  The windows share no memory with q and the angles either.
+ * Other arguments and device errors as kvq_append_chunk; a sequence that reaches
+ * past rotary->positions is skipped with KVQ_DEV_BAD_SEQ_LEN.
  */
 KVQ_API kvq_status kvq_append_rotary(const kvq_cache_desc* cache, int32_t dtype, const kvq_rotary* rotary,
                                      const kvq_rows* q, int32_t num_q_heads, const kvq_rows* k, const kvq_rows* v,
