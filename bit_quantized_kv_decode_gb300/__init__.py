@@ -755,7 +755,8 @@ def sparse_decode_attn(desc: CacheDesc, q: torch.Tensor, k_cache, v_cache, seq_l
         spans = ((po, B * Hq * D * 2), (pl or 0, B * Hq * 4 if pl else 0), (pq, B * Hq * D * 2), (pb, B * H * n * 4),
                  (pc, B * H * 4), (pn, B * 4), (pt or 0, B * mb * 4 if pt else 0))
         if given:
-            for at, length in spans:
+            arrays = [(t.data_ptr(), t.numel() * t.element_size()) for t in (*k_cache, *v_cache, dev_status) if t is not None]
+            for at, length in (*spans, *arrays):
                 # (of a longer workspace, the first bytes are used)
                 if at < pw + size and pw < at + length and at < pw + _sparse_bytes(d):
                     raise ValueError("workspace overlaps another array of the call")

@@ -42,3 +42,25 @@ def test_windows_over_queries_and_angles():
     call(own, q=q, k_window=window(n), v_window=window(2 * n + T * 8 * D))  # right before, right behind
     call(table, k_window=window(0), v_window=window(4 * n), k_window_out=window(n), v_window_out=window(5 * n))  # read by both
     assert (memory[:40 * D] == 0).all()
+
+
+def test_workspaces_over_the_cache():
+    lens = torch.tensor([200, 130], dtype=torch.int32, device="cuda")
+    desc = kvq.cache_desc(4, 1, 0, 2, 4)
+    size = kvq.sparse_workspace_size(desc, 2, 8, 32)
+    assert size > 0
+    memory = torch.zeros(size + (1 << 18), dtype=torch.uint8, device="cuda")
+    caches = [kvq.alloc_cache(desc) for _ in "kv"]
+    codes = caches[0][0]
+    q = torch.randn(2, 8, 128, device="cuda").to(torch.bfloat16)
+    blocks, counts = (torch.ones(shape, dtype=torch.int32, device="cuda") for shape in ((2, 2, 32), (2, 2)))
+    for i in range(6):
+        for at in (0, size - 256):
+            held = [list(c) for c in caches]
+            t = held[i // 3][i % 3]
+            held[i // 3][i % 3] = memory[at:at + t.numel() * t.element_size()].view(t.dtype).view(t.shape)
+            with pytest.raises(ValueError, match="workspace overlaps"):
+                kvq.sparse_decode_attn(desc, q, *held, lens, blocks, counts, max_blocks=2, workspace=memory)
+                pytest.fail(f"array {i} at {at} was not refused")
+    held = memory[size:size + codes.numel()].view(codes.shape)  # behind the bytes that are used
+    kvq.sparse_decode_attn(desc, q, (held, *caches[0][1:]), caches[1], lens, blocks, counts, max_blocks=2, workspace=memory)
