@@ -696,8 +696,19 @@ def select_blocks(desc: CacheDesc, q: torch.Tensor, k_cache, seq_lens: torch.Ten
     return blocks, counts
 
 
-def sparse_workspace_size(desc: CacheDesc, batch: int, num_q_heads: int, list_len: int) -> int:
-    """Workspace bytes of a sparse_decode_attn call with these sizes (may be 0)."""
+# Ranges of all lists of a call, at most (kvq_sparse_workspace_size).
+SPARSE_RANGES = 9728
+
+
+def sparse_workspace_size(desc: CacheDesc, batch: Optional[int], num_q_heads: int, list_len: Optional[int]) -> int:
+    """Workspace bytes of a sparse_decode_attn call with these sizes (may be 0).
+    Fewer sequences or shorter lists may take more, since their lists are cut in
+    more ranges: a buffer for several sizes, or of a captured step, has the bytes
+    given for None as batch or list_len, which suffice for every call."""
+    if batch is None or list_len is None:
+        _sparse_bytes(_lib.SparseDesc(desc, 1, num_q_heads, 1, 1, 0.0, 0))  # (checks the rest)
+        rows = SPARSE_RANGES * (num_q_heads // desc.num_kv_heads)
+        return rows * 4 + rows * desc.head_dim * 4
     return _sparse_bytes(_lib.SparseDesc(desc, batch, num_q_heads, 1, list_len, 0.0, 0))
 
 

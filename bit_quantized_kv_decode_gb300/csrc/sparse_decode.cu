@@ -23,10 +23,10 @@ int sparse_splits(long long units, int list_len) {
   int splits = 1;
   int blocks = list_len;  // of a range
   for (int s = 1;; s = (list_len - 1) / (blocks - 1) + 1) {  // (the next s with fewer: those between add only CTAs)
-    if (units * (s - 1) > 32 * kSms) break;
+    if (units * (s - 1) > 32 * kSms) break;  // (so units * s <= 64 * kSms = 9,728, which callers may rely on)
     blocks = (list_len + s - 1) / s;
     const long long ctas = units * s;
-    const long long alone = 12LL * blocks, shared = ctas * (5 * blocks + 8) / kSms;
+    const long long alone = 12LL * blocks, shared = ctas * (5LL * blocks + 8) / kSms;
     const long long cost = (alone > shared ? alone : shared) + alone / 2 + (s > 1 ? 30 : 0);
     if (best < 0 || cost < best) {
       best = cost;

@@ -550,7 +550,10 @@ KVQ_API kvq_status kvq_select_blocks(const kvq_select_desc* desc, const uint16_t
                                      int32_t* blocks, int32_t* counts, uint32_t* dev_status, void* stream);
 
 /* Workspace bytes kvq_sparse_decode_attn needs for `desc` (host only, no device
- * needed; may be 0). */
+ * needed; may be 0).  Smaller calls may need more: their lists are cut in more
+ * ranges.  Of a cache geometry and a number of query heads per KV head, no call
+ * has more than 9,728 ranges, that is 9,728 (num_q_heads / num_kv_heads)
+ * (head_dim + 1) 4 bytes. */
 KVQ_API kvq_status kvq_sparse_workspace_size(const kvq_sparse_desc* desc, size_t* bytes);
 
 /*
