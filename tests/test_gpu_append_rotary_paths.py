@@ -5,7 +5,7 @@ import pytest
 import torch
 
 from tests.rows_testlib import DTYPES
-from tests.test_gpu_append_rotary import Setup
+from tests.test_gpu_append_rotary import Setup, turn
 
 pytestmark = pytest.mark.gpu
 
@@ -117,3 +117,26 @@ def test_rows_without_a_sequence(dtype):
     s.check_rows(k_out[at], k, "k")
     for x in (q_out, k_out):
         assert (x[:before] == 7).all() and (x[before + T:] == 7).all()
+
+
+@pytest.mark.parametrize("T", [100, 5000])
+def test_rows_that_sequences_share(T):
+    """Behind a decreasing entry: reported, and a row is turned for one of its sequences, or left."""
+    import bit_quantized_kv_decode_gb300 as kvq
+    wide, B, dim = (T + 127) // 128 + 2, 5, 128
+    desc = kvq.cache_desc(4, 0, 0, 2, B * wide)
+    g = torch.Generator(device="cuda").manual_seed(42)
+    q, k, v = (torch.randn(T + 9, h, dim, generator=g, device="cuda") for h in (8, 2, 2))
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    old = [0, 3, 50, 3, 90]
+    table = kvq.rotary_table(T + 90, dim)
+    out, k_out = torch.full_like(q, 7.0), torch.full_like(k, 7.0)
+    kvq.append_rotary(desc, table, k, v, torch.tensor([0, T] * 3, dtype=torch.int32, device="cuda"),
+                      torch.tensor(old, dtype=torch.int32, device="cuda"), *(kvq.alloc_cache(desc) for _ in "kv"),
+                      max_blocks=wide, q=q, q_out=out, k_out=k_out, dev_status=status)
+    assert int(status.item()) == kvq.DEV_BAD_SEQ_LEN
+    for x, got in ((q, out), (k, k_out)):
+        right = (got == 7.0).flatten(1).all(1)
+        for b in (0, 2, 4):
+            right[:T] |= (got[:T] == turn(x[:T], table[old[b]:old[b] + T], False)).flatten(1).all(1)
+        assert right.all() and (got[T:] == 7.0).all()
