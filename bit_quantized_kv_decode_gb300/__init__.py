@@ -597,7 +597,10 @@ def append_rotary(desc: CacheDesc, table: torch.Tensor, k_new: torch.Tensor, v_n
     k_window holds turned rows.  With q [T, Hq, head_dim], rows of the same
     tokens and type, the turned queries are returned (q_out, made when not
     given), else None; with k_out [T, Hkv, head_dim] the turned keys are written
-    there too, for prompt_attn.  Both are rounded once to the rows' type."""
+    there too, for prompt_attn.  Both are rounded once to the rows' type.  Rows
+    outside every sequence, and those of a sequence that is refused, are not
+    written: give a q_out where a program reads them (a q_out made here holds
+    anything there)."""
     dev, kr, vr, rest, status = _append_args(desc, k_new, v_new, cu_seqlens, seq_lens, k_cache, v_cache, k_window, v_window,
                                              page_table, max_blocks, k_window_out, v_window_out, dev_status, "append_rotary")
     if not isinstance(table, torch.Tensor) or table.dim() != 2:

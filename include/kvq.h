@@ -436,9 +436,10 @@ KVQ_API kvq_status kvq_prompt_attn(const kvq_prompt_desc* desc, const kvq_rows* 
  *              window and window_out of a channel-wise scheme must be given; a
  *              window_out that is not its window shares no memory with it, and
  *              none shares any with the other cache's or the rows
- * Device errors as kvq_append; a sequence with a bad length or a bad page is
- * skipped (that block of it), and where sequences behind a decreasing
- * cu_seqlens entry share rows, blocks of any sequence may be left as they were.
+ * Device errors as kvq_append; a sequence with a bad length is skipped, and so
+ * is a block with a bad page (the windows are written all the same).  Where
+ * sequences behind a decreasing cu_seqlens entry share rows, blocks of any
+ * sequence may be left as they were.
  * Values that are not finite, or whose group overflows fp16, leave their group
  * zero and set KVQ_DEV_NONFINITE.
  */
@@ -465,7 +466,8 @@ KVQ_API kvq_status kvq_append_chunk(const kvq_cache_desc* cache, int32_t dtype, 
  *              16-byte aligned, apart from every other array
  *   k_out      the same with num_kv_heads, or NULL
  * Rows outside every sequence, and those of a sequence that is skipped, are
- * left as they were.  The windows share no memory with q and the angles either.
+ * left as they were (a row that two sequences share is turned for one of them,
+ * or left).  The windows share no memory with q and the angles either.
  * Other arguments and device errors as kvq_append_chunk; a sequence that reaches
  * past rotary->positions is skipped with KVQ_DEV_BAD_SEQ_LEN.
  */
