@@ -321,8 +321,8 @@ __device__ __forceinline__ void append_edge(const AppendParams& p) {
     if (!chunk.bad) copy_window(b, chunk.len);
     // Sequences with tokens are p.total at most, so that b - p.total such CTAs
     // come before this one, and there are p.total - 1 blocks at most for all of
-    // them.  (Else every one of them would read the lengths of the whole batch: 8
-    // tokens of 65,532 sequences 8.1 ms, as it is 0.28.)
+    // them.  (Were every one of them to read the lengths of the whole batch, 8 tokens
+    // of 65,532 sequences would take 8.1 ms instead of 0.28.)
     if (!alone || p.total < 2 || b - p.total >= p.total - 1) return;
     if (tid == 0) found[0] = found[1] = 0;
     __syncthreads();

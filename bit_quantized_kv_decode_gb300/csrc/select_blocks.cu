@@ -631,9 +631,12 @@ cudaError_t launch_nt(const SelectParams& p, int ranks, cudaStream_t stream) {
   return cudaLaunchKernelEx(&cfg, kernel, p);
 }
 
-// Warps of a list: one for 64 of its blocks, and one for 16 while all lists'
-// warps are resident at once (32 to an SM), so that some score while others
-// select; CTAs of 4 warps, of 16 where a cluster of 8 such has not enough.
+// Warps of a list: one for 64 of its blocks, and more, up to one for 16, as long
+// as all lists' warps are resident at once (32 to an SM): 512 lists of up to 1,024
+// blocks, 64 / 32 / 16 blocks a warp: 30 / 34 / 50 us; 1,024 of 256: 35 / 39 / 44;
+// 256 of 256: 17.2 / 16.6 / 16.9.  (1,024 lists of 256 are one wave then, in which
+// lists copy together and then select together, and memory idles at both ends.)
+// CTAs of 4 warps, of 16 where a cluster of 8 such has not enough.
 template <int D, int NG>
 cudaError_t launch(const SelectParams& p, cudaStream_t stream) {
   const long long units = (long long)p.batch * p.num_kv_heads, resident = 152 * 32 / units;
